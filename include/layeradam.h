@@ -301,6 +301,161 @@ LA_API la_status la_direction_probe(const la_layer_desc *layer, int32_t part,
                                     uint32_t fill, int32_t workgroups_per_cu,
                                     void *hip_stream);
 
+/* ---------------------------------------------------------------------------
+ * The orthogonalised update (Muon) for matrices, beside AdamW.
+ *
+ * la_orthogonalize replaces a matrix U by a nearly orthogonal one with the
+ * same singular vectors, by Newton-Schulz products:
+ *     X = U / max(||U||_F, eps)           (U^T where rows > cols)
+ *     for each step (a, b, c):
+ *         A = X X^T;  X <- a X + (b A + c A A) X
+ *     O = X                               (X^T where rows > cols)
+ * so that every singular value s of X becomes a s + b s^3 + c s^5 per step.
+ * layer_muon_step is the optimizer step around it, per matrix:
+ *     g = (G_0 + ... + G_{R-1}) * grad_unscale   (FP32, left to right)
+ *     B <- momentum * B + g
+ *     U = g + momentum * B  (nesterov)  or  B
+ *     p <- p * (1 - lr*weight_decay) - lr * s * orthogonal(U)
+ *     w = BF16(p) or FP16(p), round to nearest even, or no copy
+ * with s by la_lr_scale. Norm scales, biases and embeddings of a layer take
+ * layer_adam_step.
+ *
+ * Numerics. ||U||_F is summed in FP64. X is held as a pair of FP16 numbers
+ * (22 significant bits) under power-of-two scales that the host derives from
+ * the coefficients, so that nothing overflows; the products multiply the
+ * upper 11 bits with FP32 sums. O is within about 0.2 % (2-norm of the
+ * difference over 2-norm of O, default coefficients) of the polynomial in
+ * FP64, also for matrices of low rank or of a wide range of singular
+ * values. Results do not depend on the launch: the same inputs give the
+ * same bits. A zero matrix gives zeros; a matrix holding an Inf or NaN gives
+ * NaN everywhere.
+ *
+ * Memory. The caller passes a workspace (la_orthogonalize_workspace_bytes,
+ * layer_muon_workspace_bytes) in device memory of the current device,
+ * 256-byte aligned, whose contents need not be set and mean nothing after
+ * the call. Calls that may run at once -- on two streams, or in two captured
+ * graphs that are replayed at once -- need a workspace each. All calls are
+ * asynchronous on the given stream, allocate nothing, synchronise nothing
+ * and can be captured in a HIP graph.
+ * ------------------------------------------------------------------------- */
+
+#define LA_MAX_SIDE 1048576      /* rows and cols of one matrix, and matrices
+                                    of one stack                            */
+#define LA_MAX_POLYNOMIAL_STEPS 16
+#define LA_WORKSPACE_ALIGNMENT 256
+
+typedef enum { LA_TYPE_BF16 = 0, LA_TYPE_FP16 = 1, LA_TYPE_FP32 = 2 } la_element_type;
+
+/* The polynomial: num_steps (1..LA_MAX_POLYNOMIAL_STEPS) triples (a, b, c) in
+ * coefficients[3 * num_steps], and eps >= 0. Where a pointer to this struct
+ * is NULL, five steps of (3.4445, -4.7750, 2.0315) with eps = 1e-7 are
+ * taken. Refused: coefficients that are not finite, or with which a
+ * singular value in [0, 1] could pass 2^20, the largest one could fall
+ * below 2^-20, or b A + c A A could pass 2^40. */
+typedef struct {
+  const double *coefficients;
+  int32_t num_steps;
+  double eps;
+} la_polynomial;
+
+/* A stack of `count` matrices of rows x cols elements: element (i, j) of
+ * matrix z at in[z * in_matrix_stride + i * in_row_stride + j], and the same
+ * for out. Strides are in elements and may not make elements coincide: either
+ * row_stride >= cols and matrix_stride >= (rows - 1) * row_stride + cols, or
+ * (matrices side by side, as the heads of a projection) matrix_stride >= cols
+ * and row_stride >= (count - 1) * matrix_stride + cols. A stride that no
+ * second row or matrix uses is ignored. `in` and `out` are aligned to their
+ * element. `out` may be `in` itself with the same element type and strides;
+ * otherwise the range from out's first to last element may not overlap that
+ * of any in or out of the call. A stack with rows, cols or count 0 is
+ * skipped. */
+typedef struct {
+  const void *in;
+  void *out;
+  int64_t rows, cols, count;
+  int64_t in_row_stride, in_matrix_stride;
+  int64_t out_row_stride, out_matrix_stride;
+} la_matrix_desc;
+
+/* Up to LA_MAX_TENSORS stacks in one call; in_type is any la_element_type,
+ * out_type LA_TYPE_BF16 or LA_TYPE_FP16. */
+typedef struct {
+  const la_matrix_desc *matrices;
+  int32_t num_matrices;
+  int32_t in_type;
+  int32_t out_type;
+} la_matrices_desc;
+
+/* Workspace of one la_orthogonalize of these matrices; -1 if the descriptor
+ * or the polynomial is invalid (la_last_error says why). Pointers are not
+ * looked at. Host only. */
+LA_API int64_t la_orthogonalize_workspace_bytes(const la_matrices_desc *matrices,
+                                                const la_polynomial *polynomial);
+
+/* Enqueue the orthogonalisation of every matrix on `hip_stream`. Every
+ * argument is checked on the host before anything is enqueued; on failure
+ * nothing is enqueued and la_last_error() describes the problem. */
+LA_API la_status la_orthogonalize(const la_matrices_desc *matrices,
+                                  const la_polynomial *polynomial, void *workspace,
+                                  int64_t workspace_bytes, void *hip_stream);
+
+/* One tensor of the Muon step: a stack of `count` contiguous rows x cols
+ * matrices (count 1 for a plain weight, the experts of a mixture layer
+ * otherwise), each orthogonalised by itself. Buffers as in la_tensor_desc,
+ * 16-byte aligned; master and momentum are FP32, read and written in place. */
+typedef struct {
+  float *master;
+  float *momentum;
+  uint16_t *weight_out;
+  const void *grads[LA_MAX_REPLICAS];
+  int64_t rows, cols, count;
+} la_muon_tensor_desc;
+
+typedef struct {
+  const la_muon_tensor_desc *tensors;
+  int32_t num_tensors;
+  int32_t num_replicas;
+  int32_t grad_dtype;
+  int32_t out_dtype;
+} la_muon_layer_desc;
+
+/* The factor s of the step. */
+typedef enum {
+  LA_LR_SCALE_NONE = 0,      /* 1                                            */
+  LA_LR_SCALE_ORIGINAL = 1,  /* sqrt(max(1, rows / cols))                    */
+  LA_LR_SCALE_MATCH_RMS_ADAMW = 2 /* 0.2 sqrt(max(rows, cols)): the update's
+                                root mean square is about that of AdamW, so
+                                that AdamW's lr and weight_decay serve       */
+} la_lr_scale;
+
+/* Domains: 0 <= momentum < 1; lr, weight_decay finite and >= 0; grad_unscale
+ * finite and > 0; nesterov 0 or 1; lr_scale a la_lr_scale. */
+typedef struct {
+  double lr;
+  double momentum;
+  double weight_decay;
+  double grad_unscale;
+  int32_t nesterov;
+  int32_t lr_scale;
+  const la_polynomial *polynomial; /* NULL: the default                      */
+} la_muon_params;
+
+/* Workspace of one layer_muon_step; -1 if the descriptor or a parameter is
+ * invalid. Pointers are not looked at. Host only. */
+LA_API int64_t layer_muon_workspace_bytes(const la_muon_layer_desc *layer,
+                                          const la_muon_params *hp);
+
+/* Enqueue one Muon step of the layer's matrices on `hip_stream`.
+ * overflow_flag: as for layer_adam_step (set to 1 where an aggregated
+ * gradient element is not finite; that matrix's momentum keeps the value and
+ * its master becomes NaN). skip_if_nonzero: NULL, or as for
+ * layer_adam_step_gated: nothing is touched, the workspace included, when it
+ * holds a non-zero value as the kernels run; la_check_gradients sets it. It
+ * may not change while the step runs. */
+LA_API la_status layer_muon_step(const la_muon_layer_desc *layer, const la_muon_params *hp,
+                                 int32_t *overflow_flag, const int32_t *skip_if_nonzero,
+                                 void *workspace, int64_t workspace_bytes, void *hip_stream);
+
 /* Bytes of mixed-precision Adam state the layer stands for: 16 per
  * parameter (2 BF16 weight + 2 gradient + 4 FP32 master + 8 FP32 m and v).
  * -1 if the descriptor is invalid. Host only. */

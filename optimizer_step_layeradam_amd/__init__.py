@@ -28,12 +28,21 @@ STATUS_NAMES = {0: "LA_OK", 1: "LA_ERR_INVALID_ARGUMENT", 2: "LA_ERR_MISALIGNED"
 GRAD_BF16, GRAD_FP16 = 0, 1
 OUT_BF16, OUT_FP16, OUT_NONE = 0, 1, 2
 PROBE_READS, PROBE_WRITES = 0, 1
+TYPE_BF16, TYPE_FP16, TYPE_FP32 = 0, 1, 2
+LR_SCALES = {"none": 0, "original": 1, "match_rms_adamw": 2}
+MAX_SIDE = 1048576
+MAX_POLYNOMIAL_STEPS = 16
+WORKSPACE_ALIGNMENT = 256
+# The default polynomial of the orthogonalised update: five equal steps.
+NEWTON_SCHULZ = ((3.4445, -4.7750, 2.0315),) * 5
 
 # Exported symbols, as declared in include/layeradam.h.
 EXPORTS = ("layer_adam_step", "layer_adam_step_range", "layer_adam_step_gated",
            "layer_adam_step_device_step", "layer_adam_step_ex", "la_check_gradients",
            "la_stream_probe",
            "la_direction_probe", "la_copy_reference",
+           "la_orthogonalize", "la_orthogonalize_workspace_bytes", "layer_muon_step",
+           "layer_muon_workspace_bytes",
            "la_state_bytes", "la_traffic_bytes", "la_last_error", "la_version")
 
 
@@ -71,6 +80,59 @@ class StepOptions(ctypes.Structure):
                 ("overflow_flag", ctypes.c_void_p),
                 ("skip_if_nonzero", ctypes.c_void_p),
                 ("step_on_device", ctypes.c_void_p)]
+
+
+class Polynomial(ctypes.Structure):
+    _fields_ = [("coefficients", ctypes.POINTER(ctypes.c_double)),
+                ("num_steps", ctypes.c_int32),
+                ("eps", ctypes.c_double)]
+
+
+class MatrixDesc(ctypes.Structure):
+    _fields_ = [("in_", ctypes.c_void_p),
+                ("out", ctypes.c_void_p),
+                ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64),
+                ("count", ctypes.c_int64),
+                ("in_row_stride", ctypes.c_int64),
+                ("in_matrix_stride", ctypes.c_int64),
+                ("out_row_stride", ctypes.c_int64),
+                ("out_matrix_stride", ctypes.c_int64)]
+
+
+class MatricesDesc(ctypes.Structure):
+    _fields_ = [("matrices", ctypes.POINTER(MatrixDesc)),
+                ("num_matrices", ctypes.c_int32),
+                ("in_type", ctypes.c_int32),
+                ("out_type", ctypes.c_int32)]
+
+
+class MuonTensorDesc(ctypes.Structure):
+    _fields_ = [("master", ctypes.c_void_p),
+                ("momentum", ctypes.c_void_p),
+                ("weight_out", ctypes.c_void_p),
+                ("grads", ctypes.c_void_p * MAX_REPLICAS),
+                ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64),
+                ("count", ctypes.c_int64)]
+
+
+class MuonLayerDesc(ctypes.Structure):
+    _fields_ = [("tensors", ctypes.POINTER(MuonTensorDesc)),
+                ("num_tensors", ctypes.c_int32),
+                ("num_replicas", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32)]
+
+
+class MuonParams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double),
+                ("momentum", ctypes.c_double),
+                ("weight_decay", ctypes.c_double),
+                ("grad_unscale", ctypes.c_double),
+                ("nesterov", ctypes.c_int32),
+                ("lr_scale", ctypes.c_int32),
+                ("polynomial", ctypes.POINTER(Polynomial))]
 
 
 class LayerAdamError(RuntimeError):
@@ -189,6 +251,19 @@ def load(path: Optional[str] = None):
     lib.la_copy_reference.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
                                       ctypes.c_void_p]
     lib.la_copy_reference.restype = ctypes.c_int
+    lib.la_orthogonalize.argtypes = [ctypes.POINTER(MatricesDesc), ctypes.POINTER(Polynomial),
+                                     ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]
+    lib.la_orthogonalize.restype = ctypes.c_int
+    lib.la_orthogonalize_workspace_bytes.argtypes = [ctypes.POINTER(MatricesDesc),
+                                                     ctypes.POINTER(Polynomial)]
+    lib.la_orthogonalize_workspace_bytes.restype = ctypes.c_int64
+    lib.layer_muon_step.argtypes = [ctypes.POINTER(MuonLayerDesc), ctypes.POINTER(MuonParams),
+                                    ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                    ctypes.c_int64, ctypes.c_void_p]
+    lib.layer_muon_step.restype = ctypes.c_int
+    lib.layer_muon_workspace_bytes.argtypes = [ctypes.POINTER(MuonLayerDesc),
+                                               ctypes.POINTER(MuonParams)]
+    lib.layer_muon_workspace_bytes.restype = ctypes.c_int64
     lib.la_state_bytes.argtypes = [ctypes.POINTER(LayerDesc)]
     lib.la_state_bytes.restype = ctypes.c_int64
     lib.la_traffic_bytes.argtypes = [ctypes.POINTER(LayerDesc)]
@@ -607,6 +682,350 @@ class Layer:
 
     def traffic_bytes(self) -> int:
         return traffic_bytes_raw(self._desc)
+
+
+# ---------------------------------------------------------------------------
+# The orthogonalised update and the Muon step
+# ---------------------------------------------------------------------------
+def make_polynomial(coefficients=None, eps: float = 1e-7):
+    """A Polynomial (with its array kept alive by it), or None for the
+    library's default."""
+    if coefficients is None and eps == 1e-7:
+        return None
+    steps = [tuple(float(x) for x in t) for t in
+             (NEWTON_SCHULZ if coefficients is None else coefficients)]
+    if any(len(t) != 3 for t in steps):
+        raise ValueError("coefficients are triples (a, b, c), one for each step")
+    flat = (ctypes.c_double * max(1, 3 * len(steps)))(*[x for t in steps for x in t])
+    p = Polynomial(ctypes.cast(flat, ctypes.POINTER(ctypes.c_double)), len(steps), float(eps))
+    p.keep = flat
+    return p
+
+
+def make_matrices(matrices: Sequence[dict], in_type: int, out_type: int):
+    """A MatricesDesc from dicts with integer pointers in_ and out, rows, cols
+    and, unless contiguous single matrices are meant, count and the four
+    strides. Returns (desc, keepalive)."""
+    arr = (MatrixDesc * max(1, len(matrices)))()
+    for i, x in enumerate(matrices):
+        arr[i].in_ = x.get("in_") or 0
+        arr[i].out = x.get("out") or 0
+        arr[i].rows, arr[i].cols = int(x["rows"]), int(x["cols"])
+        arr[i].count = int(x.get("count", 1))
+        for side in ("in", "out"):
+            row = int(x.get(side + "_row_stride", x["cols"]))
+            setattr(arr[i], side + "_row_stride", row)
+            setattr(arr[i], side + "_matrix_stride",
+                    int(x.get(side + "_matrix_stride", x["rows"] * row)))
+    return MatricesDesc(ctypes.cast(arr, ctypes.POINTER(MatrixDesc)), len(matrices), in_type,
+                        out_type), arr
+
+
+def make_muon_layer(tensors: Sequence[dict], num_replicas: int, grad_dtype: int,
+                    out_dtype: int = OUT_BF16):
+    """A MuonLayerDesc from dicts with integer pointers master, momentum,
+    weight_out, grads (list of R), and rows, cols, count. Returns (desc,
+    keepalive)."""
+    arr = (MuonTensorDesc * max(1, len(tensors)))()
+    for i, t in enumerate(tensors):
+        arr[i].master = t.get("master") or 0
+        arr[i].momentum = t.get("momentum") or 0
+        arr[i].weight_out = t.get("weight_out") or 0
+        for r, g in enumerate(t.get("grads", ())):
+            arr[i].grads[r] = g or 0
+        arr[i].rows, arr[i].cols = int(t["rows"]), int(t["cols"])
+        arr[i].count = int(t.get("count", 1))
+    return MuonLayerDesc(ctypes.cast(arr, ctypes.POINTER(MuonTensorDesc)), len(tensors),
+                         num_replicas, grad_dtype, out_dtype), arr
+
+
+def make_muon_params(lr, momentum=0.95, weight_decay=0.0, nesterov=True, grad_unscale=1.0,
+                     lr_scale="match_rms_adamw", polynomial=None) -> MuonParams:
+    if lr_scale not in LR_SCALES:
+        raise ValueError(f"lr_scale must be one of {sorted(LR_SCALES)}, got {lr_scale!r}")
+    hp = MuonParams(float(lr), float(momentum), float(weight_decay), float(grad_unscale),
+                    int(bool(nesterov)), LR_SCALES[lr_scale],
+                    None if polynomial is None else ctypes.pointer(polynomial))
+    hp.keep = polynomial
+    return hp
+
+
+def orthogonalize_workspace_bytes_raw(desc: MatricesDesc, polynomial=None) -> int:
+    return load().la_orthogonalize_workspace_bytes(
+        ctypes.byref(desc), None if polynomial is None else ctypes.byref(polynomial))
+
+
+def orthogonalize_raw(desc: MatricesDesc, polynomial=None, workspace: int = 0,
+                      workspace_bytes: int = 0, stream: int = 0) -> None:
+    """la_orthogonalize on raw descriptors; raises LayerAdamError on failure."""
+    lib = load()
+    _raise_on(lib.la_orthogonalize(
+        ctypes.byref(desc), None if polynomial is None else ctypes.byref(polynomial),
+        workspace or None, workspace_bytes, stream or None), lib)
+
+
+def muon_workspace_bytes_raw(desc: MuonLayerDesc, params: MuonParams) -> int:
+    return load().layer_muon_workspace_bytes(ctypes.byref(desc), ctypes.byref(params))
+
+
+def muon_step_raw(desc: MuonLayerDesc, params: MuonParams, overflow_flag: int = 0,
+                  skip_if_nonzero: int = 0, workspace: int = 0, workspace_bytes: int = 0,
+                  stream: int = 0) -> None:
+    """layer_muon_step on raw descriptors; raises LayerAdamError on failure."""
+    lib = load()
+    _raise_on(lib.layer_muon_step(ctypes.byref(desc), ctypes.byref(params),
+                                  overflow_flag or None, skip_if_nonzero or None,
+                                  workspace or None, workspace_bytes, stream or None), lib)
+
+
+def _workspace_ptr(workspace) -> int:
+    import torch
+    if not workspace.is_cuda or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise TypeError("the workspace must be a contiguous uint8 CUDA tensor")
+    return device_address(workspace)
+
+
+def _allocate_workspace(needed: int, stream):
+    """A workspace of ``needed`` bytes from torch's allocator, taken on
+    ``stream``, so that its memory is reused only behind the work there."""
+    import torch
+    with torch.cuda.stream(stream):
+        return torch.empty(max(1, needed), dtype=torch.uint8, device="cuda")
+
+
+def _element_type_of(tensors, what: str, allowed) -> int:
+    kinds = {t.dtype for t in tensors}
+    if len(kinds) == 1 and next(iter(kinds)) in allowed:
+        return allowed[next(iter(kinds))]
+    raise TypeError(f"{what} must all have one type of {[str(k) for k in allowed]}, got {kinds}")
+
+
+def _strides(t, turned: bool):
+    """(rows, cols, count, row stride, matrix stride) of a 2-D or 3-D tensor
+    read straight or turned (its last two axes exchanged), or None if its last
+    axis, so read, is not contiguous."""
+    row, col = (-1, -2) if turned else (-2, -1)
+    if t.shape[col] > 1 and t.stride(col) != 1:
+        return None
+    return (t.shape[row], t.shape[col], t.shape[0] if t.dim() == 3 else 1, t.stride(row),
+            t.stride(0) if t.dim() == 3 else 0)
+
+
+def _describe_matrices(xs, outs):
+    import torch
+    types = {torch.bfloat16: TYPE_BF16, torch.float16: TYPE_FP16, torch.float32: TYPE_FP32}
+    in_type = _element_type_of(xs, "matrices", types)
+    types.pop(torch.float32)
+    out_type = _element_type_of(outs, "outputs", types)
+    described = []
+    for i, (x, o) in enumerate(zip(xs, outs)):
+        if x.dim() not in (2, 3):
+            raise ValueError(f"tensor {i}: a matrix or a stack of them is needed, got "
+                             f"{x.dim()} dimensions")
+        if o.shape != x.shape:
+            raise ValueError(f"tensor {i}: out has shape {tuple(o.shape)}, expected "
+                             f"{tuple(x.shape)}")
+        for turned in (False, True):
+            a, b = _strides(x, turned), _strides(o, turned)
+            if a is not None and b is not None:
+                break
+        else:
+            raise ValueError(f"tensor {i}: the matrix and its output must be contiguous along "
+                             "the same of their last two axes")
+        described.append(dict(
+            in_=device_address(x) if x.numel() else 0, out=device_address(o) if x.numel() else 0,
+            rows=a[0], cols=a[1], count=a[2], in_row_stride=a[3], in_matrix_stride=a[4],
+            out_row_stride=b[3], out_matrix_stride=b[4]))
+    return described, in_type, out_type
+
+
+def _empty_direction(x, dtype):
+    """An output for x, contiguous along the axis that x is."""
+    import torch
+    if x.dim() in (2, 3) and _strides(x, False) is None and _strides(x, True) is not None:
+        return torch.empty_like(x.transpose(-1, -2), dtype=dtype,
+                                memory_format=torch.contiguous_format).transpose(-1, -2)
+    return torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format)
+
+
+def orthogonalize(x, out=None, *, coefficients=None, eps: float = 1e-7, workspace=None,
+                  stream=None):
+    """la_orthogonalize: each matrix replaced by a nearly orthogonal one with
+    its singular vectors, by Newton-Schulz products; enqueued on ``stream``
+    (default: the current torch stream).
+
+    x: a CUDA tensor of two dimensions (one matrix) or three (a stack), or a
+       list of them, all bf16, all fp16 or all fp32; contiguous along one of
+       the last two axes, other strides are free.
+    out: tensor(s) of the same shapes in bf16 or fp16 (default: new ones, fp16
+       for fp16 and else bf16), contiguous along the same axis; may be x.
+    coefficients: one triple (a, b, c) per step (default: NEWTON_SCHULZ).
+    workspace: a uint8 CUDA tensor of at least orthogonalize_workspace_bytes()
+       (default: taken from torch's allocator for the call).
+    Returns out.
+    """
+    import torch
+    single = isinstance(x, torch.Tensor)
+    xs = [x] if single else list(x)
+    if out is None:
+        outs = [_empty_direction(t, torch.float16 if t.dtype == torch.float16 else
+                                 torch.bfloat16) for t in xs]
+    else:
+        outs = [out] if single else list(out)
+        if len(outs) != len(xs):
+            raise ValueError("one output per matrix tensor")
+    if xs:
+        described, in_type, out_type = _describe_matrices(xs, outs)
+        desc, keep = make_matrices(described, in_type, out_type)
+        polynomial = make_polynomial(coefficients, eps)
+        s = stream if stream is not None else torch.cuda.current_stream()
+        if workspace is None:
+            needed = orthogonalize_workspace_bytes_raw(desc, polynomial)
+            workspace = _allocate_workspace(needed, s)
+        orthogonalize_raw(desc, polynomial, _workspace_ptr(workspace), workspace.numel(),
+                          s.cuda_stream)
+        del keep
+    return (outs[0] if single else outs) if out is None else out
+
+
+def orthogonalize_workspace_bytes(shapes, *, coefficients=None) -> int:
+    """Bytes of workspace of one orthogonalize() of matrices of these shapes,
+    (rows, cols) or (count, rows, cols) each. Matrices that are contiguous
+    along their rows rather than their columns count as their transposes."""
+    described = []
+    for s in shapes:
+        count, rows, cols = s if len(s) == 3 else (1, *s)
+        described.append(dict(rows=rows, cols=cols, count=count))
+    desc, keep = make_matrices(described, TYPE_FP32, TYPE_BF16)
+    needed = orthogonalize_workspace_bytes_raw(desc, make_polynomial(coefficients))
+    if needed < 0:
+        raise LayerAdamError(1, last_error())
+    return needed
+
+
+def _describe_muon(params, grads):
+    import torch
+    if len(params) != len(grads):
+        raise ValueError("one list of gradient replicas per tensor")
+    if not grads:
+        return [], 1, GRAD_BF16, OUT_BF16
+    R = len(grads[0])
+    if R > MAX_REPLICAS:
+        raise ValueError(f"{R} gradient replicas per tensor; at most {MAX_REPLICAS}")
+    gd = _grad_dtype_of(grads)
+    od = _out_dtype_of([(None, None, None, x[2] if len(x) > 2 else None) for x in params])
+    out = []
+    for i, (x, gs) in enumerate(zip(params, grads)):
+        p, m = x[0], x[1]
+        w = x[2] if len(x) > 2 else None
+        if p.dim() not in (2, 3):
+            raise ValueError(f"tensor {i}: the master must be a matrix or a stack of matrices, "
+                             f"got {p.dim()} dimensions (vectors take step())")
+        count, rows, cols = p.shape if p.dim() == 3 else (1, *p.shape)
+        n = p.numel()
+        d = dict(rows=rows, cols=cols, count=count)
+        for name, t in (("master", p), ("momentum", m)):
+            if t.dtype != torch.float32:
+                raise TypeError(f"tensor {i}: {name} must be float32, got {t.dtype}")
+            if t.numel() != n or not t.is_contiguous():
+                raise ValueError(f"tensor {i}: {name} must be a contiguous tensor "
+                                 f"of {n} elements")
+        if w is not None:
+            if w.numel() != n or not w.is_contiguous():
+                raise ValueError(f"tensor {i}: the compute copy must be a contiguous "
+                                 f"tensor of {n} elements")
+        if len(gs) != R:
+            raise ValueError(f"tensor {i}: {len(gs)} gradient replicas, expected {R}")
+        for g in gs:
+            if g.numel() != n or not g.is_contiguous():
+                raise ValueError(f"tensor {i}: gradients must be contiguous tensors "
+                                 f"of {n} elements")
+        d.update(master=device_address(p), momentum=device_address(m),
+                 weight_out=0 if w is None else device_address(w),
+                 grads=[device_address(g) for g in gs])
+        out.append(d)
+    return out, R, gd, od
+
+
+class MuonLayer:
+    """The matrices of a layer described once for repeated Muon steps, with
+    the workspace that the steps use. Holds references to the tensors.
+
+    params: per tensor a tuple (master fp32, momentum fp32, compute copy bf16,
+            fp16 or None); the master's shape is (rows, cols), or (count,
+            rows, cols) for a stack of matrices that are orthogonalised one by
+            one. Norm scales, biases and embeddings belong to a Layer.
+    grads:  per tensor a list of R gradient replicas (all bf16 or all fp16).
+    workspace: a uint8 CUDA tensor of at least workspace_bytes(), for layers
+            that are stepped one after the other on one stream to share;
+            default: one of the layer's own, taken at the first step.
+    """
+
+    def __init__(self, params, grads, workspace=None):
+        self._tensors = (list(params), [list(g) for g in grads])
+        tensors, self.num_replicas, self.grad_dtype, self.out_dtype = _describe_muon(params,
+                                                                                     grads)
+        self._desc, self._keep = make_muon_layer(tensors, self.num_replicas, self.grad_dtype,
+                                                 self.out_dtype)
+        self.numel = sum(t["rows"] * t["cols"] * t["count"] for t in tensors)
+        self._given = workspace is not None
+        self._workspace = workspace
+        self._stream = None
+
+    def workspace_bytes(self, *, nesterov: bool = True, coefficients=None) -> int:
+        hp = make_muon_params(0.0, nesterov=nesterov, polynomial=make_polynomial(coefficients))
+        needed = muon_workspace_bytes_raw(self._desc, hp)
+        if needed < 0:
+            raise LayerAdamError(1, last_error())
+        return needed
+
+    def step(self, *, lr: float, momentum: float = 0.95, weight_decay: float = 0.0,
+             nesterov: bool = True, grad_unscale: float = 1.0,
+             lr_scale: str = "match_rms_adamw", coefficients=None, eps: float = 1e-7,
+             overflow_flag=None, skip_if_nonzero=None, stream=None) -> None:
+        """One layer_muon_step, enqueued on ``stream`` (default: the current
+        torch stream)."""
+        import torch
+        hp = make_muon_params(lr, momentum, weight_decay, nesterov, grad_unscale, lr_scale,
+                              make_polynomial(coefficients, eps))
+        s = stream if stream is not None else torch.cuda.current_stream()
+        if not self._given:
+            needed = muon_workspace_bytes_raw(self._desc, hp)
+            if self._workspace is None or self._workspace.numel() < needed:
+                self._workspace, self._stream = _allocate_workspace(needed, s), s
+            elif self._stream != s and not torch.cuda.is_current_stream_capturing():
+                self._workspace.record_stream(s)
+        muon_step_raw(self._desc, hp, _flag_ptr(overflow_flag),
+                      _flag_ptr(skip_if_nonzero, "skip_if_nonzero"),
+                      _workspace_ptr(self._workspace), self._workspace.numel(), s.cuda_stream)
+
+    def check_gradients(self, found_nonfinite, *, grad_unscale: float = 1.0,
+                        stream=None) -> None:
+        """la_check_gradients of the layer's gradients, for skip_if_nonzero."""
+        check_gradients(self._tensors[1], found_nonfinite, grad_unscale=grad_unscale,
+                        stream=stream)
+
+
+def muon_step(params, grads, *, lr: float, momentum: float = 0.95, weight_decay: float = 0.0,
+              nesterov: bool = True, grad_unscale: float = 1.0,
+              lr_scale: str = "match_rms_adamw", coefficients=None, eps: float = 1e-7,
+              overflow_flag=None, skip_if_nonzero=None, workspace=None, stream=None) -> None:
+    """One Muon step of a layer's matrices (params and grads as for
+    MuonLayer), enqueued on ``stream`` (default: the current torch stream);
+    the workspace, unless given, is taken from torch's allocator for the call.
+
+    lr_scale: the factor of the direction -- "match_rms_adamw" (0.2
+              sqrt(max(rows, cols)), for AdamW's lr and weight_decay),
+              "original" (sqrt(max(1, rows / cols))) or "none".
+    overflow_flag: optional int32 CUDA tensor of one element (set to 1 on a
+              non-finite aggregated gradient; never cleared).
+    skip_if_nonzero: optional int32 CUDA tensor: nothing is touched if it holds
+              a non-zero value when the kernels run.
+    """
+    MuonLayer(params, grads, workspace).step(
+        lr=lr, momentum=momentum, weight_decay=weight_decay, nesterov=nesterov,
+        grad_unscale=grad_unscale, lr_scale=lr_scale, coefficients=coefficients, eps=eps,
+        overflow_flag=overflow_flag, skip_if_nonzero=skip_if_nonzero, stream=stream)
 
 
 def copy_reference(dst, src, stream=None) -> None:

@@ -17,12 +17,15 @@
 #include <vector>
 
 #include "la_copy.h"
+#include "la_error.h"
 #include "la_internal.h"
 #include "layeradam.h"
 
 namespace {
-
 thread_local char g_error[512] = "";
+}  // namespace
+
+namespace la {
 
 la_status fail(la_status code, const char* fmt, ...) {
   va_list ap;
@@ -36,6 +39,31 @@ la_status ok() {
   g_error[0] = '\0';
   return LA_OK;
 }
+
+// One workgroup per chunk up to this many; the kernels stride past it.
+constexpr int kMaxGrid = 1 << 30;
+
+// Most workgroups of one launch: kMaxGrid, or LAYERADAM_MAX_GRID (1..kMaxGrid,
+// read once), which lets a test drive the kernels' striding loops with
+// layers of ordinary size.
+int max_grid() {
+  static const int value = [] {
+    const char* env = std::getenv("LAYERADAM_MAX_GRID");
+    if (env == nullptr || *env == '\0') return kMaxGrid;
+    char* end = nullptr;
+    const long v = std::strtol(env, &end, 10);
+    return (*end == '\0' && v >= 1 && v <= kMaxGrid) ? static_cast<int>(v) : kMaxGrid;
+  }();
+  return value;
+}
+
+}  // namespace la
+
+namespace {
+
+using la::fail;
+using la::max_grid;
+using la::ok;
 
 // Per-device launch facts, read once per device: the LDS of one compute
 // unit and the most one workgroup may take (the kernels size their LDS
@@ -79,23 +107,6 @@ int workgroups_per_cu_override() {
     char* end = nullptr;
     const long v = std::strtol(env, &end, 10);
     return (*end == '\0' && v >= 0 && v <= 64) ? static_cast<int>(v) : -1;
-  }();
-  return value;
-}
-
-// One workgroup per chunk up to this many; the kernels stride past it.
-constexpr int kMaxGrid = 1 << 30;
-
-// Most workgroups of one launch: kMaxGrid, or LAYERADAM_MAX_GRID (1..kMaxGrid,
-// read once), which lets a test drive the kernels' striding loops with
-// layers of ordinary size.
-int max_grid() {
-  static const int value = [] {
-    const char* env = std::getenv("LAYERADAM_MAX_GRID");
-    if (env == nullptr || *env == '\0') return kMaxGrid;
-    char* end = nullptr;
-    const long v = std::strtol(env, &end, 10);
-    return (*end == '\0' && v >= 1 && v <= kMaxGrid) ? static_cast<int>(v) : kMaxGrid;
   }();
   return value;
 }
