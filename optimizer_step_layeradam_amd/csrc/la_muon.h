@@ -107,8 +107,8 @@ struct ProductGroup {
   const half_bits* q;      // N x ldq
   const half_bits* hi;     // linear term: M x ldc (kSquare: A; kUpdate...: X straight)
   const half_bits* lo;     // kUpdate
-  const float* diag;       // m: diagonal of A (kSquare) or of B (kUpdate, kOut, kMuon)
-  float* diag_out;         // m: diagonal of A (kGram) or of B (kSquare)
+  const float* diag;       // m padded: diagonal of A (kSquare) or of B (kUpdate, kOut, kMuon)
+  float* diag_out;         // m padded: diagonal of A (kGram) or of B (kSquare)
   half_bits* c;            // result, M x ldc (kOut: none)
   half_bits* c_lo;         // kUpdate, or null where nothing reads it
   half_bits* turned;       // kUpdate: N x ld_turned
@@ -120,6 +120,7 @@ struct ProductGroup {
   int32_t ldp, ldq, ldc, ld_turned;
   int32_t count;
   int32_t tall;            // diag runs along N rather than M
+  int32_t vectors;         // kOut, kMuon: every 8 elements of a row are 16-byte aligned
   float step;              // kMuon: lr times the stack's scale
 };
 

@@ -182,8 +182,8 @@ int64_t lay_out(std::vector<Stack>& stacks, int steps, bool direction, bool cont
       at = std::max(at, second + round_up(4 * k * s.numel_direction, LA_WORKSPACE_ALIGNMENT));
     s.gram = take(2 * k * s.m * s.ldm);
     s.poly = take(2 * k * s.m * s.ldm);
-    s.gram_diag = take(4 * k * s.m);
-    s.poly_diag = take(4 * k * s.m);
+    s.gram_diag = take(4 * k * s.ldm);
+    s.poly_diag = take(4 * k * s.ldm);
     s.partial = take(8 * k * s.partials);
   }
   return at;
@@ -219,7 +219,7 @@ la_status enqueue_products(const std::vector<Stack>& stacks, const Polynomial& p
             ws, what == la::Product::kSquare ? s.gram_diag : s.poly_diag);
         x.diag_out = place<float>(
             ws, what == la::Product::kGram ? s.gram_diag : s.poly_diag);
-        x.diag_stride = s.m;
+        x.diag_stride = s.ldm;
         x.count = static_cast<int32_t>(s.count);
         x.tall = tall;
         if (what == la::Product::kGram || what == la::Product::kSquare) {
@@ -467,6 +467,8 @@ la_status orthogonalize(const la_matrices_desc* d, const la_polynomial* polynomi
         x.out = d->matrices[s.index].out;
         x.out_ld = d->matrices[s.index].out_row_stride;
         x.out_stride = d->matrices[s.index].out_matrix_stride;
+        x.vectors = aligned(x.out, 16) && (s.rows == 1 || x.out_ld % 8 == 0) &&
+                    (s.count == 1 || x.out_stride % 8 == 0);
       },
       ws, nullptr, stream);
 }
@@ -616,6 +618,7 @@ la_status muon_step(const la_muon_layer_desc* layer, const la_muon_params* hp, i
         const la_muon_tensor_desc& t = layer->tensors[s.index];
         x.master = t.master;
         x.out = copy ? t.weight_out : nullptr;
+        x.vectors = s.cols % 8 == 0;
         x.step = static_cast<float>(hp->lr * lr_scale(hp->lr_scale, s.rows, s.cols));
       },
       ws, skip, stream);

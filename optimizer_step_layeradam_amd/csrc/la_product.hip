@@ -3,6 +3,7 @@
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+#include <stdlib.h>
 
 #include "la_muon.h"
 
@@ -12,13 +13,39 @@ namespace la {
 namespace {
 
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
-typedef _Float16 half4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+
+// Raw buffer resource over a uniform base: no stride, 2 GiB of range, the
+// fourth word of a 32-bit-format buffer.
+constexpr int kRsrcRange = 0x7fffffff;
+constexpr int kRsrcWord3 = 0x00020000;
+
+// 16 bytes per lane from memory to 1 KiB of LDS at `to` (lane order), without
+// a register between; done when the wave's vmcnt says so.
+__device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t from, _Float16* to, int offset,
+                                            int uniform_offset) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(
+      from, (__attribute__((address_space(3))) void*)to, 16, offset, uniform_offset, 0, 0);
+}
+
+// This wave's copies have landed and its reads of LDS are done; so are those
+// of every wave of the workgroup after it.
+__device__ __forceinline__ void wait_and_meet() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// Orders the wave's own LDS accesses, which lanes exchange data through.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
 
 struct ProductArgs {
   ProductGroup g[kGroupsPerLaunch];
   int64_t tile_end[kGroupsPerLaunch];  // cumulative tiles
-  int32_t tiles_n[kGroupsPerLaunch];   // tiles along N (square form: along either side)
+  int32_t tiles_m[kGroupsPerLaunch], tiles_n[kGroupsPerLaunch];
   int32_t tiles[kGroupsPerLaunch];     // tiles of one matrix
   ProductScales s;
   const int32_t* skip;
@@ -38,16 +65,6 @@ __device__ __forceinline__ uint16_t fp16_bits(float x) {
   return __builtin_isnan(x) ? uint16_t(0x7E00) : h;
 }
 
-// Tile index within a stack of symmetric results: row i of the lower triangle
-// holds the tiles (i, 0) .. (i, i).
-__device__ __forceinline__ void triangle(int t, int& i, int& j) {
-  int r = static_cast<int>((__builtin_sqrtf(8.0f * t + 1.0f) - 1.0f) * 0.5f);
-  while (static_cast<int64_t>(r) * (r + 1) / 2 > t) --r;
-  while (static_cast<int64_t>(r + 1) * (r + 2) / 2 <= t) ++r;
-  i = r;
-  j = t - static_cast<int>(static_cast<int64_t>(r) * (r + 1) / 2);
-}
-
 // Workgroup w of n runs on XCD w % 8: give each XCD consecutive tiles of
 // every 256, so that the tiles its L2 serves share operand rows.
 __device__ __forceinline__ int64_t xcd_order(int64_t w, int64_t n) {
@@ -58,15 +75,198 @@ __device__ __forceinline__ int64_t xcd_order(int64_t w, int64_t n) {
   return base + x * q + (x < r ? x : r) + (l >> 3);
 }
 
+// Tile t of a matrix, in bands of four tile rows taken column by column: 32
+// consecutive tiles are about 4 x 8 of them.
+__device__ __forceinline__ void rectangle(int t, int tiles_m, int tiles_n, int& i, int& j) {
+  const int band = t / (4 * tiles_n), first = 4 * band;
+  const int rows = tiles_m - first < 4 ? tiles_m - first : 4;
+  const int l = t - band * 4 * tiles_n;
+  i = first + l % rows;
+  j = l / rows;
+}
+
+// The same for the lower triangle: a band's columns up to its first row are
+// whole, the last ones shorter by one tile each.
+__device__ __forceinline__ void triangle(int t, int tiles_m, int& i, int& j) {
+  int r = static_cast<int>((__builtin_sqrtf(8.0f * t + 1.0f) - 1.0f) * 0.5f);
+  while (static_cast<int64_t>(r) * (r + 1) / 2 > t) --r;
+  while (static_cast<int64_t>(r + 1) * (r + 2) / 2 <= t) ++r;
+  const int first = r & ~3;
+  const int rows = tiles_m - first < 4 ? tiles_m - first : 4;
+  int l = t - static_cast<int>(static_cast<int64_t>(first) * (first + 1) / 2);
+  if (l < rows * (first + 1)) {
+    i = first + l % rows;
+    j = l / rows;
+    return;
+  }
+  l -= rows * (first + 1);
+  int c = 1;
+  while (l >= rows - c) {
+    l -= rows - c;
+    ++c;
+  }
+  i = first + c + l;
+  j = first + c;
+}
+
+// ---- the kernel ----------------------------------------------------------------------
+// A workgroup of WM x WN waves forms a tile of (32 MT WM) x (64 WN) elements
+// of C, each wave MT x 2 blocks of 32 x 32. A stage is kDepth elements of the
+// summed side: 128 bytes of every row of both operands, copied from memory
+// straight into LDS, where a row's 16-byte pieces are stored at piece ^
+// (row / 2 % 8): a wave's read of one piece of 32 rows then meets every bank
+// group equally often, whichever of its lanes are served together. Two stages
+// are held; the copy of one runs under the products of the other. Per stage a
+// wave takes four steps of 16 elements, whose fragments it reads one step
+// ahead; before the last step's products it waits for its own copies and
+// meets the others, so that the next stage's first fragments arrive under
+// these products.
+
+template <int MT, int WM, int WN>
+struct Tile {
+  static constexpr int waves = WM * WN;
+  static constexpr int threads = 64 * waves;
+  static constexpr int rows = 32 * MT * WM, cols = 64 * WN;
+  static constexpr int stage = (rows + cols) * kDepth;  // elements
+  static constexpr int copies = stage * 2 / (threads * 16);
+  static_assert(2 * stage * 2 >= waves * 16384, "the epilogue takes 16 KiB of LDS per wave");
+  static_assert(rows % (8 * waves) == 0 && cols % (8 * waves) == 0, "whole rows per copy");
+};
+
+template <int MT>
+struct Fragments {
+  half8 p[MT], q[2];
+};
+
+// Eight results of one row, in place of their sums: what is kept of them in
+// binary16 (zero outside the matrix), after what the epilogue stores itself.
 template <Product WHAT, int OUT>
-__global__ __launch_bounds__(256) void product_kernel(ProductArgs a) {
-  constexpr int BM = 128, BN = 128;
+__device__ __forceinline__ half8 finish(const ProductGroup& g, const ProductScales& s, int z,
+                                        int row, int col, const float (&sum)[8]) {
+  const bool row_in = row < g.M;
+  const int r = row_in ? row : g.M - 1;
+  const int c = col < g.ldc ? col : g.ldc - 8;
+  const int64_t at = z * g.c_stride + static_cast<int64_t>(r) * g.ldc + c;
+  half8 h = {};
+  if constexpr (WHAT == Product::kGram) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float v = sum[e] * s.acc;
+      if (row_in && col + e < g.N) {
+        if (row == col + e) g.diag_out[z * g.diag_stride + row] = v;
+        else h[e] = static_cast<_Float16>(v);
+      }
+    }
+  } else if constexpr (WHAT == Product::kSquare) {
+    const half8 hi = *reinterpret_cast<const half8*>(reinterpret_cast<const _Float16*>(g.hi) + at);
+    const float* D = g.diag + z * g.diag_stride;
+    const float dr = D[r];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float dc = D[c + e];
+      if (row_in && col + e < g.N) {
+        if (row == col + e)
+          g.diag_out[z * g.diag_stride + row] =
+              (s.linear * dr + (s.diag * (dr * dr) + s.acc * sum[e])) * s.out;
+        else
+          h[e] = static_cast<_Float16>((s.linear + s.diag * (dr + dc)) *
+                                           static_cast<float>(hi[e]) + s.acc * sum[e]);
+      }
+    }
+  } else {
+    const half8 hi = *reinterpret_cast<const half8*>(reinterpret_cast<const _Float16*>(g.hi) + at);
+    const float* D = g.diag + z * g.diag_stride;
+    float v[8];
+    if constexpr (WHAT == Product::kUpdate) {
+      const half8 lo =
+          *reinterpret_cast<const half8*>(reinterpret_cast<const _Float16*>(g.lo) + at);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = static_cast<float>(hi[e]);
+        const float d = s.diag * (g.tall ? D[c + e] : D[r]);
+        v[e] = s.linear * (x + static_cast<float>(lo[e]) * 0x1p-11f) + (d * x + s.acc * sum[e]);
+      }
+      half8 l;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (row_in && col + e < g.N) h[e] = static_cast<_Float16>(v[e]);
+        l[e] = static_cast<_Float16>((v[e] - static_cast<float>(h[e])) * 0x1p11f);
+      }
+      if (g.c_lo != nullptr && row_in && col < g.ldc)
+        *reinterpret_cast<half8*>(reinterpret_cast<_Float16*>(g.c_lo) + at) = l;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float d = s.diag * (g.tall ? D[c + e] : D[r]);
+        v[e] = (s.linear + d) * static_cast<float>(hi[e]) + s.acc * sum[e];
+      }
+      if (row_in && col < g.N) {
+        const bool whole = g.vectors && col + 8 <= g.N;
+        if constexpr (WHAT == Product::kOut) {
+          uint16_t* o = static_cast<uint16_t*>(g.out) + z * g.out_stride + row * g.out_ld + col;
+          u16x8 w;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] = OUT == kBf16 ? bf16_bits(v[e]) : fp16_bits(v[e]);
+          if (whole) {
+            *reinterpret_cast<u16x8*>(o) = w;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (col + e < g.N) o[e] = w[e];
+          }
+        } else {
+          const int64_t k = (static_cast<int64_t>(z) * g.M + row) * g.N + col;
+          float* m = g.master + k;
+          uint16_t* o = static_cast<uint16_t*>(g.out) + k;
+          float p[8];
+          u16x8 w;
+          if (whole) {
+            const f32x4 p0 = *reinterpret_cast<const f32x4*>(m);
+            const f32x4 p1 = *reinterpret_cast<const f32x4*>(m + 4);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] = e < 4 ? p0[e] : p1[e - 4];
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] = col + e < g.N ? m[e] : 0.0f;
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            p[e] = p[e] * s.decay - g.step * v[e];
+            w[e] = OUT == kBf16 ? bf16_bits(p[e]) : fp16_bits(p[e]);
+          }
+          if (whole) {
+            *reinterpret_cast<f32x4*>(m) = f32x4{p[0], p[1], p[2], p[3]};
+            *reinterpret_cast<f32x4*>(m + 4) = f32x4{p[4], p[5], p[6], p[7]};
+            if constexpr (OUT >= 0) *reinterpret_cast<u16x8*>(o) = w;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (col + e < g.N) {
+                m[e] = p[e];
+                if constexpr (OUT >= 0) o[e] = w[e];
+              }
+          }
+        }
+      }
+    }
+  }
+  if constexpr (WHAT == Product::kGram || WHAT == Product::kSquare || WHAT == Product::kUpdate) {
+    if (row_in && col < g.ldc)
+      *reinterpret_cast<half8*>(reinterpret_cast<_Float16*>(g.c) + at) = h;
+  }
+  return h;
+}
+
+template <Product WHAT, int OUT, int MT, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void product_kernel(ProductArgs a) {
+  using T = Tile<MT, WM, WN>;
   constexpr bool SYM = WHAT == Product::kGram || WHAT == Product::kSquare;
-  __shared__ __align__(16) _Float16 sp[2][BM * kDepth];
-  __shared__ __align__(16) _Float16 sq[2][BN * kDepth];
+  constexpr bool TURN = SYM || WHAT == Product::kUpdate;
+  __shared__ __align__(1024) _Float16 lds[2 * T::stage];
   if (a.skip != nullptr && *a.skip != 0) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = (wave / WN) * 32 * MT, wn = (wave % WN) * 64;
   const int64_t total = a.tile_end[a.count - 1];
 
   for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
@@ -78,177 +278,157 @@ __global__ __launch_bounds__(256) void product_kernel(ProductArgs a) {
     const int z = static_cast<int>(local / a.tiles[gi]);
     const int t = static_cast<int>(local % a.tiles[gi]);
     int ti, tj;
-    if constexpr (SYM) {
-      triangle(t, ti, tj);
-    } else {
-      ti = t / a.tiles_n[gi];
-      tj = t % a.tiles_n[gi];
-    }
-    const int row0 = ti * BM, col0 = tj * BN;
+    if constexpr (SYM) triangle(t, a.tiles_m[gi], ti, tj);
+    else rectangle(t, a.tiles_m[gi], a.tiles_n[gi], ti, tj);
+    const int row0 = ti * T::rows, col0 = tj * T::cols;
 
-    // Thread t loads 16-byte piece (t & 7) of row (t >> 3) + 32 i of each
-    // operand's stage; a row past the matrix is its last one, whose results
-    // are not stored.
-    const _Float16* P = reinterpret_cast<const _Float16*>(g.p) + z * g.p_stride;
-    const _Float16* Q = reinterpret_cast<const _Float16*>(g.q) + z * g.q_stride;
-    const _Float16* pp[4];
-    const _Float16* qq[4];
+    // Copy c of a stage brings 8 rows per wave, one 16-byte piece per lane. A
+    // row past the matrix is its last one again: its results are not kept.
+    // Offsets are 32 bits from the tile's first row (at most 256 rows of 2
+    // MiB).
+    const int64_t p_first = static_cast<int64_t>(z) * g.p_stride + static_cast<int64_t>(row0) * g.ldp;
+    const int64_t q_first = static_cast<int64_t>(z) * g.q_stride + static_cast<int64_t>(col0) * g.ldq;
+    const __amdgpu_buffer_rsrc_t rp = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<half_bits*>(g.p + p_first), 0, kRsrcRange, kRsrcWord3);
+    const __amdgpu_buffer_rsrc_t rq = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<half_bits*>(g.q + q_first), 0, kRsrcRange, kRsrcWord3);
+    constexpr int PC = T::rows / (8 * T::waves), QC = T::cols / (8 * T::waves);
+    int po[PC], qo[QC];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = (tid >> 3) + 32 * i;
-      const int piece = (tid & 7) ^ ((r >> 1) & 7);
-      const int pr = row0 + r < g.M ? row0 + r : g.M - 1;
-      const int qr = col0 + r < g.N ? col0 + r : g.N - 1;
-      pp[i] = P + static_cast<int64_t>(pr) * g.ldp + piece * 8;
-      qq[i] = Q + static_cast<int64_t>(qr) * g.ldq + piece * 8;
+    for (int c = 0; c < PC; ++c) {
+      const int r = (c * T::waves + wave) * 8 + (lane >> 3);
+      const int most = g.M - 1 - row0;
+      po[c] = (r < most ? r : most) * g.ldp * 2 + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
     }
-
-    f32x16 acc[2][2] = {};
-    const int stages = g.K / kDepth;
-    half8 rp[4], rq[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      rp[i] = *reinterpret_cast<const half8*>(pp[i]);
-      rq[i] = *reinterpret_cast<const half8*>(qq[i]);
+    for (int c = 0; c < QC; ++c) {
+      const int r = (c * T::waves + wave) * 8 + (lane >> 3);
+      const int most = g.N - 1 - col0;
+      qo[c] = (r < most ? r : most) * g.ldq * 2 + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
     }
-    for (int k = 0; k < stages; ++k) {
-      const int b = k & 1;
+    auto copy = [&](int k) {
+      _Float16* to = lds + (k & 1) * T::stage + wave * 8 * kDepth;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        *reinterpret_cast<half8*>(&sp[b][(tid + 256 * i) * 8]) = rp[i];
-        *reinterpret_cast<half8*>(&sq[b][(tid + 256 * i) * 8]) = rq[i];
+      for (int c = 0; c < PC; ++c)
+        copy_to_lds(rp, to + c * T::waves * 8 * kDepth, po[c], k * kDepth * 2);
+      to += T::rows * kDepth;
+#pragma unroll
+      for (int c = 0; c < QC; ++c)
+        copy_to_lds(rq, to + c * T::waves * 8 * kDepth, qo[c], k * kDepth * 2);
+    };
+    auto read = [&](Fragments<MT>& f, int k, int step) {
+      const _Float16* from = lds + (k & 1) * T::stage;
+      const int piece = 2 * step + (lane >> 5);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int r = wm + 32 * i + (lane & 31);
+        f.p[i] = *reinterpret_cast<const half8*>(from + r * kDepth + ((piece ^ ((r >> 1) & 7)) << 3));
       }
-      __syncthreads();
-      if (k + 1 < stages) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          rp[i] = *reinterpret_cast<const half8*>(pp[i] + static_cast<int64_t>(k + 1) * kDepth);
-          rq[i] = *reinterpret_cast<const half8*>(qq[i] + static_cast<int64_t>(k + 1) * kDepth);
-        }
-      }
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        half8 fp[2], fq[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = wm + 32 * i + (lane & 31), c = 2 * kk + (lane >> 5);
-          fp[i] = *reinterpret_cast<const half8*>(&sp[b][r * kDepth + ((c ^ ((r >> 1) & 7)) * 8)]);
-          const int s = wn + 32 * i + (lane & 31);
-          fq[i] = *reinterpret_cast<const half8*>(&sq[b][s * kDepth + ((c ^ ((s >> 1) & 7)) * 8)]);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fp[i], fq[j], acc[i][j], 0, 0, 0);
-      }
-    }
-
-    // Lane l holds column l & 31 and, in register r, row 8 (r / 4) +
-    // 4 (l / 32) + r % 4 of each 32 x 32 result.
-    const _Float16* HI = reinterpret_cast<const _Float16*>(g.hi) + z * g.c_stride;
-    const _Float16* LO = reinterpret_cast<const _Float16*>(g.lo) + z * g.c_stride;
-    _Float16* C = reinterpret_cast<_Float16*>(g.c) + z * g.c_stride;
-    _Float16* CLO = reinterpret_cast<_Float16*>(g.c_lo) + z * g.c_stride;
-    _Float16* T = reinterpret_cast<_Float16*>(g.turned) + z * g.turned_stride;
-    const float* D = g.diag + z * g.diag_stride;
-    float* DOUT = g.diag_out + z * g.diag_stride;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
+      from += T::rows * kDepth;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int col = col0 + wn + 32 * j + (lane & 31);
+        const int r = wn + 32 * j + (lane & 31);
+        f.q[j] = *reinterpret_cast<const half8*>(from + r * kDepth + ((piece ^ ((r >> 1) & 7)) << 3));
+      }
+    };
+    f32x16 acc[MT][2] = {};
+    auto multiply = [&](const Fragments<MT>& f) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int row = row0 + wm + 32 * i + 8 * q + 4 * (lane >> 5);
-          _Float16 h[4] = {};
+      for (int i = 0; i < MT; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float sum = acc[i][j][4 * q + e];
-            const bool in = row + e < g.M && col < g.N;
-            const int64_t at = static_cast<int64_t>(row + e) * g.ldc + col;
-            if constexpr (WHAT == Product::kGram) {
-              if (in) {
-                const float v = sum * a.s.acc;
-                if (row + e == col) DOUT[col] = v;
-                else h[e] = static_cast<_Float16>(v);
-              }
-            } else if constexpr (WHAT == Product::kSquare) {
-              if (in) {
-                if (row + e == col) {
-                  const float d = D[col];
-                  DOUT[col] = (a.s.linear * d + (a.s.diag * (d * d) + a.s.acc * sum)) * a.s.out;
-                } else {
-                  const float d = a.s.diag * (D[row + e] + D[col]);
-                  h[e] = static_cast<_Float16>((a.s.linear + d) * static_cast<float>(HI[at]) +
-                                               a.s.acc * sum);
-                }
-              }
-            } else if (in) {
-              const float hi = static_cast<float>(HI[at]);
-              const float d = a.s.diag * (g.tall ? D[col] : D[row + e]);
-              float v;
-              if constexpr (WHAT == Product::kUpdate)
-                v = a.s.linear * (hi + static_cast<float>(LO[at]) * 0x1p-11f) + (d * hi + a.s.acc * sum);
-              else
-                v = (a.s.linear + d) * hi + a.s.acc * sum;
-              if constexpr (WHAT == Product::kUpdate) {
-                h[e] = static_cast<_Float16>(v);
-                if (g.c_lo != nullptr)
-                  CLO[at] = static_cast<_Float16>((v - static_cast<float>(h[e])) * 0x1p11f);
-              } else if constexpr (WHAT == Product::kOut) {
-                static_cast<uint16_t*>(g.out)[z * g.out_stride + (row + e) * g.out_ld + col] =
-                    OUT == kBf16 ? bf16_bits(v) : fp16_bits(v);
-              } else {
-                const int64_t k = (static_cast<int64_t>(z) * g.M + row + e) * g.N + col;
-                const float p = g.master[k] * a.s.decay - g.step * v;
-                g.master[k] = p;
-                if constexpr (OUT >= 0)
-                  static_cast<uint16_t*>(g.out)[k] = OUT == kBf16 ? bf16_bits(p) : fp16_bits(p);
-              }
-            }
-            if constexpr (SYM || WHAT == Product::kUpdate) {
-              if (row + e < g.M && col < g.ldc) C[at] = h[e];
-            }
+        for (int j = 0; j < 2; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.p[i], f.q[j], acc[i][j], 0, 0, 0);
+    };
+
+    const int stages = g.K / kDepth;
+    Fragments<MT> f0, f1;
+    copy(0);
+    wait_and_meet();
+    read(f0, 0, 0);
+    for (int k = 0; k < stages; ++k) {
+      if (k + 1 < stages) copy(k + 1);
+      read(f1, k, 1);
+      multiply(f0);
+      read(f0, k, 2);
+      multiply(f1);
+      read(f1, k, 3);
+      multiply(f0);
+      wait_and_meet();
+      if (k + 1 < stages) read(f0, k + 1, 0);
+      multiply(f1);
+    }
+    // every wave is past its last read of LDS: the last wait_and_meet
+
+    // Per 64 rows: the sums change from the accumulators' layout (lane l:
+    // column l % 32; register r: row 8 (r / 4) + 4 (l / 32) + r % 4) to eight
+    // neighbours of a row per lane through 8 KiB of LDS per wave, are
+    // finished, and their binary16 form passes through another 8 KiB to be
+    // stored turned. Both places are the wave's own.
+    float* sums = reinterpret_cast<float*>(lds) + wave * 4096;
+    _Float16* turn = reinterpret_cast<_Float16*>(sums + 2048);
+    const bool mirror = TURN && (!SYM || ti != tj);
+#pragma unroll
+    for (int c = 0; c < MT / 2; ++c) {
+      const int rowc = row0 + wm + 64 * c, colw = col0 + wn;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int r = 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
+            sums[r * 64 + ((32 * j + (lane & 31)) ^ ((lane >> 5) << 5))] = acc[2 * c + hf][j][e];
           }
-          // four consecutive elements of the turned result (row is a multiple
-          // of 4 and the padded side of 64)
-          if constexpr (SYM) {
-            if (ti != tj && col < g.N && row < g.ldc)
-              *reinterpret_cast<half4*>(&C[static_cast<int64_t>(col) * g.ldc + row]) =
-                  half4{h[0], h[1], h[2], h[3]};
-          } else if constexpr (WHAT == Product::kUpdate) {
-            if (col < g.N && row < g.ld_turned)
-              *reinterpret_cast<half4*>(&T[static_cast<int64_t>(col) * g.ld_turned + row]) =
-                  half4{h[0], h[1], h[2], h[3]};
+        wave_fence();
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const int r = 8 * p + (lane >> 3), k = (lane & 7) * 8;
+          const float* from = sums + r * 64 + (k ^ (((r >> 2) & 1) << 5));
+          float v[8];
+          *reinterpret_cast<f32x4*>(v) = *reinterpret_cast<const f32x4*>(from);
+          *reinterpret_cast<f32x4*>(v + 4) = *reinterpret_cast<const f32x4*>(from + 4);
+          const half8 h = finish<WHAT, OUT>(g, a.s, z, rowc + 32 * hf + r, colw + k, v);
+          if constexpr (TURN) {
+            const int rr = 32 * hf + r;
+            *reinterpret_cast<half8*>(turn + rr * 64 + (((lane & 7) ^ ((rr >> 3) & 7)) << 3)) = h;
           }
         }
+        wave_fence();
       }
-    __syncthreads();  // the stages are free for the next tile
+      if (mirror) {
+        _Float16* to = reinterpret_cast<_Float16*>(SYM ? g.c : g.turned) +
+                       static_cast<int64_t>(z) * (SYM ? g.c_stride : g.turned_stride);
+        const int ld = SYM ? g.ldc : g.ld_turned;
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          const int k = 8 * p + (lane >> 3), r = (lane & 7) * 8;
+          half8 h;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            h[e] = turn[(r + e) * 64 + ((p ^ (lane & 7)) << 3) + (lane >> 3)];
+          if (colw + k < g.N && rowc + r < ld)
+            *reinterpret_cast<half8*>(to + static_cast<int64_t>(colw + k) * ld + rowc + r) = h;
+        }
+        wave_fence();
+      }
+    }
+    __syncthreads();  // LDS is free for the next tile
   }
 }
 
-template <Product WHAT, int OUT>
-hipError_t launch_one(ProductArgs& a, int64_t total, hipStream_t stream, int64_t max_grid) {
-  int64_t grid = total < kMaxWorkgroups ? total : kMaxWorkgroups;
-  if (grid > max_grid) grid = max_grid;
-  void* params[] = {&a};
-  return hipLaunchKernel(reinterpret_cast<const void*>(&product_kernel<WHAT, OUT>),
-                         dim3(static_cast<unsigned>(grid)), dim3(256), params, 0, stream);
-}
-
-}  // namespace
-
-hipError_t launch_product(const ProductGroup* groups, int count, Product what, int out_type,
-                          const ProductScales& s, const int32_t* skip, hipStream_t stream,
-                          int64_t max_grid) {
+template <Product WHAT, int OUT, int MT, int WM, int WN>
+hipError_t launch_tile(const ProductGroup* groups, int count, const ProductScales& s,
+                       const int32_t* skip, hipStream_t stream, int64_t max_grid) {
+  using T = Tile<MT, WM, WN>;
+  constexpr bool SYM = WHAT == Product::kGram || WHAT == Product::kSquare;
   ProductArgs a = {};
-  const bool symmetric = what == Product::kGram || what == Product::kSquare;
   int64_t total = 0;
   for (int i = 0; i < count; ++i) {
     a.g[i] = groups[i];
-    const int64_t tm = (groups[i].M + 127) / 128, tn = (groups[i].N + 127) / 128;
-    const int64_t tiles = symmetric ? tm * (tm + 1) / 2 : tm * tn;
+    const int64_t tm = (groups[i].M + T::rows - 1) / T::rows;
+    const int64_t tn = (groups[i].N + T::cols - 1) / T::cols;
+    const int64_t tiles = SYM ? tm * (tm + 1) / 2 : tm * tn;
+    a.tiles_m[i] = static_cast<int32_t>(tm);
     a.tiles_n[i] = static_cast<int32_t>(tn);
     a.tiles[i] = static_cast<int32_t>(tiles);
     total += tiles * groups[i].count;
@@ -257,17 +437,44 @@ hipError_t launch_product(const ProductGroup* groups, int count, Product what, i
   a.s = s;
   a.skip = skip;
   a.count = count;
+  int64_t grid = total < kMaxWorkgroups ? total : kMaxWorkgroups;
+  if (grid > max_grid) grid = max_grid;
+  void* params[] = {&a};
+  return hipLaunchKernel(reinterpret_cast<const void*>(&product_kernel<WHAT, OUT, MT, WM, WN>),
+                         dim3(static_cast<unsigned>(grid)), dim3(T::threads), params, 0, stream);
+}
+
+template <Product WHAT, int OUT>
+hipError_t launch_one(const ProductGroup* groups, int count, const ProductScales& s,
+                      const int32_t* skip, hipStream_t stream, int64_t max_grid) {
+  constexpr bool SYM = WHAT == Product::kGram || WHAT == Product::kSquare;
+  int64_t large = 0;
+  for (int i = 0; i < count; ++i) {
+    const int64_t tm = (groups[i].M + 255) / 256, tn = (groups[i].N + 255) / 256;
+    large += (SYM ? tm * (tm + 1) / 2 : tm * tn) * groups[i].count;
+  }
+  static const int force = [] { const char* e = getenv("LA_TILE"); return e ? atoi(e) : 0; }();
+  if (force ? force == 256 : large >= 200)
+    return launch_tile<WHAT, OUT, 4, 2, 4>(groups, count, s, skip, stream, max_grid);
+  return launch_tile<WHAT, OUT, 2, 2, 2>(groups, count, s, skip, stream, max_grid);
+}
+
+}  // namespace
+
+hipError_t launch_product(const ProductGroup* groups, int count, Product what, int out_type,
+                          const ProductScales& s, const int32_t* skip, hipStream_t stream,
+                          int64_t max_grid) {
   switch (what) {
-    case Product::kGram: return launch_one<Product::kGram, 0>(a, total, stream, max_grid);
-    case Product::kSquare: return launch_one<Product::kSquare, 0>(a, total, stream, max_grid);
-    case Product::kUpdate: return launch_one<Product::kUpdate, 0>(a, total, stream, max_grid);
+    case Product::kGram: return launch_one<Product::kGram, 0>(groups, count, s, skip, stream, max_grid);
+    case Product::kSquare: return launch_one<Product::kSquare, 0>(groups, count, s, skip, stream, max_grid);
+    case Product::kUpdate: return launch_one<Product::kUpdate, 0>(groups, count, s, skip, stream, max_grid);
     case Product::kOut:
-      return out_type == kFp16 ? launch_one<Product::kOut, kFp16>(a, total, stream, max_grid)
-                               : launch_one<Product::kOut, kBf16>(a, total, stream, max_grid);
+      return out_type == kFp16 ? launch_one<Product::kOut, kFp16>(groups, count, s, skip, stream, max_grid)
+                               : launch_one<Product::kOut, kBf16>(groups, count, s, skip, stream, max_grid);
     default:
-      return out_type == kFp16   ? launch_one<Product::kMuon, kFp16>(a, total, stream, max_grid)
-             : out_type == kBf16 ? launch_one<Product::kMuon, kBf16>(a, total, stream, max_grid)
-                                 : launch_one<Product::kMuon, -1>(a, total, stream, max_grid);
+      return out_type == kFp16   ? launch_one<Product::kMuon, kFp16>(groups, count, s, skip, stream, max_grid)
+             : out_type == kBf16 ? launch_one<Product::kMuon, kBf16>(groups, count, s, skip, stream, max_grid)
+                                 : launch_one<Product::kMuon, -1>(groups, count, s, skip, stream, max_grid);
   }
 }
 
