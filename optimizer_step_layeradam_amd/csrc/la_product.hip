@@ -6,11 +6,24 @@
 #include <stdlib.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "la_muon.h"
 
 #pragma clang fp contract(off)
 
+#ifndef LA_B2
+#define LA_B2 4
+#endif
+#ifndef LA_NT
+#define LA_NT 4
+#endif
+#ifndef LA_D4
+#define LA_D4 64
+#endif
+#ifndef LA_B4
+#define LA_B4 2
+#endif
 namespace la {
 namespace {
 
@@ -32,10 +45,12 @@ __device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t from, _Float1
       from, (__attribute__((address_space(3))) void*)to, 16, offset, uniform_offset, 0, 0);
 }
 
-// This wave's copies have landed and its reads of LDS are done; so are those
-// of every wave of the workgroup after it.
+// All but the last PENDING of this wave's copies have landed and its reads of
+// LDS are done; so are those of every wave of the workgroup after it.
+template <int PENDING>
 __device__ __forceinline__ void wait_and_meet() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  static_assert(PENDING >= 0 && PENDING < 64, "six bits");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(PENDING) : "memory");
 }
 
 // Orders the wave's own LDS accesses, which lanes exchange data through.
@@ -126,15 +141,26 @@ __device__ __forceinline__ void triangle(int t, int tiles_m, int& i, int& j) {
 // meets the others, so that the next stage's first fragments arrive under
 // these products.
 
-template <int MT, int NT, int WM, int WN>
+template <int MT, int NT, int WM, int WN, int DEPTH, int BUFFERS>
 struct Tile {
   static constexpr int waves = WM * WN;
   static constexpr int threads = 64 * waves;
   static constexpr int rows = 32 * MT * WM, cols = 32 * NT * WN;
-  static constexpr int stage = (rows + cols) * kDepth;  // elements
-  static constexpr int copies = stage * 2 / (threads * 16);
-  static_assert(2 * stage * 2 >= waves * 16384, "the epilogue takes 16 KiB of LDS per wave");
-  static_assert(rows % (8 * waves) == 0 && cols % (8 * waves) == 0, "whole rows per copy");
+  static constexpr int stage = (rows + cols) * DEPTH;  // elements
+  static constexpr int pieces = DEPTH / 8;             // of 16 bytes in a row
+  static constexpr int copy_rows = 64 / pieces;        // rows that one copy of a wave brings
+  static constexpr int p_copies = rows / (copy_rows * waves);
+  static constexpr int q_copies = cols / (copy_rows * waves);
+  static constexpr int in_flight = (BUFFERS - 2) * (p_copies + q_copies);
+  static_assert(BUFFERS * stage * 2 >= waves * 16384, "the epilogue takes 16 KiB of LDS per wave");
+  static_assert(rows % (copy_rows * waves) == 0 && cols % (copy_rows * waves) == 0,
+                "whole rows per copy");
+  static_assert(kDepth % DEPTH == 0 && (DEPTH == 32 || DEPTH == 64), "whole stages");
+  // Where piece p of row r is kept: 64 banks hold 256 bytes, two rows of 128
+  // bytes or four of 64.
+  static __device__ __forceinline__ int slot(int r, int p) {
+    return DEPTH == 64 ? p ^ ((r >> 1) & 7) : p ^ ((r >> 2) & 3);
+  }
 };
 
 template <int MT, int NT>
@@ -267,12 +293,12 @@ __device__ __forceinline__ half8 finish(const ProductGroup& g, const ProductScal
   return h;
 }
 
-template <Product WHAT, int OUT, int MT, int NT, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN) void product_kernel(ProductArgs a) {
-  using T = Tile<MT, NT, WM, WN>;
+template <Product WHAT, int OUT, int MT, int NT, int WM, int WN, int DEPTH, int BUFFERS>
+__global__ __launch_bounds__(64 * WM * WN, MT * NT == 8 ? 2 : 1) void product_kernel(ProductArgs a) {
+  using T = Tile<MT, NT, WM, WN, DEPTH, BUFFERS>;
   constexpr bool SYM = WHAT == Product::kGram || WHAT == Product::kSquare;
   constexpr bool TURN = SYM || WHAT == Product::kUpdate;
-  __shared__ __align__(1024) _Float16 lds[2 * T::stage];
+  __shared__ __align__(1024) _Float16 lds[BUFFERS * T::stage];
   if (a.skip != nullptr && *a.skip != 0) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -292,8 +318,7 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(ProductArgs a) {
     else rectangle(t, a.tiles_m[gi], a.tiles_n[gi], ti, tj);
     const int row0 = ti * T::rows, col0 = tj * T::cols;
 
-    // Copy c of a stage brings 8 rows per wave, one 16-byte piece per lane. A
-    // row past the matrix is its last one again: its results are not kept.
+    // A row past the matrix is its last one again: its results are not kept.
     // Offsets are 32 bits from the tile's first row (at most 256 rows of 2
     // MiB).
     const int64_t p_first = static_cast<int64_t>(z) * g.p_stride + static_cast<int64_t>(row0) * g.ldp;
@@ -302,43 +327,38 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(ProductArgs a) {
         const_cast<half_bits*>(g.p + p_first), 0, kRsrcRange, kRsrcWord3);
     const __amdgpu_buffer_rsrc_t rq = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<half_bits*>(g.q + q_first), 0, kRsrcRange, kRsrcWord3);
-    constexpr int PC = T::rows / (8 * T::waves), QC = T::cols / (8 * T::waves);
-    int po[PC], qo[QC];
-#pragma unroll
-    for (int c = 0; c < PC; ++c) {
-      const int r = (c * T::waves + wave) * 8 + (lane >> 3);
-      const int most = g.M - 1 - row0;
-      po[c] = (r < most ? r : most) * g.ldp * 2 + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
-    }
-#pragma unroll
-    for (int c = 0; c < QC; ++c) {
-      const int r = (c * T::waves + wave) * 8 + (lane >> 3);
-      const int most = g.N - 1 - col0;
-      qo[c] = (r < most ? r : most) * g.ldq * 2 + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
-    }
-    auto copy = [&](int k) {
-      _Float16* to = lds + (k & 1) * T::stage + wave * 8 * kDepth;
-#pragma unroll
-      for (int c = 0; c < PC; ++c)
-        copy_to_lds(rp, to + c * T::waves * 8 * kDepth, po[c], k * kDepth * 2);
-      to += T::rows * kDepth;
-#pragma unroll
-      for (int c = 0; c < QC; ++c)
-        copy_to_lds(rq, to + c * T::waves * 8 * kDepth, qo[c], k * kDepth * 2);
+    int po[T::p_copies], qo[T::q_copies];
+    auto offset = [&](int c, int most, int ld) {
+      const int r = (c * T::waves + wave) * T::copy_rows + lane / T::pieces;
+      return (r < most ? r : most) * ld * 2 + (T::slot(r, lane % T::pieces) << 4);
     };
-    auto read = [&](Fragments<MT, NT>& f, int k, int step) {
-      const _Float16* from = lds + (k & 1) * T::stage;
+#pragma unroll
+    for (int c = 0; c < T::p_copies; ++c) po[c] = offset(c, g.M - 1 - row0, g.ldp);
+#pragma unroll
+    for (int c = 0; c < T::q_copies; ++c) qo[c] = offset(c, g.N - 1 - col0, g.ldq);
+    // copies [from, to) of stage k
+    auto copy = [&](int k, int buffer, int from, int to) {
+      _Float16* base = lds + buffer * T::stage + wave * T::copy_rows * DEPTH;
+#pragma unroll
+      for (int c = from; c < to; ++c) {
+        const bool p = c < T::p_copies;
+        copy_to_lds(p ? rp : rq, base + c * T::waves * T::copy_rows * DEPTH,
+                    p ? po[p ? c : 0] : qo[p ? 0 : c - T::p_copies], k * DEPTH * 2);
+      }
+    };
+    auto read = [&](Fragments<MT, NT>& f, int buffer, int step) {
+      const _Float16* from = lds + buffer * T::stage;
       const int piece = 2 * step + (lane >> 5);
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         const int r = wm + 32 * i + (lane & 31);
-        f.p[i] = *reinterpret_cast<const half8*>(from + r * kDepth + ((piece ^ ((r >> 1) & 7)) << 3));
+        f.p[i] = *reinterpret_cast<const half8*>(from + r * DEPTH + (T::slot(r, piece) << 3));
       }
-      from += T::rows * kDepth;
+      from += T::rows * DEPTH;
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         const int r = wn + 32 * j + (lane & 31);
-        f.q[j] = *reinterpret_cast<const half8*>(from + r * kDepth + ((piece ^ ((r >> 1) & 7)) << 3));
+        f.q[j] = *reinterpret_cast<const half8*>(from + r * DEPTH + (T::slot(r, piece) << 3));
       }
     };
     f32x16 acc[MT][NT] = {};
@@ -350,33 +370,91 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(ProductArgs a) {
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.p[i], f.q[j], acc[i][j], 0, 0, 0);
     };
 
-    // one read of LDS under every MT NT / (MT + NT) products
-    auto interleave = [&] {
+    // Deals a step's reads of LDS, and behind them `copies` copies, out among
+    // its products: a wave that issues its copies in a row waits for the
+    // address unit, and its products behind them (measured: 29 % of the time).
+    auto interleave = [&](auto copies) {
+      constexpr int reads = MT + NT, products = MT * NT, n = decltype(copies)::value;
+      constexpr int each = n > 0 ? 1 : products / reads;
+      if constexpr (products >= reads + n) {
 #pragma unroll
-      for (int i = 0; i < MT + NT; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                   // LDS read
-        __builtin_amdgcn_sched_group_barrier(0x008, MT * NT / (MT + NT), 0);  // MFMA
+        for (int i = 0; i < reads; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);     // LDS read
+          __builtin_amdgcn_sched_group_barrier(0x008, each, 0);  // MFMA
+        }
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);  // copy
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        }
+        if constexpr (n > 0) __builtin_amdgcn_sched_group_barrier(0x008, products - reads - n, 0);
       }
+      __builtin_amdgcn_sched_barrier(0);
     };
-    const int stages = g.K / kDepth;
-    Fragments<MT, NT> f0, f1;
-    copy(0);
-    wait_and_meet();
-    read(f0, 0, 0);
-    for (int k = 0; k < stages; ++k) {
-      if (k + 1 < stages) copy(k + 1);
-      read(f1, k, 1);
-      multiply(f0);
-      interleave();
-      read(f0, k, 2);
-      multiply(f1);
-      interleave();
-      read(f1, k, 3);
-      multiply(f0);
-      interleave();
-      wait_and_meet();
-      if (k + 1 < stages) read(f0, k + 1, 0);
-      multiply(f1);
+    constexpr int ALL = T::p_copies + T::q_copies;
+    constexpr int A = (ALL + 2) / 3, B = (ALL - A + 1) / 2, C = ALL - A - B;
+    using Acopies = std::integral_constant<int, A>;
+    using Bcopies = std::integral_constant<int, B>;
+    using Ccopies = std::integral_constant<int, C>;
+    using None = std::integral_constant<int, 0>;
+    const int stages = g.K / DEPTH;
+    Fragments<MT, NT> f[2];
+    if constexpr (BUFFERS == 2) {
+      // Stage k + 2 takes stage k's buffer: its copies start behind the meeting
+      // after stage k's last reads, under the last products of stage k, and go
+      // on under the first half of stage k + 1. The loop has no branch that
+      // would part the products: past the end the last stage is copied again,
+      // into a buffer that nobody reads.
+      auto stage = [&](int k) { return k < stages ? k : stages - 1; };
+      copy(0, 0, 0, ALL);
+      wait_and_meet<0>();
+      read(f[0], 0, 0);
+      copy(stage(1), 1, 0, A);
+      for (int k = 0; k < stages; ++k) {
+        const int b = k & 1;
+        read(f[1], b, 1);
+        copy(stage(k + 1), b ^ 1, A, A + B);
+        multiply(f[0]);
+        interleave(Bcopies());
+        read(f[0], b, 2);
+        copy(stage(k + 1), b ^ 1, A + B, ALL);
+        multiply(f[1]);
+        interleave(Ccopies());
+        read(f[1], b, 3);
+        multiply(f[0]);
+        interleave(None());
+        wait_and_meet<0>();
+        read(f[0], b ^ 1, 0);
+        copy(stage(k + 2), b, 0, A);
+        multiply(f[1]);
+        interleave(Acopies());
+      }
+      wait_and_meet<0>();
+    } else {
+#pragma unroll
+      for (int k = 0; k < BUFFERS - 1; ++k)
+        if (k < stages) copy(k, k, 0, ALL);
+      if (stages >= BUFFERS - 1) wait_and_meet<T::in_flight>();
+      else wait_and_meet<0>();
+      read(f[0], 0, 0);
+      int buffer = 0;
+      for (int k = 0; k < stages; ++k) {
+        const int next = buffer + 1 == BUFFERS ? 0 : buffer + 1;
+        const int last = buffer == 0 ? BUFFERS - 1 : buffer - 1;
+        const bool more = k + BUFFERS - 1 < stages;
+        if (more) copy(k + BUFFERS - 1, last, 0, ALL);
+#pragma unroll
+        for (int step = 1; step < DEPTH / 16; ++step) {
+          read(f[step & 1], buffer, step);
+          multiply(f[(step - 1) & 1]);
+          interleave(None());
+        }
+        if (more) wait_and_meet<T::in_flight>();
+        else wait_and_meet<0>();
+        if (k + 1 < stages) read(f[0], next, 0);
+        multiply(f[1]);
+        buffer = next;
+      }
     }
     // every wave is past its last read of LDS: the last wait_and_meet
 
@@ -457,14 +535,14 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(ProductArgs a) {
         wave_fence();
       }
     }
-    __syncthreads();  // LDS is free for the next tile
+    wait_and_meet<0>();  // LDS is free for the next tile, and no store is counted with its copies
   }
 }
 
-template <Product WHAT, int OUT, int MT, int NT, int WM, int WN>
+template <Product WHAT, int OUT, int MT, int NT, int WM, int WN, int DEPTH, int BUFFERS>
 hipError_t launch_tile(const ProductGroup* groups, int count, const ProductScales& s,
                        const int32_t* skip, hipStream_t stream, int64_t max_grid) {
-  using T = Tile<MT, NT, WM, WN>;
+  using T = Tile<MT, NT, WM, WN, DEPTH, BUFFERS>;
   constexpr bool SYM = WHAT == Product::kGram || WHAT == Product::kSquare;
   // The tiles of the longest sums first: the short ones fill the last round's
   // gaps (the 14B-shaped layer's X X^T: 2.05 -> 1.4 ms).
@@ -491,7 +569,7 @@ hipError_t launch_tile(const ProductGroup* groups, int count, const ProductScale
   int64_t grid = total < kMaxWorkgroups ? total : kMaxWorkgroups;
   if (grid > max_grid) grid = max_grid;
   void* params[] = {&a};
-  return hipLaunchKernel(reinterpret_cast<const void*>(&product_kernel<WHAT, OUT, MT, NT, WM, WN>),
+  return hipLaunchKernel(reinterpret_cast<const void*>(&product_kernel<WHAT, OUT, MT, NT, WM, WN, DEPTH, BUFFERS>),
                          dim3(static_cast<unsigned>(grid)), dim3(T::threads), params, 0, stream);
 }
 
@@ -505,9 +583,12 @@ hipError_t launch_one(const ProductGroup* groups, int count, const ProductScales
     large += (SYM ? tm * (tm + 1) / 2 : tm * tn) * groups[i].count;
   }
   static const int force = [] { const char* e = getenv("LA_TILE"); return e ? atoi(e) : 0; }();
-  if (force ? force == 256 : large >= 200)
-    return launch_tile<WHAT, OUT, 4, 4, 2, 2>(groups, count, s, skip, stream, max_grid);
-  return launch_tile<WHAT, OUT, 2, 2, 2, 2>(groups, count, s, skip, stream, max_grid);
+  if (force ? force == 256 : large >= 200) {
+    constexpr int MT = 4, NT = SYM ? 4 : LA_NT;
+    return launch_tile<WHAT, OUT, MT, NT, 2, 2, NT == 4 ? LA_D4 : 32, NT == 4 ? LA_B4 : 3>(
+        groups, count, s, skip, stream, max_grid);
+  }
+  return launch_tile<WHAT, OUT, 2, 2, 2, 2, 64, LA_B2>(groups, count, s, skip, stream, max_grid);
 }
 
 }  // namespace
