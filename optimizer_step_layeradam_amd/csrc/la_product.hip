@@ -31,6 +31,7 @@ typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // Raw buffer resource over a uniform base: no stride, 2 GiB of range, the
 // fourth word of a 32-bit-format buffer.
@@ -168,6 +169,17 @@ struct Fragments {
   half8 p[MT], q[NT];
 };
 
+// x y + z in one rounding: where the terms are converted from binary16 it is one
+// instruction for both.
+__device__ __forceinline__ float fma(float x, float y, float z) {
+  return __builtin_fmaf(x, y, z);
+}
+
+// `mask` over the bits of eight binary16 numbers.
+__device__ __forceinline__ half8 keep(half8 h, u32x4 mask) {
+  return __builtin_bit_cast(half8, __builtin_bit_cast(u32x4, h) & mask);
+}
+
 // What the epilogue reads for eight neighbours of one row: loaded ahead of the
 // sums' exchange, so that its latency is paid once for four rows of a lane.
 template <Product WHAT>
@@ -206,34 +218,36 @@ __device__ __forceinline__ void load_operands(Operands<WHAT>& x, const ProductGr
 
 // Eight results of one row from their sums: what is kept of them in binary16
 // (zero outside the matrix), after what the epilogue stores itself. dc: the
-// diagonal along the columns (kSquare; the others where g.tall).
+// diagonal along the columns (kSquare; the others where g.tall); mask: the
+// columns inside the matrix.
 template <Product WHAT, int OUT>
 __device__ __forceinline__ half8 finish(const ProductGroup& g, const ProductScales& s, int z,
                                         int row, int col, const float (&sum)[8],
-                                        const Operands<WHAT>& x, const float (&dc)[8]) {
+                                        const Operands<WHAT>& x, const float (&dc)[8],
+                                        u32x4 mask) {
   const bool row_in = row < g.M;
   const int64_t at = z * g.c_stride + static_cast<int64_t>(row) * g.ldc + col;
-  half8 h = {};
-  if constexpr (WHAT == Product::kGram) {
+  half8 h;
+  if constexpr (WHAT == Product::kGram || WHAT == Product::kSquare) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float v = sum[e] * s.acc;
-      if (row_in && col + e < g.N) {
-        if (row == col + e) g.diag_out[z * g.diag_stride + row] = v;
-        else h[e] = static_cast<_Float16>(v);
-      }
+      if constexpr (WHAT == Product::kGram)
+        h[e] = static_cast<_Float16>(sum[e] * s.acc);
+      else
+        h[e] = static_cast<_Float16>(fma(fma(s.diag, x.diag + dc[e], s.linear),
+                                         static_cast<float>(x.hi[e]), s.acc * sum[e]));
     }
-  } else if constexpr (WHAT == Product::kSquare) {
+    if (row_in && row >= col && row < col + 8) {  // the lane that holds a diagonal element
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (row_in && col + e < g.N) {
-        if (row == col + e)
-          g.diag_out[z * g.diag_stride + row] =
-              (s.linear * x.diag + (s.diag * (x.diag * x.diag) + s.acc * sum[e])) * s.out;
-        else
-          h[e] = static_cast<_Float16>((s.linear + s.diag * (x.diag + dc[e])) *
-                                           static_cast<float>(x.hi[e]) + s.acc * sum[e]);
-      }
+      for (int e = 0; e < 8; ++e)
+        if (row == col + e) {
+          if constexpr (WHAT == Product::kGram)
+            g.diag_out[z * g.diag_stride + row] = sum[e] * s.acc;
+          else
+            g.diag_out[z * g.diag_stride + row] =
+                (s.linear * x.diag + (s.diag * (x.diag * x.diag) + s.acc * sum[e])) * s.out;
+          h[e] = static_cast<_Float16>(0.0f);
+        }
     }
   } else if constexpr (WHAT == Product::kUpdate) {
     half8 l;
@@ -241,9 +255,9 @@ __device__ __forceinline__ half8 finish(const ProductGroup& g, const ProductScal
     for (int e = 0; e < 8; ++e) {
       const float hi = static_cast<float>(x.hi[e]);
       const float d = s.diag * (g.tall ? dc[e] : x.diag);
-      const float v = s.linear * (hi + static_cast<float>(x.lo[e]) * 0x1p-11f) +
-                      (d * hi + s.acc * sum[e]);
-      if (row_in && col + e < g.N) h[e] = static_cast<_Float16>(v);
+      const float v = fma(s.linear, fma(static_cast<float>(x.lo[e]), 0x1p-11f, hi),
+                          fma(d, hi, s.acc * sum[e]));
+      h[e] = static_cast<_Float16>(v);
       l[e] = static_cast<_Float16>((v - static_cast<float>(h[e])) * 0x1p11f);
     }
     if (g.c_lo != nullptr && row_in && col < g.ldc)
@@ -255,7 +269,7 @@ __device__ __forceinline__ half8 finish(const ProductGroup& g, const ProductScal
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float d = s.diag * (g.tall ? dc[e] : x.diag);
-      v[e] = (s.linear + d) * static_cast<float>(x.hi[e]) + s.acc * sum[e];
+      v[e] = fma(s.linear + d, static_cast<float>(x.hi[e]), s.acc * sum[e]);
       if constexpr (WHAT == Product::kMuon)
         v[e] = x.master[e >> 2][e & 3] * s.decay - g.step * v[e];
       w[e] = OUT == kBf16 ? bf16_bits(v[e]) : fp16_bits(v[e]);
@@ -287,10 +301,13 @@ __device__ __forceinline__ half8 finish(const ProductGroup& g, const ProductScal
     }
   }
   if constexpr (WHAT == Product::kGram || WHAT == Product::kSquare || WHAT == Product::kUpdate) {
+    const uint32_t r = row_in ? ~0u : 0u;
+    h = keep(h, mask & u32x4{r, r, r, r});
     if (row_in && col < g.ldc)
       *reinterpret_cast<half8*>(reinterpret_cast<_Float16*>(g.c) + at) = h;
+    return h;
   }
-  return h;
+  return half8{};
 }
 
 template <Product WHAT, int OUT, int MT, int NT, int WM, int WN, int DEPTH, int BUFFERS>
@@ -376,19 +393,18 @@ __global__ __launch_bounds__(64 * WM * WN, MT * NT == 8 ? 2 : 1) void product_ke
     auto interleave = [&](auto copies) {
       constexpr int reads = MT + NT, products = MT * NT, n = decltype(copies)::value;
       constexpr int each = n > 0 ? 1 : products / reads;
-      if constexpr (products >= reads + n) {
 #pragma unroll
-        for (int i = 0; i < reads; ++i) {
-          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);     // LDS read
-          __builtin_amdgcn_sched_group_barrier(0x008, each, 0);  // MFMA
-        }
-#pragma unroll
-        for (int i = 0; i < n; ++i) {
-          __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);  // copy
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        }
-        if constexpr (n > 0) __builtin_amdgcn_sched_group_barrier(0x008, products - reads - n, 0);
+      for (int i = 0; i < reads; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);     // LDS read
+        __builtin_amdgcn_sched_group_barrier(0x008, each, 0);  // MFMA
       }
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);  // copy
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      }
+      if constexpr (n > 0 && products > reads + n)
+        __builtin_amdgcn_sched_group_barrier(0x008, products - reads - n, 0);
       __builtin_amdgcn_sched_barrier(0);
     };
     constexpr int ALL = T::p_copies + T::q_copies;
@@ -467,7 +483,9 @@ __global__ __launch_bounds__(64 * WM * WN, MT * NT == 8 ? 2 : 1) void product_ke
     _Float16* turn = reinterpret_cast<_Float16*>(sums + 2048);
     const bool mirror = TURN && (!SYM || ti != tj);
     const int k8 = (lane & 7) * 8;
-    constexpr int AHEAD = MT * NT > 4 ? 1 : 2;  // halves of a part whose operands are held
+    // halves of a part whose operands are held: both, but for kMuon's twelve
+    // registers a row in the large tile
+    constexpr int AHEAD = MT * NT > 4 && WHAT == Product::kMuon ? 1 : 2;
 #pragma unroll
     for (int part = 0; part < MT * NT / 4; ++part) {
       const int ci = part % (MT / 2), cj = part / (MT / 2);
@@ -480,6 +498,12 @@ __global__ __launch_bounds__(64 * WM * WN, MT * NT == 8 ? 2 : 1) void product_ke
           *reinterpret_cast<f32x4*>(dc) = d[0];
           *reinterpret_cast<f32x4*>(dc + 4) = d[1];
         }
+      }
+      u32x4 mask;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = colw + k8 + 2 * e;
+        mask[e] = c + 1 < g.N ? ~0u : c < g.N ? 0xFFFFu : 0u;
       }
       Operands<WHAT> x[AHEAD][4];
       auto load = [&](int hf) {
@@ -508,7 +532,7 @@ __global__ __launch_bounds__(64 * WM * WN, MT * NT == 8 ? 2 : 1) void product_ke
           *reinterpret_cast<f32x4*>(v) = *reinterpret_cast<const f32x4*>(from);
           *reinterpret_cast<f32x4*>(v + 4) = *reinterpret_cast<const f32x4*>(from + 4);
           const half8 h = finish<WHAT, OUT>(g, a.s, z, rowc + 32 * hf + r, colw + k8, v,
-                                            x[hf % AHEAD][p], dc);
+                                            x[hf % AHEAD][p], dc, mask);
           if constexpr (TURN) {
             const int rr = 32 * hf + r;
             *reinterpret_cast<half8*>(turn + rr * 64 + (((lane & 7) ^ ((rr >> 3) & 7)) << 3)) = h;
@@ -584,9 +608,9 @@ hipError_t launch_one(const ProductGroup* groups, int count, const ProductScales
   }
   static const int force = [] { const char* e = getenv("LA_TILE"); return e ? atoi(e) : 0; }();
   if (force ? force == 256 : large >= 200) {
-    constexpr int MT = 4, NT = SYM ? 4 : LA_NT;
-    return launch_tile<WHAT, OUT, MT, NT, 2, 2, NT == 4 ? LA_D4 : 32, NT == 4 ? LA_B4 : 3>(
-        groups, count, s, skip, stream, max_grid);
+    static const int w8 = [] { const char* e = getenv("LA_W8"); return e ? atoi(e) : 0; }();
+    if (w8) return launch_tile<WHAT, OUT, 4, 2, 2, 4, 64, 2>(groups, count, s, skip, stream, max_grid);
+    return launch_tile<WHAT, OUT, 4, 4, 2, 2, 64, 2>(groups, count, s, skip, stream, max_grid);
   }
   return launch_tile<WHAT, OUT, 2, 2, 2, 2, 64, LA_B2>(groups, count, s, skip, stream, max_grid);
 }
