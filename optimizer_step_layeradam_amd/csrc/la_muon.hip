@@ -257,11 +257,10 @@ __global__ __launch_bounds__(kThreads) void normalise_kernel(DirectionArgs a) {
             static_cast<double>(element<TYPE>(g.in, z * g.matrix_stride + r * g.row_stride + c)) *
             factor);
       const _Float16 hi = static_cast<_Float16>(x);
-      const _Float16 lo = static_cast<_Float16>((x - static_cast<float>(hi)) * 0x1p11f);
       if (r < g.rows) {
         const int64_t at = (z * g.rows + r) * g.ld_straight + c;
         reinterpret_cast<_Float16*>(g.straight)[at] = hi;
-        reinterpret_cast<_Float16*>(g.straight_lo)[at] = lo;
+        g.straight_lo[at] = static_cast<int8_t>(low_byte(x, hi));
       }
       turn[rx][cx] = hi;
     }

@@ -169,12 +169,12 @@ int64_t lay_out(std::vector<Stack>& stacks, int steps, bool direction, bool cont
     }
     const int64_t k = s.count;
     s.straight[0] = take(2 * k * s.numel_straight);
-    s.straight_lo[0] = take(2 * k * s.numel_straight);
+    s.straight_lo[0] = take(k * s.numel_straight);
     s.turned[0] = take(2 * k * s.numel_turned);
     const int64_t second = at;
     if (steps > 1) {
       s.straight[1] = take(2 * k * s.numel_straight);
-      if (steps > 2) s.straight_lo[1] = take(2 * k * s.numel_straight);
+      if (steps > 2) s.straight_lo[1] = take(k * s.numel_straight);
       s.turned[1] = take(2 * k * s.numel_turned);
     }
     s.direction = second;
@@ -247,13 +247,13 @@ la_status enqueue_products(const std::vector<Stack>& stacks, const Polynomial& p
           x.M = static_cast<int32_t>(s.rows);
           x.N = static_cast<int32_t>(s.cols);
           x.hi = straight;
-          x.lo = place<uint16_t>(ws, s.straight_lo[now]);
+          x.lo = place<int8_t>(ws, s.straight_lo[now]);
           x.ldc = static_cast<int32_t>(s.ld_straight);
           x.c_stride = s.numel_straight;
           if (what == la::Product::kUpdate) {
             x.c = place<uint16_t>(ws, s.straight[then]);
             // the last step reads hi alone
-            x.c_lo = k + 2 < p.steps ? place<uint16_t>(ws, s.straight_lo[then]) : nullptr;
+            x.c_lo = k + 2 < p.steps ? place<int8_t>(ws, s.straight_lo[then]) : nullptr;
             x.turned = place<uint16_t>(ws, s.turned[then]);
             x.ld_turned = static_cast<int32_t>(s.ld_turned);
             x.turned_stride = s.numel_turned;
@@ -293,7 +293,7 @@ la::DirectionGroup direction_group(const Stack& s, void* ws) {
   la::DirectionGroup d = {};
   d.partial = place<double>(ws, s.partial);
   d.straight = place<uint16_t>(ws, s.straight[0]);
-  d.straight_lo = place<uint16_t>(ws, s.straight_lo[0]);
+  d.straight_lo = place<int8_t>(ws, s.straight_lo[0]);
   d.turned = place<uint16_t>(ws, s.turned[0]);
   d.rows = static_cast<int32_t>(s.rows);
   d.cols = static_cast<int32_t>(s.cols);

@@ -31,6 +31,7 @@ typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // Raw buffer resource over a uniform base: no stride, 2 GiB of range, the
@@ -185,7 +186,7 @@ __device__ __forceinline__ half8 keep(half8 h, u32x4 mask) {
 template <Product WHAT>
 struct Operands {
   half8 hi;          // all but kGram
-  half8 lo;          // kUpdate
+  u32x2 lo;          // kUpdate
   f32x4 master[2];   // kMuon
   float diag;        // the row's
 };
@@ -199,7 +200,7 @@ __device__ __forceinline__ void load_operands(Operands<WHAT>& x, const ProductGr
     const int64_t at = z * g.c_stride + static_cast<int64_t>(r) * g.ldc + c;
     x.hi = *reinterpret_cast<const half8*>(reinterpret_cast<const _Float16*>(g.hi) + at);
     if constexpr (WHAT == Product::kUpdate)
-      x.lo = *reinterpret_cast<const half8*>(reinterpret_cast<const _Float16*>(g.lo) + at);
+      x.lo = *reinterpret_cast<const u32x2*>(g.lo + at);
     if (WHAT == Product::kSquare || !g.tall) x.diag = g.diag[z * g.diag_stride + r];
     if constexpr (WHAT == Product::kMuon) {
       if (row < g.M && col < g.N) {
@@ -250,18 +251,18 @@ __device__ __forceinline__ half8 finish(const ProductGroup& g, const ProductScal
         }
     }
   } else if constexpr (WHAT == Product::kUpdate) {
-    half8 l;
+    u32x2 l = {};
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float hi = static_cast<float>(x.hi[e]);
+      const int lo = static_cast<int>(x.lo[e >> 2] << (24 - 8 * (e & 3))) >> 24;
       const float d = s.diag * (g.tall ? dc[e] : x.diag);
-      const float v = fma(s.linear, fma(static_cast<float>(x.lo[e]), 0x1p-11f, hi),
-                          fma(d, hi, s.acc * sum[e]));
+      const float v = fma(s.linear, with_low_byte(hi, lo), fma(d, hi, s.acc * sum[e]));
       h[e] = static_cast<_Float16>(v);
-      l[e] = static_cast<_Float16>((v - static_cast<float>(h[e])) * 0x1p11f);
+      l[e >> 2] |= (static_cast<uint32_t>(low_byte(v, h[e])) & 0xFFu) << (8 * (e & 3));
     }
     if (g.c_lo != nullptr && row_in && col < g.ldc)
-      *reinterpret_cast<half8*>(reinterpret_cast<_Float16*>(g.c_lo) + at) = l;
+      *reinterpret_cast<u32x2*>(g.c_lo + at) = l;
   } else if (row_in && col < g.N) {
     const bool whole = g.vectors && col + 8 <= g.N;
     float v[8];
