@@ -326,8 +326,10 @@ LA_API la_status la_direction_probe(const la_layer_desc *layer, int32_t part,
  * upper 11 bits with FP32 sums. O is within about 0.2 % (2-norm of the
  * difference over 2-norm of O, default coefficients) of the polynomial in
  * FP64, also for matrices of low rank or of a wide range of singular
- * values. Results do not depend on the launch: the same inputs give the
- * same bits. A zero matrix gives zeros; a matrix holding an Inf or NaN gives
+ * values. The same call with the same inputs gives the same bits. Matrices
+ * with a short side of up to 128 can take another form of the same
+ * polynomial, and which one they take may depend on the call's other
+ * matrices. A zero matrix gives zeros; a matrix holding an Inf or NaN gives
  * NaN everywhere.
  *
  * Memory. The caller passes a workspace (la_orthogonalize_workspace_bytes,

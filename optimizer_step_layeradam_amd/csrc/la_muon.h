@@ -142,6 +142,52 @@ hipError_t launch_product(const ProductGroup* groups, int count, Product what, i
                           const ProductScales& s, const int32_t* skip, hipStream_t stream,
                           int64_t max_grid);
 
+// ---- narrow matrices ---------------------------------------------------------------
+
+// Matrices whose short side is at most this take the iteration on S = X X^T.
+constexpr int kNarrow = 128;
+
+// Steps of a polynomial at most (LA_MAX_POLYNOMIAL_STEPS).
+constexpr int kMaxSteps = 16;
+
+// One stack of narrow matrices.
+struct NarrowGroup {
+  const void* in;           // directions, rows x cols
+  double* partial;          // count x partials sums of squares, or null: formed here
+  float* gram;              // count x splits partial sums of S, in the accumulators' order
+  half_bits* q;             // count x (hi, lo) of the polynomial's factor
+  void* out;                // result, or the compute copy or null
+  float* master;            // the Muon step; null: the result goes to out
+  int64_t row_stride, matrix_stride, out_row_stride, out_matrix_stride;
+  int32_t rows, cols, count;
+  int32_t partials;
+  int32_t splits, chunk;    // columns of one part of the sum, a multiple of 64
+  float step;               // lr times the stack's scale
+};
+
+struct NarrowStep {
+  float a, b, c;
+  int32_t s, p, t, q;  // exponents of the scales of S, P = a + b S + c S S, P S and Q = P ... P
+};
+
+// kWhole: all of it, one workgroup per matrix; kSum, kFactor, kApply: its
+// three parts, with as many workgroups as there is work for.
+enum class NarrowPart { kWhole, kSum, kFactor, kApply };
+
+struct NarrowPlan {
+  NarrowStep step[kMaxSteps];
+  int32_t steps;
+  int32_t x;        // exponent of the scale of X
+  double eps;
+  float decay;
+  int32_t out_type; // kBf16, kFp16, -1: none
+};
+
+// side: 64 or 128, at least every group's short side.
+hipError_t launch_narrow(const NarrowGroup* groups, int count, int side, int type,
+                         NarrowPart part, const NarrowPlan& plan, const int32_t* skip,
+                         hipStream_t stream, int64_t max_grid);
+
 // The byte that follows hi = binary16(x). Where hi is below the format's normal
 // range the byte saturates: the error stays under half of hi's spacing there,
 // 2^-25 of the scaled value.

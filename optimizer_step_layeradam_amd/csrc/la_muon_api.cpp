@@ -35,12 +35,15 @@ constexpr double kDefaultEps = 1e-7;
 struct Step {
   double a, b, c;
   int x, gram, poly;  // exponents of the scales of X, A and B
+  // narrow form: of P = a + b S + c S S, of P S and of Q, the product of the P
+  int factor, turn, whole;
 };
 
 struct Polynomial {
   Step step[LA_MAX_POLYNOMIAL_STEPS];
   int steps;
   double eps;
+  double growth;  // bound of Q after the last step
 };
 
 // Smallest e with x <= 2^e.
@@ -66,6 +69,7 @@ la_status derive_polynomial(const la_polynomial* p, Polynomial* out) {
   out->eps = p == nullptr ? kDefaultEps : p->eps;
   if (!finite_nonneg(out->eps)) return fail(LA_ERR_INVALID_ARGUMENT, "eps = %g", out->eps);
   double s = 1.0;
+  out->growth = 1.0;
   for (int k = 0; k < steps; ++k) {
     const double* t = p == nullptr ? kDefault : p->coefficients + 3 * k;
     const double a = t[0], b = t[1], c = t[2];
@@ -73,11 +77,15 @@ la_status derive_polynomial(const la_polynomial* p, Polynomial* out) {
       return fail(LA_ERR_INVALID_ARGUMENT, "coefficients of step %d: (%g, %g, %g)", k, a, b, c);
     auto value = [&](double q) { return std::fabs((a + (b + c * q) * q) * std::sqrt(q)); };
     auto inner = [&](double q) { return std::fabs((b + c * q) * q); };
+    auto whole = [&](double q) { return std::fabs(a + (b + c * q) * q); };
     const double end = s * s;
-    double next = value(end), poly = inner(end);
+    double next = value(end), poly = inner(end), factor = std::max(std::fabs(a), whole(end));
     if (c != 0.0) {
       const double q = -b / (2.0 * c);
-      if (q > 0.0 && q < end) poly = std::max(poly, inner(q));
+      if (q > 0.0 && q < end) {
+        poly = std::max(poly, inner(q));
+        factor = std::max(factor, whole(q));
+      }
     }
     // a + 3 b q + 5 c q^2 = 0 at the inner extremes
     auto extreme = [&](double q) {
@@ -96,8 +104,16 @@ la_status derive_polynomial(const la_polynomial* p, Polynomial* out) {
       return fail(LA_ERR_INVALID_ARGUMENT,
                   "step %d: the polynomial reaches %g (its inner part %g) on [0, %g]", k, next,
                   poly, s);
-    out->step[k] = {a, b, c, 14 - exponent(s), 14 - exponent(end),
-                    14 - exponent(std::max(poly, 0x1p-20))};
+    out->growth *= factor * 1.01;
+    out->step[k] = {a,
+                    b,
+                    c,
+                    14 - exponent(s),
+                    14 - exponent(end),
+                    14 - exponent(std::max(poly, 0x1p-20)),
+                    14 - exponent(factor * 1.01),
+                    14 - exponent(factor * end * 1.01),
+                    14 - exponent(out->growth)};
     s = next * 1.01;
   }
   return LA_OK;
@@ -118,7 +134,44 @@ struct Stack {
   int32_t partials;
   int64_t chunk, rows_per_partial;
   int index;  // in the caller's list
+  // the narrow form
+  bool narrow, whole;  // whole: one workgroup per matrix does everything
+  int side;
+  int64_t splits, columns;  // parts of the long side, and columns in each
+  int64_t sums, factors;
 };
+
+// A factor Q that reaches past this leaves its 22 bits too coarse beside the
+// singular values near 1, whose factor is about 1 (the default polynomial
+// reaches 490): such polynomials take the step-by-step form everywhere.
+constexpr double kMostGrowth = 512.0;
+
+// Up to this many columns one workgroup does a narrow matrix alone, from its
+// norm to its result, and so it does where there are matrices enough to fill
+// the GPU. Beyond, the sum over the columns and the last product are cut into
+// about kParts parts.
+constexpr int64_t kWholeColumns = 512;
+constexpr int64_t kWholeCount = 512;
+constexpr int64_t kParts = 512;
+
+// Beside wide stacks, whose launches it can share, a narrow stack of fewer
+// elements than this does not get launches of its own (a layer of 256 x 256,
+// 2 of 256 x 64 and 688 x 256: 183 us in shared launches, 258 us apart; 40 of
+// 128 x 5120 apart: 880 -> 479 us).
+constexpr int64_t kOwnLaunches = int64_t(1) << 22;
+
+void choose_form(Stack& s, const Polynomial& p, bool beside_wide) {
+  s.m = std::min(s.rows, s.cols);
+  s.n = std::max(s.rows, s.cols);
+  s.narrow = s.m <= la::kNarrow && p.growth <= kMostGrowth &&
+             (!beside_wide || s.rows * s.cols * s.count >= kOwnLaunches);
+  if (!s.narrow) return;
+  s.side = s.m <= 64 ? 64 : 128;
+  s.whole = s.n <= kWholeColumns || s.count >= kWholeCount;
+  s.splits = std::min((kParts + s.count - 1) / s.count, (s.n + 255) / 256);
+  s.columns = round_up((s.n + s.splits - 1) / s.splits, 64);
+  s.splits = (s.n + s.columns - 1) / s.columns;
+}
 
 la_status check_sides(int i, int64_t rows, int64_t cols, int64_t count) {
   if (rows < 0 || cols < 0 || count < 0 || rows > LA_MAX_SIDE || cols > LA_MAX_SIDE ||
@@ -137,20 +190,22 @@ la_status check_sides(int i, int64_t rows, int64_t cols, int64_t count) {
 // Lays the stacks out; returns the bytes of the whole. `direction`: an FP32
 // direction is kept (Muon with the Nesterov form). It shares the second
 // iterate's place, which is first written after the direction's last use.
-int64_t lay_out(std::vector<Stack>& stacks, int steps, bool direction, bool contiguous) {
+int64_t lay_out(std::vector<Stack>& stacks, const Polynomial& p, bool direction, bool contiguous) {
+  const int steps = p.steps;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t here = at;
     at += round_up(bytes, LA_WORKSPACE_ALIGNMENT);
     return here;
   };
+  bool wide = false;
+  for (const Stack& s : stacks) wide |= std::min(s.rows, s.cols) > la::kNarrow;
   for (Stack& s : stacks) {
+    choose_form(s, p, wide);
     s.ld_straight = round_up(s.cols, la::kDepth);
     s.ld_turned = round_up(s.rows, la::kDepth);
     s.numel_straight = s.rows * s.ld_straight;
     s.numel_turned = s.cols * s.ld_turned;
-    s.m = std::min(s.rows, s.cols);
-    s.n = std::max(s.rows, s.cols);
     s.ldm = round_up(s.m, la::kDepth);
     const int64_t numel = s.rows * s.cols;
     s.numel_direction = round_up(numel, 8);
@@ -168,6 +223,16 @@ int64_t lay_out(std::vector<Stack>& stacks, int steps, bool direction, bool cont
           static_cast<int32_t>((s.rows + s.rows_per_partial - 1) / s.rows_per_partial);
     }
     const int64_t k = s.count;
+    if (s.narrow) {
+      if (direction) s.direction = take(4 * k * s.numel_direction);
+      if (!s.whole) {
+        const int64_t square = static_cast<int64_t>(s.side) * s.side;
+        s.sums = take(4 * k * s.splits * square);
+        s.factors = take(2 * 2 * k * square);
+      }
+      s.partial = take(8 * k * s.partials);
+      continue;
+    }
     s.straight[0] = take(2 * k * s.numel_straight);
     s.straight_lo[0] = take(k * s.numel_straight);
     s.turned[0] = take(2 * k * s.numel_turned);
@@ -288,6 +353,68 @@ la_status enqueue_products(const std::vector<Stack>& stacks, const Polynomial& p
   return ok();
 }
 
+// The narrow stacks, from their directions to the results. `fill` gives a
+// group its source and its output.
+template <typename Fill>
+la_status enqueue_narrow(const std::vector<Stack>& stacks, const Polynomial& p, int type,
+                         int out_type, float decay, Fill fill, void* ws, const int32_t* skip,
+                         hipStream_t stream) {
+  la::NarrowPlan plan = {};
+  plan.steps = p.steps;
+  plan.x = p.step[0].x;
+  plan.eps = p.eps;
+  plan.decay = decay;
+  plan.out_type = out_type;
+  for (int k = 0; k < p.steps; ++k) {
+    const Step& t = p.step[k];
+    plan.step[k] = {static_cast<float>(t.a), static_cast<float>(t.b), static_cast<float>(t.c),
+                    t.gram, t.factor, t.turn, t.whole};
+  }
+  for (const int side : {64, 128})
+    for (const bool whole : {true, false}) {
+      la::NarrowGroup g[la::kGroupsPerLaunch];
+      int count = 0;
+      auto flush = [&]() -> hipError_t {
+        hipError_t e = hipSuccess;
+        auto launch = [&](la::NarrowPart part) {
+          if (e == hipSuccess)
+            e = la::launch_narrow(g, count, side, type, part, plan, skip, stream, la::max_grid());
+        };
+        if (count > 0) {
+          if (whole) {
+            launch(la::NarrowPart::kWhole);
+          } else {
+            launch(la::NarrowPart::kSum);
+            launch(la::NarrowPart::kFactor);
+            launch(la::NarrowPart::kApply);
+          }
+        }
+        count = 0;
+        return e;
+      };
+      hipError_t e = hipSuccess;
+      for (const Stack& s : stacks) {
+        if (!s.narrow || s.side != side || s.whole != whole) continue;
+        la::NarrowGroup& x = g[count++] = {};
+        x.rows = static_cast<int32_t>(s.rows);
+        x.cols = static_cast<int32_t>(s.cols);
+        x.count = static_cast<int32_t>(s.count);
+        x.partial = place<double>(ws, s.partial);
+        x.partials = s.partials;
+        x.gram = place<float>(ws, s.sums);
+        x.q = place<uint16_t>(ws, s.factors);
+        x.splits = static_cast<int32_t>(s.splits);
+        x.chunk = static_cast<int32_t>(s.columns);
+        fill(s, x);
+        if (count == la::kGroupsPerLaunch && (e = flush()) != hipSuccess) break;
+      }
+      if (e == hipSuccess) e = flush();
+      if (e != hipSuccess)
+        return fail(LA_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(e));
+    }
+  return ok();
+}
+
 // The direction's fields that a stack gives by itself.
 la::DirectionGroup direction_group(const Stack& s, void* ws) {
   la::DirectionGroup d = {};
@@ -401,7 +528,7 @@ la_status plan_matrices(const la_matrices_desc* d, const la_polynomial* polynomi
     s.index = i;
     stacks->push_back(s);
   }
-  *bytes = lay_out(*stacks, p->steps, false, false);
+  *bytes = lay_out(*stacks, *p, false, false);
   return LA_OK;
 }
 
@@ -442,27 +569,56 @@ la_status orthogonalize(const la_matrices_desc* d, const la_polynomial* polynomi
   if ((st = check_disjoint(written, read)) != LA_OK) return st;
 
   hipStream_t stream = static_cast<hipStream_t>(hip_stream);
-  for (size_t first = 0; first < stacks.size(); first += la::kGroupsPerLaunch) {
-    la::DirectionGroup g[la::kGroupsPerLaunch];
-    const int count =
-        static_cast<int>(std::min<size_t>(la::kGroupsPerLaunch, stacks.size() - first));
-    for (int i = 0; i < count; ++i) {
-      const Stack& s = stacks[first + i];
-      g[i] = direction_group(s, ws);
-      g[i].in = d->matrices[s.index].in;
-      g[i].row_stride = d->matrices[s.index].in_row_stride;
-      g[i].matrix_stride = d->matrices[s.index].in_matrix_stride;
-    }
-    hipError_t e = la::launch_square_sums(g, count, d->in_type, stream, la::max_grid());
-    if (e == hipSuccess)
-      e = la::launch_normalise(g, count, d->in_type,
-                               static_cast<float>(std::ldexp(1.0, p.step[0].x)), p.eps, nullptr,
-                               stream, la::max_grid());
-    if (e != hipSuccess)
-      return fail(LA_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(e));
+  // the whole narrow form sums its squares itself
+  std::vector<Stack> wide, summed;
+  for (const Stack& x : stacks) {
+    if (!x.narrow) wide.push_back(x);
+    if (!x.narrow || !x.whole) summed.push_back(x);
   }
+  auto directions = [&](const std::vector<Stack>& list, auto launch) -> la_status {
+    for (size_t first = 0; first < list.size(); first += la::kGroupsPerLaunch) {
+      la::DirectionGroup g[la::kGroupsPerLaunch];
+      const int count =
+          static_cast<int>(std::min<size_t>(la::kGroupsPerLaunch, list.size() - first));
+      for (int i = 0; i < count; ++i) {
+        const Stack& s = list[first + i];
+        g[i] = direction_group(s, ws);
+        g[i].in = d->matrices[s.index].in;
+        g[i].row_stride = d->matrices[s.index].in_row_stride;
+        g[i].matrix_stride = d->matrices[s.index].in_matrix_stride;
+      }
+      const hipError_t e = launch(g, count);
+      if (e != hipSuccess)
+        return fail(LA_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(e));
+    }
+    return LA_OK;
+  };
+  st = directions(summed, [&](const la::DirectionGroup* g, int count) {
+    return la::launch_square_sums(g, count, d->in_type, stream, la::max_grid());
+  });
+  if (st != LA_OK) return st;
+  st = enqueue_narrow(
+      stacks, p, d->in_type, d->out_type, 0.0f,
+      [&](const Stack& s, la::NarrowGroup& x) {
+        const la_matrix_desc& t = d->matrices[s.index];
+        x.in = t.in;
+        x.row_stride = t.in_row_stride;
+        x.matrix_stride = t.in_matrix_stride;
+        x.out = t.out;
+        x.out_row_stride = t.out_row_stride;
+        x.out_matrix_stride = t.out_matrix_stride;
+        if (s.whole) x.partial = nullptr;
+      },
+      ws, nullptr, stream);
+  if (st != LA_OK) return st;
+  st = directions(wide, [&](const la::DirectionGroup* g, int count) {
+    return la::launch_normalise(g, count, d->in_type,
+                                static_cast<float>(std::ldexp(1.0, p.step[0].x)), p.eps, nullptr,
+                                stream, la::max_grid());
+  });
+  if (st != LA_OK) return st;
   return enqueue_products(
-      stacks, p, la::Product::kOut, d->out_type, 0.0f,
+      wide, p, la::Product::kOut, d->out_type, 0.0f,
       [&](const Stack& s, la::ProductGroup& x) {
         x.out = d->matrices[s.index].out;
         x.out_ld = d->matrices[s.index].out_row_stride;
@@ -520,7 +676,7 @@ la_status plan_layer(const la_muon_layer_desc* layer, const la_muon_params* hp, 
     s.index = i;
     stacks->push_back(s);
   }
-  *bytes = lay_out(*stacks, p->steps, hp->nesterov != 0, true);
+  *bytes = lay_out(*stacks, *p, hp->nesterov != 0, true);
   return LA_OK;
 }
 
@@ -572,54 +728,85 @@ la_status muon_step(const la_muon_layer_desc* layer, const la_muon_params* hp, i
   if ((st = check_disjoint(written, read)) != LA_OK) return st;
 
   hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+  // the direction of a stack: u = g + mu B in the workspace, or B itself
+  auto direction = [&](const Stack& s) -> const float* {
+    return hp->nesterov ? place<float>(ws, s.direction) : layer->tensors[s.index].momentum;
+  };
+  auto direction_stride = [&](const Stack& s) {
+    return hp->nesterov ? s.numel_direction : s.rows * s.cols;
+  };
   for (size_t first = 0; first < stacks.size(); first += la::kGroupsPerLaunch) {
     la::MomentumGroup g[la::kGroupsPerLaunch] = {};
-    la::DirectionGroup d[la::kGroupsPerLaunch];
     const int count =
         static_cast<int>(std::min<size_t>(la::kGroupsPerLaunch, stacks.size() - first));
     for (int i = 0; i < count; ++i) {
       const Stack& s = stacks[first + i];
       const la_muon_tensor_desc& t = layer->tensors[s.index];
-      d[i] = direction_group(s, ws);
       g[i].momentum = t.momentum;
       g[i].direction = hp->nesterov ? place<float>(ws, s.direction) : nullptr;
       for (int r = 0; r < layer->num_replicas; ++r)
         g[i].g[r] = static_cast<const uint16_t*>(t.grads[r]);
-      g[i].partial = d[i].partial;
+      g[i].partial = place<double>(ws, s.partial);
       g[i].numel = s.rows * s.cols;
       g[i].direction_stride = s.numel_direction;
       g[i].chunk = s.chunk;
       g[i].partials = s.partials;
       g[i].count = static_cast<int32_t>(s.count);
       g[i].vectors = s.count == 1 || g[i].numel % 8 == 0;
-      d[i].in = hp->nesterov ? g[i].direction : g[i].momentum;
-      d[i].row_stride = s.cols;
-      d[i].matrix_stride = hp->nesterov ? s.numel_direction : g[i].numel;
     }
-    hipError_t e = la::launch_momentum(g, count, layer->num_replicas,
-                                       layer->grad_dtype == LA_GRAD_FP16,
-                                       static_cast<float>(hp->momentum),
-                                       static_cast<float>(hp->grad_unscale), flag, skip, stream,
-                                       la::max_grid());
-    if (e == hipSuccess)
-      e = la::launch_normalise(d, count, la::kFp32,
-                               static_cast<float>(std::ldexp(1.0, p.step[0].x)), p.eps, skip,
-                               stream, la::max_grid());
+    const hipError_t e = la::launch_momentum(
+        g, count, layer->num_replicas, layer->grad_dtype == LA_GRAD_FP16,
+        static_cast<float>(hp->momentum), static_cast<float>(hp->grad_unscale), flag, skip, stream,
+        la::max_grid());
     if (e != hipSuccess)
       return fail(LA_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(e));
   }
   const int out = layer->out_dtype == LA_OUT_BF16   ? la::kBf16
                   : layer->out_dtype == LA_OUT_FP16 ? la::kFp16
                                                     : -1;
+  const float decay = static_cast<float>(1.0 - hp->lr * hp->weight_decay);
+  auto step = [&](const Stack& s) {
+    return static_cast<float>(hp->lr * lr_scale(hp->lr_scale, s.rows, s.cols));
+  };
+  st = enqueue_narrow(
+      stacks, p, la::kFp32, out, decay,
+      [&](const Stack& s, la::NarrowGroup& x) {
+        x.in = direction(s);
+        x.row_stride = s.cols;
+        x.matrix_stride = direction_stride(s);
+        x.master = layer->tensors[s.index].master;
+        x.out = copy ? layer->tensors[s.index].weight_out : nullptr;
+        x.step = step(s);
+      },
+      ws, skip, stream);
+  if (st != LA_OK) return st;
+  std::vector<Stack> wide;
+  for (const Stack& s : stacks)
+    if (!s.narrow) wide.push_back(s);
+  for (size_t first = 0; first < wide.size(); first += la::kGroupsPerLaunch) {
+    la::DirectionGroup g[la::kGroupsPerLaunch];
+    const int count =
+        static_cast<int>(std::min<size_t>(la::kGroupsPerLaunch, wide.size() - first));
+    for (int i = 0; i < count; ++i) {
+      const Stack& s = wide[first + i];
+      g[i] = direction_group(s, ws);
+      g[i].in = direction(s);
+      g[i].row_stride = s.cols;
+      g[i].matrix_stride = direction_stride(s);
+    }
+    const hipError_t e = la::launch_normalise(
+        g, count, la::kFp32, static_cast<float>(std::ldexp(1.0, p.step[0].x)), p.eps, skip, stream,
+        la::max_grid());
+    if (e != hipSuccess)
+      return fail(LA_ERR_HIP, "kernel launch failed: %s", hipGetErrorString(e));
+  }
   return enqueue_products(
-      stacks, p, la::Product::kMuon, out,
-      static_cast<float>(1.0 - hp->lr * hp->weight_decay),
+      wide, p, la::Product::kMuon, out, decay,
       [&](const Stack& s, la::ProductGroup& x) {
-        const la_muon_tensor_desc& t = layer->tensors[s.index];
-        x.master = t.master;
-        x.out = copy ? t.weight_out : nullptr;
+        x.master = layer->tensors[s.index].master;
+        x.out = copy ? layer->tensors[s.index].weight_out : nullptr;
         x.vectors = s.cols % 8 == 0;
-        x.step = static_cast<float>(hp->lr * lr_scale(hp->lr_scale, s.rows, s.cols));
+        x.step = step(s);
       },
       ws, skip, stream);
 }

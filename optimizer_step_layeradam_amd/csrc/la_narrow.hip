@@ -1,0 +1,437 @@
+// la_narrow.hip -- the orthogonalised update of narrow matrices (short side m
+// at most 128) for gfx950.
+//
+// Every step multiplies X by a polynomial in S = X X^T, and these commute: so
+// S and the product Q of the steps' factors are carried along as m x m
+// matrices,
+//
+//   S_0 = X_0 X_0^T;  P = a + b S + c S S;  Q <- P Q;  S <- P S P
+//
+// and X is read twice in all, for S_0 and for O = Q X_0, where the
+// step-by-step form reads and writes it in every step. What the short form
+// asks for is precision: an error in S grows by up to a^2 per step where the
+// singular values are small. Every operand here is a pair of binary16 numbers
+// (hi + lo / 2^11, 22 bits) under a power-of-two scale from the host's bounds,
+// every product the three hi hi + hi lo + lo hi with binary32 sums: measured
+// 1e-6 to 5e-4 of the direction over all spectra tried, less than the
+// step-by-step form's.
+//
+// m x m matrices of up to 128 x 128 live in the registers of one workgroup, in
+// the accumulators' layout, and pass through LDS (two operands of 64 KiB) to be
+// multiplied. They are symmetric up to rounding, so the layout's four
+// consecutive rows of one column are stored as four consecutive columns of one
+// row.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "la_muon.h"
+
+#pragma clang fp contract(off)
+
+namespace la {
+namespace {
+
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef _Float16 half4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+struct NarrowArgs {
+  NarrowGroup g[kGroupsPerLaunch];
+  int64_t end[kGroupsPerLaunch];  // cumulative workgroups
+  NarrowPlan plan;
+  const int32_t* skip;
+  int32_t count;
+  NarrowPart part;
+};
+static_assert(sizeof(NarrowArgs) <= 4096, "kernel arguments");
+
+template <int TYPE, typename Raw>
+__device__ __forceinline__ float decode(Raw v) {
+  if constexpr (TYPE == kFp32) return v;
+  else if constexpr (TYPE == kFp16) return static_cast<float>(__builtin_bit_cast(_Float16, v));
+  else return __uint_as_float(static_cast<uint32_t>(v) << 16);
+}
+
+__device__ __forceinline__ uint16_t bits16(float x, int type) {
+  const uint32_t b = __float_as_uint(x);
+  const uint32_t r = (b + 0x7FFFu + ((b >> 16) & 1u)) >> 16;
+  const uint16_t h = __builtin_bit_cast(uint16_t, static_cast<_Float16>(x));
+  const bool nan = __builtin_isnan(x);
+  return type == kFp16 ? (nan ? uint16_t(0x7E00) : h) : static_cast<uint16_t>(nan ? 0x7FC0u : r);
+}
+
+// Where 16-byte piece p of row r of an operand with K elements a row is kept,
+// so that 32 rows' reads of one piece meet every bank equally often.
+template <int K>
+__device__ __forceinline__ int slot(int r, int p) {
+  return K == 64 ? p ^ ((r >> 1) & 7) : p ^ (r & 15);
+}
+
+template <int MP, int TYPE>
+__global__ __launch_bounds__(MP == 128 ? 512 : 256) void narrow_kernel(NarrowArgs a) {
+  using Raw = std::conditional_t<TYPE == kFp32, float, uint16_t>;
+  constexpr int WAVES = MP == 128 ? 8 : 4, THREADS = 64 * WAVES, BJ = MP / 64;
+  constexpr int OPERAND = 2 * MP * MP;  // elements: hi, then lo
+  constexpr int LO = MP * MP;           // of an m x m operand
+  constexpr int XLO = MP * 64;          // of a block of X
+  constexpr int PER = MP * 64 / THREADS;
+  static_assert(PER == 16, "sixteen elements of a block per thread");
+  // an m x m operand; another, or two blocks of X
+  __shared__ __align__(1024) _Float16 lds[OPERAND + (OPERAND > 4 * XLO ? OPERAND : 4 * XLO)];
+  __shared__ double sums[WAVES];
+  if (a.skip != nullptr && *a.skip != 0) return;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32 * BJ;
+  _Float16* const first_operand = lds;
+  _Float16* const second = lds + OPERAND;
+  const bool whole = a.part == NarrowPart::kWhole;
+  const int64_t total = a.end[a.count - 1];
+
+  for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
+    int gi = 0;
+    while (w >= a.end[gi]) ++gi;
+    const NarrowGroup& g = a.g[gi];
+    const int64_t local = w - (gi ? a.end[gi - 1] : 0);
+    const bool tall = g.rows > g.cols;
+    const int m = tall ? g.cols : g.rows, n = tall ? g.rows : g.cols;
+    const int parts = a.part == NarrowPart::kSum     ? g.splits
+                      : a.part == NarrowPart::kApply ? g.splits
+                                                     : 1;
+    const int64_t z = local / parts;
+    const int split = static_cast<int>(local % parts);
+    const int first = whole ? 0 : split * g.chunk;
+    const int last = whole || first + g.chunk > n ? n : first + g.chunk;
+    const int64_t source = z * g.matrix_stride;
+
+    // Element e of this thread in the block of columns c0 .. c0 + 63 of X
+    // (m x n): along the axis on which the matrix is contiguous.
+    auto place = [&](int e, int& i, int& c) {
+      const int unit = wave + WAVES * e;
+      if (tall) {
+        c = MP == 128 ? unit >> 1 : unit;
+        i = MP == 128 ? lane + 64 * (unit & 1) : lane;
+      } else {
+        c = lane;
+        i = unit;
+      }
+    };
+    // Raw elements, from inside the matrix whatever the place: a load under a
+    // condition would be waited for before the next is asked for.
+    auto fetch = [&](Raw (&v)[PER], int c0) {
+#pragma unroll
+      for (int e = 0; e < PER; ++e) {
+        int i, c;
+        place(e, i, c);
+        i = i < m ? i : m - 1;
+        c = c0 + c < last ? c0 + c : last - 1;
+        v[e] = static_cast<const Raw*>(g.in)[source + (tall ? c * g.row_stride + i
+                                                            : i * g.row_stride + c)];
+      }
+    };
+    auto value = [&](Raw v, int e, int c0) {
+      int i, c;
+      place(e, i, c);
+      return i < m && c0 + c < last ? decode<TYPE>(v) : 0.0f;
+    };
+
+    double factor = 0.0;
+    if (a.part != NarrowPart::kFactor) {
+      double sum = 0.0;
+      if (g.partial != nullptr) {
+        for (int k = tid; k < g.partials; k += THREADS) sum += g.partial[z * g.partials + k];
+      } else {
+        for (int c0 = 0; c0 < n; c0 += 64) {
+          Raw v[PER];
+          fetch(v, c0);
+#pragma unroll
+          for (int e = 0; e < PER; ++e) {
+            const double x = value(v[e], e, c0);
+            sum += x * x;
+          }
+        }
+      }
+#pragma unroll
+      for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d, 64);
+      if (lane == 0) sums[wave] = sum;
+      __syncthreads();
+      sum = sums[0];
+      for (int k = 1; k < WAVES; ++k) sum += sums[k];
+      const double norm = __builtin_sqrt(sum);
+      const double denominator = norm < a.plan.eps ? a.plan.eps : norm;  // NaN stays
+      if (denominator > 0.0) factor = __builtin_ldexp(1.0, a.plan.x) / denominator;
+      if (!(sum < __builtin_inf())) factor = __builtin_nan("");
+    }
+
+    // A block of X as an operand: rows i, summed over c (turned: rows c, summed
+    // over i).
+    auto put = [&](const Raw (&v)[PER], int c0, _Float16* to, bool turned) {
+#pragma unroll
+      for (int e = 0; e < PER; ++e) {
+        int i, c;
+        place(e, i, c);
+        const float x = static_cast<float>(static_cast<double>(value(v[e], e, c0)) * factor);
+        const _Float16 hi = static_cast<_Float16>(x);
+        const int at = turned ? c * MP + slot<MP>(c, i >> 3) * 8 + (i & 7)
+                              : i * 64 + slot<64>(i, c >> 3) * 8 + (c & 7);
+        to[at] = hi;
+        to[XLO + at] = static_cast<_Float16>((x - static_cast<float>(hi)) * 0x1p11f);
+      }
+    };
+
+    // acc += P Q^T over K for the wave's 32 rows of P and blocks of 32 rows of
+    // Q; low parts, hi lo and lo hi, in sums of their own, 2^11 times as large
+    // (three chains of matrix instructions that do not wait for each other).
+    auto multiply = [&](auto k_const, auto blocks, const _Float16* p, int p_lo, int p_row,
+                        const _Float16* q, int q_lo, int q_row, f32x16* acc, f32x16* low) {
+      constexpr int K = decltype(k_const)::value, BLOCKS = decltype(blocks)::value;
+      const int r = p_row + (lane & 31);
+      constexpr bool APART = BLOCKS == 1;  // two blocks have chains enough
+      f32x16 other[BLOCKS] = {};
+#pragma unroll 2
+      for (int k = 0; k < K / 16; ++k) {
+        const int piece = 2 * k + (lane >> 5);
+        const _Float16* pp = p + r * K + slot<K>(r, piece) * 8;
+        const half8 ph = *reinterpret_cast<const half8*>(pp);
+        const half8 pl = *reinterpret_cast<const half8*>(pp + p_lo);
+#pragma unroll
+        for (int j = 0; j < BLOCKS; ++j) {
+          const int s = q_row + 32 * j + (lane & 31);
+          const _Float16* qq = q + s * K + slot<K>(s, piece) * 8;
+          const half8 qh = *reinterpret_cast<const half8*>(qq);
+          const half8 ql = *reinterpret_cast<const half8*>(qq + q_lo);
+          acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph, qh, acc[j], 0, 0, 0);
+          low[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph, ql, low[j], 0, 0, 0);
+          f32x16& last_low = APART ? other[j] : low[j];
+          last_low = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl, qh, last_low, 0, 0, 0);
+        }
+      }
+      if constexpr (APART)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) low[0][e] += other[0][e];
+    };
+    using Side = std::integral_constant<int, MP>;
+    using Stage = std::integral_constant<int, 64>;
+    using Blocks = std::integral_constant<int, BJ>;
+    using One = std::integral_constant<int, 1>;
+
+    // The m x m matrices, in the accumulators' layout.
+    f32x16 S[BJ] = {}, Q[BJ] = {};
+    // P Q^T of two m x m operands, times 2^-e
+    auto product = [&](const _Float16* p, const _Float16* q, int e, f32x16 (&out)[BJ]) {
+      f32x16 acc[BJ] = {}, low[BJ] = {};
+      multiply(Side(), Blocks(), p, LO, wm, q, LO, wn, acc, low);
+      const float f = __builtin_ldexpf(1.0f, -e);
+#pragma unroll
+      for (int j = 0; j < BJ; ++j)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) out[j][k] = (acc[j][k] + low[j][k] * 0x1p-11f) * f;
+    };
+    auto store = [&](const f32x16 (&v)[BJ], _Float16* to, int e) {
+      const float f = __builtin_ldexpf(1.0f, e);
+#pragma unroll
+      for (int j = 0; j < BJ; ++j) {
+        const int row = wn + 32 * j + (lane & 31);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          half4 hi, lo;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float x = v[j][4 * q + k] * f;
+            hi[k] = static_cast<_Float16>(x);
+            lo[k] = static_cast<_Float16>((x - static_cast<float>(hi[k])) * 0x1p11f);
+          }
+          _Float16* at = to + row * MP + slot<MP>(row, (wm >> 3) + q) * 8 + 4 * (lane >> 5);
+          *reinterpret_cast<half4*>(at) = hi;
+          *reinterpret_cast<half4*>(at + LO) = lo;
+        }
+      }
+    };
+
+    if (whole || a.part == NarrowPart::kSum) {
+      f32x16 acc[BJ] = {}, low[BJ] = {};
+      Raw v[PER];
+      fetch(v, first);
+      int b = 0;
+      for (int c0 = first; c0 < last; c0 += 64, b ^= 1) {
+        put(v, c0, lds + b * OPERAND, false);
+        __syncthreads();
+        if (c0 + 64 < last) fetch(v, c0 + 64);
+        multiply(Stage(), Blocks(), lds + b * OPERAND, XLO, wm, lds + b * OPERAND, XLO, wn, acc, low);
+      }
+      __syncthreads();
+      const float f = __builtin_ldexpf(1.0f, -2 * a.plan.x);
+#pragma unroll
+      for (int j = 0; j < BJ; ++j)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) S[j][k] = (acc[j][k] + low[j][k] * 0x1p-11f) * f;
+      if (!whole) {
+        float* to = g.gram + (z * g.splits + split) * (MP * MP) + wave * (BJ * 1024) + lane;
+#pragma unroll
+        for (int j = 0; j < BJ; ++j)
+#pragma unroll
+          for (int k = 0; k < 16; ++k) to[(16 * j + k) * 64] = S[j][k];
+      }
+    }
+    if (a.part == NarrowPart::kFactor) {
+      for (int s = 0; s < g.splits; ++s) {
+        const float* from = g.gram + (z * g.splits + s) * (MP * MP) + wave * (BJ * 1024) + lane;
+#pragma unroll
+        for (int j = 0; j < BJ; ++j)
+#pragma unroll
+          for (int k = 0; k < 16; ++k) S[j][k] += from[(16 * j + k) * 64];
+      }
+    }
+
+    if (whole || a.part == NarrowPart::kFactor) {
+      store(S, first_operand, a.plan.step[0].s);
+      __syncthreads();
+#pragma unroll 1
+      for (int k = 0; k < a.plan.steps; ++k) {
+        const NarrowStep& t = a.plan.step[k];
+        const bool more = k + 1 < a.plan.steps;
+        f32x16 P[BJ];
+        product(first_operand, first_operand, 2 * t.s, P);
+#pragma unroll
+        for (int j = 0; j < BJ; ++j)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int row = wm + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
+            const int col = wn + 32 * j + (lane & 31);
+            P[j][e] = (row == col && row < m ? t.a : 0.0f) + (t.b * S[j][e] + t.c * P[j][e]);
+          }
+        store(P, second, t.p);
+        __syncthreads();
+        if (more) {
+          // An operand stored from V holds V^T: T = S^T P, S <- P^T T, and its
+          // mirror image T^T P, which the two operands exchanged give bit for
+          // bit: their mean is symmetric.
+          f32x16 T[BJ];
+          product(first_operand, second, t.p + t.s, T);
+          __syncthreads();
+          store(T, first_operand, t.t);
+          __syncthreads();
+          product(second, first_operand, t.t + t.p, S);
+          product(first_operand, second, t.t + t.p, T);
+          __syncthreads();
+#pragma unroll
+          for (int j = 0; j < BJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) S[j][e] = 0.5f * (S[j][e] + T[j][e]);
+        }
+        if (k == 0) {
+#pragma unroll
+          for (int j = 0; j < BJ; ++j) Q[j] = P[j];
+        } else {
+          const int before = a.plan.step[k - 1].q;
+          store(Q, first_operand, before);
+          __syncthreads();
+          product(second, first_operand, t.p + before, Q);
+          __syncthreads();
+        }
+        if (more) store(S, first_operand, a.plan.step[k + 1].s);
+        __syncthreads();
+      }
+      store(Q, first_operand, a.plan.step[a.plan.steps - 1].q);
+      __syncthreads();
+      if (!whole) {
+        half8* to = reinterpret_cast<half8*>(g.q + z * OPERAND);
+        for (int k = tid; k < OPERAND / 8; k += THREADS)
+          to[k] = reinterpret_cast<const half8*>(first_operand)[k];
+      }
+    }
+
+    if (whole || a.part == NarrowPart::kApply) {
+      if (!whole) {
+        const half8* from = reinterpret_cast<const half8*>(g.q + z * OPERAND);
+        for (int k = tid; k < OPERAND / 8; k += THREADS)
+          reinterpret_cast<half8*>(first_operand)[k] = from[k];
+      }
+      // Tiles of 64 columns, one 32 x 32 block per wave; two blocks of X take
+      // turns in the second buffer. Lanes run along the axis on which the
+      // result is contiguous.
+      const int wi = (wave >> 1) * 32, wj = (wave & 1) * 32;
+      const float f =
+          __builtin_ldexpf(1.0f, -(a.plan.x + a.plan.step[a.plan.steps - 1].q));
+      Raw v[PER];
+      fetch(v, first);
+      int b = 0;
+      for (int c0 = first; c0 < last; c0 += 64, b ^= 1) {
+        _Float16* x = second + b * 2 * XLO;
+        put(v, c0, x, true);
+        __syncthreads();
+        if (c0 + 64 < last) fetch(v, c0 + 64);
+        f32x16 acc[1] = {}, low[1] = {};
+        if (tall) multiply(Side(), One(), x, XLO, wj, first_operand, LO, wi, acc, low);
+        else multiply(Side(), One(), first_operand, LO, wi, x, XLO, wj, acc, low);
+        const int rows = tall ? last : m, cols = tall ? m : last;
+        const int row0 = (tall ? c0 + wj : wi) + 4 * (lane >> 5);
+        const int col = (tall ? wi : c0 + wj) + (lane & 31);
+        float p[16];
+        if (g.master != nullptr) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int row = row0 + 8 * (k >> 2) + (k & 3);
+            p[k] = g.master[(z * g.rows + (row < rows ? row : rows - 1)) * g.cols +
+                            (col < cols ? col : cols - 1)];
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int row = row0 + 8 * (k >> 2) + (k & 3);
+          float o = (acc[0][k] + low[0][k] * 0x1p-11f) * f;
+          int64_t at = z * g.out_matrix_stride + row * g.out_row_stride + col;
+          if (g.master != nullptr) {
+            at = (z * g.rows + row) * g.cols + col;
+            o = p[k] * a.plan.decay - g.step * o;
+            if (row < rows && col < cols) g.master[at] = o;
+          }
+          if (g.out != nullptr && row < rows && col < cols)
+            static_cast<uint16_t*>(g.out)[at] = bits16(o, a.plan.out_type);
+        }
+      }
+    }
+    __syncthreads();  // LDS is free for the next matrix
+  }
+}
+
+template <int MP, int TYPE>
+hipError_t launch(NarrowArgs& a, int64_t total, hipStream_t stream, int64_t max_grid) {
+  int64_t grid = total < kMaxWorkgroups ? total : kMaxWorkgroups;
+  if (grid > max_grid) grid = max_grid;
+  void* params[] = {&a};
+  return hipLaunchKernel(reinterpret_cast<const void*>(&narrow_kernel<MP, TYPE>),
+                         dim3(static_cast<unsigned>(grid)), dim3(MP == 128 ? 512 : 256), params, 0,
+                         stream);
+}
+
+}  // namespace
+
+hipError_t launch_narrow(const NarrowGroup* groups, int count, int side, int type,
+                         NarrowPart part, const NarrowPlan& plan, const int32_t* skip,
+                         hipStream_t stream, int64_t max_grid) {
+  NarrowArgs a = {};
+  int64_t total = 0;
+  for (int i = 0; i < count; ++i) {
+    a.g[i] = groups[i];
+    const bool split = part == NarrowPart::kSum || part == NarrowPart::kApply;
+    total += static_cast<int64_t>(groups[i].count) * (split ? groups[i].splits : 1);
+    a.end[i] = total;
+  }
+  a.plan = plan;
+  a.skip = skip;
+  a.count = count;
+  a.part = part;
+  if (side == 64)
+    return type == kFp32   ? launch<64, kFp32>(a, total, stream, max_grid)
+           : type == kFp16 ? launch<64, kFp16>(a, total, stream, max_grid)
+                           : launch<64, kBf16>(a, total, stream, max_grid);
+  return type == kFp32   ? launch<128, kFp32>(a, total, stream, max_grid)
+         : type == kFp16 ? launch<128, kFp16>(a, total, stream, max_grid)
+                         : launch<128, kBf16>(a, total, stream, max_grid);
+}
+
+}  // namespace la

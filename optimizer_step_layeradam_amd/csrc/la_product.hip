@@ -12,18 +12,6 @@
 
 #pragma clang fp contract(off)
 
-#ifndef LA_B2
-#define LA_B2 4
-#endif
-#ifndef LA_NT
-#define LA_NT 4
-#endif
-#ifndef LA_D4
-#define LA_D4 64
-#endif
-#ifndef LA_B4
-#define LA_B4 2
-#endif
 namespace la {
 namespace {
 
@@ -154,7 +142,7 @@ struct Tile {
   static constexpr int p_copies = rows / (copy_rows * waves);
   static constexpr int q_copies = cols / (copy_rows * waves);
   static constexpr int in_flight = (BUFFERS - 2) * (p_copies + q_copies);
-  static_assert(BUFFERS * stage * 2 >= waves * 16384, "the epilogue takes 16 KiB of LDS per wave");
+  static_assert(BUFFERS * stage * 2 >= waves * 32 * MT * 256, "the epilogue's part of LDS");
   static_assert(rows % (copy_rows * waves) == 0 && cols % (copy_rows * waves) == 0,
                 "whole rows per copy");
   static_assert(kDepth % DEPTH == 0 && (DEPTH == 32 || DEPTH == 64), "whole stages");
@@ -473,24 +461,21 @@ __global__ __launch_bounds__(64 * WM * WN, MT * NT == 8 ? 2 : 1) void product_ke
         buffer = next;
       }
     }
-    // every wave is past its last read of LDS: the last wait_and_meet
-
-    // Per 64 rows: the sums change from the accumulators' layout (lane l:
-    // column l % 32; register r: row 8 (r / 4) + 4 (l / 32) + r % 4) to eight
-    // neighbours of a row per lane through 8 KiB of LDS per wave, are
-    // finished, and their binary16 form passes through another 8 KiB to be
-    // stored turned. Both places are the wave's own.
-    float* sums = reinterpret_cast<float*>(lds) + wave * 4096;
-    _Float16* turn = reinterpret_cast<_Float16*>(sums + 2048);
+    // Every wave is past its last read of LDS. The sums change from the
+    // accumulators' layout (lane l: column l % 32; register r: row 8 (r / 4) +
+    // 4 (l / 32) + r % 4) to eight neighbours of a row per lane through the
+    // wave's own part of LDS, 64 columns at a time: rows of 256 bytes, whose
+    // halves are exchanged every four rows. Their binary16 form goes back into
+    // the first half of the row it came from, at 16-byte piece ^ (row / 8 % 8),
+    // to be stored turned. The loops are not unrolled: a tile's epilogue would
+    // be more code than the instruction cache holds.
+    float* sums = reinterpret_cast<float*>(lds) + wave * (32 * MT * 64);
+    _Float16* turn = reinterpret_cast<_Float16*>(sums);
     const bool mirror = TURN && (!SYM || ti != tj);
     const int k8 = (lane & 7) * 8;
-    // halves of a part whose operands are held: both, but for kMuon's twelve
-    // registers a row in the large tile
-    constexpr int AHEAD = MT * NT > 4 && WHAT == Product::kMuon ? 1 : 2;
-#pragma unroll
-    for (int part = 0; part < MT * NT / 4; ++part) {
-      const int ci = part % (MT / 2), cj = part / (MT / 2);
-      const int rowc = row0 + wm + 64 * ci, colw = col0 + wn + 64 * cj;
+#pragma unroll 1
+    for (int cj = 0; cj < NT / 2; ++cj) {
+      const int rowc = row0 + wm, colw = col0 + wn + 64 * cj;
       float dc[8] = {};
       if constexpr (WHAT != Product::kGram) {
         if (WHAT == Product::kSquare || g.tall) {
@@ -506,59 +491,70 @@ __global__ __launch_bounds__(64 * WM * WN, MT * NT == 8 ? 2 : 1) void product_ke
         const int c = colw + k8 + 2 * e;
         mask[e] = c + 1 < g.N ? ~0u : c < g.N ? 0xFFFFu : 0u;
       }
-      Operands<WHAT> x[AHEAD][4];
-      auto load = [&](int hf) {
+      Operands<WHAT> next[4];
+      auto load = [&](int i) {
 #pragma unroll
         for (int p = 0; p < 4; ++p)
-          load_operands(x[hf % AHEAD][p], g, z, rowc + 32 * hf + 8 * p + (lane >> 3), colw + k8);
+          load_operands(next[p], g, z, rowc + 32 * i + 8 * p + (lane >> 3), colw + k8);
       };
       load(0);
-      if constexpr (AHEAD == 2) load(1);
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
+      for (int c = 0; c < NT / 2; ++c) {
+        if (c != cj) continue;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int r = 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-            sums[r * 64 + ((32 * j + (lane & 31)) ^ ((lane >> 5) << 5))] =
-                acc[2 * ci + hf][2 * cj + j][e];
-          }
-        wave_fence();
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int r = 32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
+              sums[r * 64 + ((32 * j + (lane & 31)) ^ ((lane >> 5) << 5))] = acc[i][2 * c + j][e];
+            }
+      }
+      wave_fence();
+#pragma unroll 1
+      for (int i = 0; i < MT; ++i) {
+        Operands<WHAT> x[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) x[p] = next[p];
+        if (i + 1 < MT) load(i + 1);
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-          const int r = 8 * p + (lane >> 3);
+          const int r = 32 * i + 8 * p + (lane >> 3);
           const float* from = sums + r * 64 + (k8 ^ (((r >> 2) & 1) << 5));
           float v[8];
           *reinterpret_cast<f32x4*>(v) = *reinterpret_cast<const f32x4*>(from);
           *reinterpret_cast<f32x4*>(v + 4) = *reinterpret_cast<const f32x4*>(from + 4);
-          const half8 h = finish<WHAT, OUT>(g, a.s, z, rowc + 32 * hf + r, colw + k8, v,
-                                            x[hf % AHEAD][p], dc, mask);
+          const half8 h =
+              finish<WHAT, OUT>(g, a.s, z, rowc + r, colw + k8, v, x[p], dc, mask);
           if constexpr (TURN) {
-            const int rr = 32 * hf + r;
-            *reinterpret_cast<half8*>(turn + rr * 64 + (((lane & 7) ^ ((rr >> 3) & 7)) << 3)) = h;
+            wave_fence();
+            *reinterpret_cast<half8*>(turn + r * 128 + (((lane & 7) ^ ((r >> 3) & 7)) << 3)) = h;
           }
         }
-        if constexpr (AHEAD == 1)
-          if (hf == 0) load(1);
-        wave_fence();
       }
       if (mirror) {
+        wave_fence();
         _Float16* to = reinterpret_cast<_Float16*>(SYM ? g.c : g.turned) +
                        static_cast<int64_t>(z) * (SYM ? g.c_stride : g.turned_stride);
         const int ld = SYM ? g.ldc : g.ld_turned;
-#pragma unroll
+        const int r = (lane & 7) * 8;
+#pragma unroll 1
         for (int p = 0; p < 8; ++p) {
-          const int k = 8 * p + (lane >> 3), r = (lane & 7) * 8;
-          half8 h;
+          const int k = 8 * p + (lane >> 3);
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            h[e] = turn[(r + e) * 64 + ((p ^ (lane & 7)) << 3) + (lane >> 3)];
-          if (colw + k < g.N && rowc + r < ld)
-            *reinterpret_cast<half8*>(to + static_cast<int64_t>(colw + k) * ld + rowc + r) = h;
+          for (int c = 0; c < MT / 2; ++c) {
+            half8 h;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              h[e] = turn[(64 * c + r + e) * 128 + ((p ^ (lane & 7)) << 3) + (lane >> 3)];
+            const int row = rowc + 64 * c + r;
+            if (colw + k < g.N && row < ld)
+              *reinterpret_cast<half8*>(to + static_cast<int64_t>(colw + k) * ld + row) = h;
+          }
         }
-        wave_fence();
       }
+      wave_fence();
     }
     wait_and_meet<0>();  // LDS is free for the next tile, and no store is counted with its copies
   }
@@ -609,11 +605,9 @@ hipError_t launch_one(const ProductGroup* groups, int count, const ProductScales
   }
   static const int force = [] { const char* e = getenv("LA_TILE"); return e ? atoi(e) : 0; }();
   if (force ? force == 256 : large >= 200) {
-    static const int w8 = [] { const char* e = getenv("LA_W8"); return e ? atoi(e) : 0; }();
-    if (w8) return launch_tile<WHAT, OUT, 4, 2, 2, 4, 64, 2>(groups, count, s, skip, stream, max_grid);
     return launch_tile<WHAT, OUT, 4, 4, 2, 2, 64, 2>(groups, count, s, skip, stream, max_grid);
   }
-  return launch_tile<WHAT, OUT, 2, 2, 2, 2, 64, LA_B2>(groups, count, s, skip, stream, max_grid);
+  return launch_tile<WHAT, OUT, 2, 2, 2, 2, 64, 4>(groups, count, s, skip, stream, max_grid);
 }
 
 }  // namespace

@@ -46,13 +46,33 @@ def test_types(dtype, out):
         check(x, o)
 
 
-def test_many_stacks_in_one_call_equal_one_call_each():
-    xs = [matrices((1 + i % 3, 1 + 13 * i % 150, 1 + 29 * i % 170), seed=i).to(torch.bfloat16)
-          .cuda() for i in range(37)]
+@pytest.mark.parametrize("least", [1, 129])
+def test_many_stacks_in_one_call_equal_one_call_each(least):
+    """37 stacks, narrow ones (short side up to 128) or wide ones, take the same
+    form together as alone, and so give the same bits."""
+    xs = [matrices((1 + i % 3, least + 13 * i % 120, least + 29 * i % 127), seed=i)
+          .to(torch.bfloat16).cuda() for i in range(37)]
     together = la.orthogonalize(xs)
     for x, o in zip(xs, together):
         alone = la.orthogonalize(x)
         assert torch.equal(o.view(torch.int16), alone.view(torch.int16)), x.shape
+
+
+def test_narrow_and_wide_stacks_in_one_call():
+    shapes = [(1 + i % 3, 1 + 13 * i % 150, 1 + 29 * i % 170) for i in range(37)]
+    shapes += [(40, 100, 1100), (20, 4200, 60)]  # narrow ones of their own launches
+    xs = [matrices(s, seed=i).to(torch.bfloat16).cuda() for i, s in enumerate(shapes)]
+    for x, o in zip(xs, la.orthogonalize(xs)):
+        check(x, o)
+
+
+@pytest.mark.parametrize("shape", [(128, 5000), (5000, 127), (64, 3001), (2999, 65), (1, 12000),
+                                   (12000, 2), (3, 33, 2000), (5, 1500, 100), (600, 20, 50),
+                                   (513, 70, 90), (128, 513), (64, 512), (514, 128)], ids=str)
+@pytest.mark.parametrize("kind", ["gauss", "lowrank", "spiked"])
+def test_long_narrow_matrices_and_many_of_them(shape, kind):
+    x = matrices(shape, kind, seed=sum(shape)).cuda()
+    check(x, la.orthogonalize(x))
 
 
 def test_magnitudes_do_not_matter():

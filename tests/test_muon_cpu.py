@@ -180,7 +180,7 @@ def test_muon_many_tensors():
 
 
 def test_workspace_of_a_step():
-    def need(nesterov, steps, shape=(40, 60)):
+    def need(nesterov, steps, shape=(400, 600)):
         desc, keep = la.make_muon_layer([dict(rows=shape[0], cols=shape[1])], 1, 0)
         hp = la.make_muon_params(0.0, nesterov=nesterov,
                                  polynomial=la.make_polynomial(((1.5, -0.5, 0.0),) * steps))
@@ -188,13 +188,16 @@ def test_workspace_of_a_step():
 
     assert 0 < need(False, 1) < need(False, 2) < need(False, 3) == need(False, 16)
     assert need(True, 1) > need(False, 1)
+    # a narrow matrix keeps its FP32 direction at most; a long one also sums of its S
+    assert 4 * 40 * 60 <= need(True, 5, (40, 60)) < 4 * 40 * 60 + 1024 > need(False, 5, (40, 60))
+    assert need(False, 5, (9000, 40)) > need(False, 5, (500, 40))
     # large matrices: no more than six padded 16-bit copies and two Gram matrices
     assert need(True, 5, (4096, 4096)) < 8.01 * 2 * 4096 ** 2
 
 
 def test_workspace_by_shapes():
-    assert la.orthogonalize_workspace_bytes([(3, 40, 60)]) > \
-        la.orthogonalize_workspace_bytes([(40, 60)])
+    assert la.orthogonalize_workspace_bytes([(3, 400, 600)]) > \
+        la.orthogonalize_workspace_bytes([(400, 600)])
     with pytest.raises(la.LayerAdamError):
         la.orthogonalize_workspace_bytes([(-1, 4)])
 
