@@ -87,6 +87,7 @@ struct DirectionGroup {
   int32_t ld_straight, ld_turned;
   int32_t partials;        // sums of squares per matrix
   int32_t rows_per_partial;
+  int32_t vectors;         // 1: every 8 elements of a row are 16-byte aligned
 };
 
 // Sums of squares of the directions (orthogonalize only: the momentum pass

@@ -586,6 +586,9 @@ la_status orthogonalize(const la_matrices_desc* d, const la_polynomial* polynomi
         g[i].in = d->matrices[s.index].in;
         g[i].row_stride = d->matrices[s.index].in_row_stride;
         g[i].matrix_stride = d->matrices[s.index].in_matrix_stride;
+        g[i].vectors = aligned(g[i].in, 16) && s.cols % 8 == 0 &&
+                       (s.rows == 1 || g[i].row_stride % 8 == 0) &&
+                       (s.count == 1 || g[i].matrix_stride % 8 == 0);
       }
       const hipError_t e = launch(g, count);
       if (e != hipSuccess)
@@ -793,6 +796,7 @@ la_status muon_step(const la_muon_layer_desc* layer, const la_muon_params* hp, i
       g[i].in = direction(s);
       g[i].row_stride = s.cols;
       g[i].matrix_stride = direction_stride(s);
+      g[i].vectors = s.cols % 8 == 0;
     }
     const hipError_t e = la::launch_normalise(
         g, count, la::kFp32, static_cast<float>(std::ldexp(1.0, p.step[0].x)), p.eps, skip, stream,

@@ -317,8 +317,15 @@ __global__ __launch_bounds__(64 * WM * WN, MT * NT == 8 ? 2 : 1) void product_ke
     const ProductGroup& g = a.g[gi];
     const int64_t first = gi ? a.tile_end[gi - 1] : 0;
     const int64_t local = xcd_order(w - first, a.tile_end[gi] - first);
-    const int z = static_cast<int>(local / a.tiles[gi]);
-    const int t = static_cast<int>(local % a.tiles[gi]);
+    // in 32 bits where they suffice: a 64-bit division is a routine
+    int z, t;
+    if (total <= 0x7fffffff) {
+      z = static_cast<int>(static_cast<uint32_t>(local) / static_cast<uint32_t>(a.tiles[gi]));
+      t = static_cast<int>(local) - z * a.tiles[gi];
+    } else {
+      z = static_cast<int>(local / a.tiles[gi]);
+      t = static_cast<int>(local % a.tiles[gi]);
+    }
     int ti, tj;
     if constexpr (SYM) triangle(t, a.tiles_m[gi], ti, tj);
     else rectangle(t, a.tiles_m[gi], a.tiles_n[gi], ti, tj);
@@ -539,7 +546,7 @@ __global__ __launch_bounds__(64 * WM * WN, MT * NT == 8 ? 2 : 1) void product_ke
                        static_cast<int64_t>(z) * (SYM ? g.c_stride : g.turned_stride);
         const int ld = SYM ? g.ldc : g.ld_turned;
         const int r = (lane & 7) * 8;
-#pragma unroll 1
+#pragma unroll 2
         for (int p = 0; p < 8; ++p) {
           const int k = 8 * p + (lane >> 3);
 #pragma unroll
@@ -598,15 +605,20 @@ template <Product WHAT, int OUT>
 hipError_t launch_one(const ProductGroup* groups, int count, const ProductScales& s,
                       const int32_t* skip, hipStream_t stream, int64_t max_grid) {
   constexpr bool SYM = WHAT == Product::kGram || WHAT == Product::kSquare;
-  int64_t large = 0;
-  for (int i = 0; i < count; ++i) {
-    const int64_t tm = (groups[i].M + 255) / 256, tn = (groups[i].N + 255) / 256;
-    large += (SYM ? tm * (tm + 1) / 2 : tm * tn) * groups[i].count;
-  }
+  // A workgroup has a compute unit to itself in either size, and one of the
+  // large tile takes 5/3 of the time of a small one (K = 4096: 84 us to 50 us):
+  // the size whose rounds over the 256 compute units take less.
+  auto rounds = [&](int64_t side) {
+    int64_t tiles = 0;
+    for (int i = 0; i < count; ++i) {
+      const int64_t tm = (groups[i].M + side - 1) / side, tn = (groups[i].N + side - 1) / side;
+      tiles += (SYM ? tm * (tm + 1) / 2 : tm * tn) * groups[i].count;
+    }
+    return (tiles + 255) / 256;
+  };
   static const int force = [] { const char* e = getenv("LA_TILE"); return e ? atoi(e) : 0; }();
-  if (force ? force == 256 : large >= 200) {
+  if (force ? force == 256 : 5 * rounds(256) < 3 * rounds(128))
     return launch_tile<WHAT, OUT, 4, 4, 2, 2, 64, 2>(groups, count, s, skip, stream, max_grid);
-  }
   return launch_tile<WHAT, OUT, 2, 2, 2, 2, 64, 4>(groups, count, s, skip, stream, max_grid);
 }
 
