@@ -171,7 +171,7 @@ struct NarrowStep {
   int32_t s, p, t, q;  // exponents of the scales of S, P = a + b S + c S S, P S and Q = P ... P
 };
 
-// kWhole: all of it, one workgroup per matrix; kSum, kFactor, kApply: its
+// kWhole (side 64 only): all of it, one workgroup per matrix; kSum, kFactor, kApply: its
 // three parts, with as many workgroups as there is work for.
 enum class NarrowPart { kWhole, kSum, kFactor, kApply };
 

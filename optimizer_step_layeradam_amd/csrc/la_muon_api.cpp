@@ -153,22 +153,27 @@ constexpr double kMostGrowth = 512.0;
 constexpr int64_t kWholeColumns = 512;
 constexpr int64_t kWholeCount = 512;
 constexpr int64_t kParts = 512;
+constexpr int64_t kMostParts = 32;  // of one matrix: one workgroup adds them up
 
-// Beside wide stacks, whose launches it can share, a narrow stack of fewer
-// elements than this does not get launches of its own (a layer of 256 x 256,
-// 2 of 256 x 64 and 688 x 256: 183 us in shared launches, 258 us apart; 40 of
-// 128 x 5120 apart: 880 -> 479 us).
-constexpr int64_t kOwnLaunches = int64_t(1) << 22;
+// Beside wide stacks, whose launches it can share, a small narrow stack does
+// not get one of its own: sides up to kWholeColumns (a longer side makes the
+// step-by-step form's few tiles of X X^T long: 6 of 6566 x 12 and 12 of 770 x 2
+// beside 4 of 2160 x 246 take 558 us in shared launches, 362 us in their own)
+// and up to this many elements as that form pads them (a layer of 256 x 256, 2
+// of 256 x 64 and 688 x 256: 186 us in shared launches, 258 us apart).
+constexpr int64_t kSharedElements = int64_t(1) << 20;
 
 void choose_form(Stack& s, const Polynomial& p, bool beside_wide) {
   s.m = std::min(s.rows, s.cols);
   s.n = std::max(s.rows, s.cols);
-  s.narrow = s.m <= la::kNarrow && p.growth <= kMostGrowth &&
-             (!beside_wide || s.rows * s.cols * s.count >= kOwnLaunches);
+  const bool shares = beside_wide && s.n <= kWholeColumns &&
+                      s.count * s.n * round_up(s.m, la::kDepth) <= kSharedElements;
+  s.narrow = s.m <= la::kNarrow && p.growth <= kMostGrowth && !shares;
   if (!s.narrow) return;
   s.side = s.m <= 64 ? 64 : 128;
-  s.whole = s.n <= kWholeColumns || s.count >= kWholeCount;
-  s.splits = std::min((kParts + s.count - 1) / s.count, (s.n + 255) / 256);
+  // 128 x 128 operands leave the whole form no registers
+  s.whole = s.side == 64 && (s.n <= kWholeColumns || s.count >= kWholeCount);
+  s.splits = std::min({(kParts + s.count - 1) / s.count, (s.n + 255) / 256, kMostParts});
   s.columns = round_up((s.n + s.splits - 1) / s.splits, 64);
   s.splits = (s.n + s.columns - 1) / s.columns;
 }

@@ -44,7 +44,6 @@ struct NarrowArgs {
   NarrowPlan plan;
   const int32_t* skip;
   int32_t count;
-  NarrowPart part;
 };
 static_assert(sizeof(NarrowArgs) <= 4096, "kernel arguments");
 
@@ -70,8 +69,9 @@ __device__ __forceinline__ int slot(int r, int p) {
   return K == 64 ? p ^ ((r >> 1) & 7) : p ^ (r & 15);
 }
 
-template <int MP, int TYPE>
-__global__ __launch_bounds__(MP == 128 ? 512 : 256) void narrow_kernel(NarrowArgs a) {
+template <int MP, int TYPE, NarrowPart PART>
+__global__ __launch_bounds__(MP == 128 ? 512 : 256, PART == NarrowPart::kWhole ? 1 : 2)
+void narrow_kernel(NarrowArgs a) {
   using Raw = std::conditional_t<TYPE == kFp32, float, uint16_t>;
   constexpr int WAVES = MP == 128 ? 8 : 4, THREADS = 64 * WAVES, BJ = MP / 64;
   constexpr int OPERAND = 2 * MP * MP;  // elements: hi, then lo
@@ -88,7 +88,7 @@ __global__ __launch_bounds__(MP == 128 ? 512 : 256) void narrow_kernel(NarrowArg
   const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32 * BJ;
   _Float16* const first_operand = lds;
   _Float16* const second = lds + OPERAND;
-  const bool whole = a.part == NarrowPart::kWhole;
+  constexpr bool whole = PART == NarrowPart::kWhole;
   const int64_t total = a.end[a.count - 1];
 
   for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
@@ -98,48 +98,60 @@ __global__ __launch_bounds__(MP == 128 ? 512 : 256) void narrow_kernel(NarrowArg
     const int64_t local = w - (gi ? a.end[gi - 1] : 0);
     const bool tall = g.rows > g.cols;
     const int m = tall ? g.cols : g.rows, n = tall ? g.rows : g.cols;
-    const int parts = a.part == NarrowPart::kSum     ? g.splits
-                      : a.part == NarrowPart::kApply ? g.splits
-                                                     : 1;
+    const int parts = PART == NarrowPart::kSum || PART == NarrowPart::kApply ? g.splits : 1;
     const int64_t z = local / parts;
     const int split = static_cast<int>(local % parts);
     const int first = whole ? 0 : split * g.chunk;
     const int last = whole || first + g.chunk > n ? n : first + g.chunk;
     const int64_t source = z * g.matrix_stride;
 
-    // Element e of this thread in the block of columns c0 .. c0 + 63 of X
-    // (m x n): along the axis on which the matrix is contiguous.
+    // Element e of this thread in a block of 64 columns of X (m x n): along the
+    // axis on which the matrix is contiguous, a short row's 64 lanes shared by
+    // as many columns as fit. False, for the whole wave, past the block.
+    int log = 0;
+    while ((1 << log) < m && log < 6) ++log;
     auto place = [&](int e, int& i, int& c) {
       const int unit = wave + WAVES * e;
-      if (tall) {
-        c = MP == 128 ? unit >> 1 : unit;
-        i = MP == 128 ? lane + 64 * (unit & 1) : lane;
-      } else {
+      if (!tall) {
         c = lane;
         i = unit;
+        return unit < m;
       }
+      if (MP == 128) {
+        c = unit >> 1;
+        i = lane + 64 * (unit & 1);
+        return true;
+      }
+      c = (unit << (6 - log)) + (lane >> log);
+      i = lane & ((1 << log) - 1);
+      return (unit << (6 - log)) < 64;
     };
     // Raw elements, from inside the matrix whatever the place: a load under a
-    // condition would be waited for before the next is asked for.
+    // condition would be waited for before the next is asked for (measured: two
+    // and a half times the time of the whole sum).
     auto fetch = [&](Raw (&v)[PER], int c0) {
 #pragma unroll
       for (int e = 0; e < PER; ++e) {
         int i, c;
         place(e, i, c);
         i = i < m ? i : m - 1;
+        c = c < 64 ? c : 63;
         c = c0 + c < last ? c0 + c : last - 1;
-        v[e] = static_cast<const Raw*>(g.in)[source + (tall ? c * g.row_stride + i
-                                                            : i * g.row_stride + c)];
+        const Raw* from = static_cast<const Raw*>(g.in) + source;
+        if (tall && MP == 64) {
+          v[e] = from[c * g.row_stride + i];
+        } else {  // the row is the wave's
+          const int row = __builtin_amdgcn_readfirstlane(tall ? c : i);
+          v[e] = (from + row * g.row_stride)[static_cast<uint32_t>(tall ? i : c)];
+        }
       }
     };
-    auto value = [&](Raw v, int e, int c0) {
-      int i, c;
-      place(e, i, c);
-      return i < m && c0 + c < last ? decode<TYPE>(v) : 0.0f;
+    auto value = [&](Raw v, int i, int c) {
+      return i < m && c < last ? decode<TYPE>(v) : 0.0f;
     };
 
     double factor = 0.0;
-    if (a.part != NarrowPart::kFactor) {
+    if constexpr (PART != NarrowPart::kFactor) {
       double sum = 0.0;
       if (g.partial != nullptr) {
         for (int k = tid; k < g.partials; k += THREADS) sum += g.partial[z * g.partials + k];
@@ -149,7 +161,9 @@ __global__ __launch_bounds__(MP == 128 ? 512 : 256) void narrow_kernel(NarrowArg
           fetch(v, c0);
 #pragma unroll
           for (int e = 0; e < PER; ++e) {
-            const double x = value(v[e], e, c0);
+            int i, c;
+            const bool in = place(e, i, c);
+            const double x = in ? value(v[e], i, c0 + c) : 0.0f;
             sum += x * x;
           }
         }
@@ -167,13 +181,14 @@ __global__ __launch_bounds__(MP == 128 ? 512 : 256) void narrow_kernel(NarrowArg
     }
 
     // A block of X as an operand: rows i, summed over c (turned: rows c, summed
-    // over i).
+    // over i). Rows i past the last unit that place() gives stay as they were.
     auto put = [&](const Raw (&v)[PER], int c0, _Float16* to, bool turned) {
 #pragma unroll
       for (int e = 0; e < PER; ++e) {
         int i, c;
-        place(e, i, c);
-        const float x = static_cast<float>(static_cast<double>(value(v[e], e, c0)) * factor);
+        if (!place(e, i, c)) continue;
+        const float x =
+            static_cast<float>(static_cast<double>(value(v[e], i, c0 + c)) * factor);
         const _Float16 hi = static_cast<_Float16>(x);
         const int at = turned ? c * MP + slot<MP>(c, i >> 3) * 8 + (i & 7)
                               : i * 64 + slot<64>(i, c >> 3) * 8 + (c & 7);
@@ -182,37 +197,42 @@ __global__ __launch_bounds__(MP == 128 ? 512 : 256) void narrow_kernel(NarrowArg
       }
     };
 
-    // acc += P Q^T over K for the wave's 32 rows of P and blocks of 32 rows of
+    // acc += P Q^T over 16 * depth elements for the wave's 32 rows of P and blocks of 32 rows of
     // Q; low parts, hi lo and lo hi, in sums of their own, 2^11 times as large
     // (three chains of matrix instructions that do not wait for each other).
     auto multiply = [&](auto k_const, auto blocks, const _Float16* p, int p_lo, int p_row,
-                        const _Float16* q, int q_lo, int q_row, f32x16* acc, f32x16* low) {
+                        const _Float16* q, int q_lo, int q_row, int depth, f32x16* acc,
+                        f32x16* low) {
       constexpr int K = decltype(k_const)::value, BLOCKS = decltype(blocks)::value;
       const int r = p_row + (lane & 31);
       constexpr bool APART = BLOCKS == 1;  // two blocks have chains enough
+      constexpr int PAIR = BLOCKS == 1 ? 2 : 1;
       f32x16 other[BLOCKS] = {};
-#pragma unroll 2
-      for (int k = 0; k < K / 16; ++k) {
-        const int piece = 2 * k + (lane >> 5);
-        const _Float16* pp = p + r * K + slot<K>(r, piece) * 8;
-        const half8 ph = *reinterpret_cast<const half8*>(pp);
-        const half8 pl = *reinterpret_cast<const half8*>(pp + p_lo);
+#pragma unroll 1
+      for (int k0 = 0; k0 < depth; k0 += PAIR)
 #pragma unroll
-        for (int j = 0; j < BLOCKS; ++j) {
-          const int s = q_row + 32 * j + (lane & 31);
-          const _Float16* qq = q + s * K + slot<K>(s, piece) * 8;
-          const half8 qh = *reinterpret_cast<const half8*>(qq);
-          const half8 ql = *reinterpret_cast<const half8*>(qq + q_lo);
-          acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph, qh, acc[j], 0, 0, 0);
-          low[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph, ql, low[j], 0, 0, 0);
-          f32x16& last_low = APART ? other[j] : low[j];
-          last_low = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl, qh, last_low, 0, 0, 0);
+        for (int h = 0; h < PAIR; ++h) {
+          const int piece = 2 * (k0 + h) + (lane >> 5);
+          const _Float16* pp = p + r * K + slot<K>(r, piece) * 8;
+          const half8 ph = *reinterpret_cast<const half8*>(pp);
+          const half8 pl = *reinterpret_cast<const half8*>(pp + p_lo);
+#pragma unroll
+          for (int j = 0; j < BLOCKS; ++j) {
+            const int s = q_row + 32 * j + (lane & 31);
+            const _Float16* qq = q + s * K + slot<K>(s, piece) * 8;
+            const half8 qh = *reinterpret_cast<const half8*>(qq);
+            const half8 ql = *reinterpret_cast<const half8*>(qq + q_lo);
+            acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph, qh, acc[j], 0, 0, 0);
+            low[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ph, ql, low[j], 0, 0, 0);
+            f32x16& last_low = APART ? other[j] : low[j];
+            last_low = __builtin_amdgcn_mfma_f32_32x32x16_f16(pl, qh, last_low, 0, 0, 0);
+          }
         }
-      }
       if constexpr (APART)
 #pragma unroll
         for (int e = 0; e < 16; ++e) low[0][e] += other[0][e];
     };
+    const int deep = ((m + 31) >> 5) * 2;  // past m every operand is zero
     using Side = std::integral_constant<int, MP>;
     using Stage = std::integral_constant<int, 64>;
     using Blocks = std::integral_constant<int, BJ>;
@@ -223,7 +243,7 @@ __global__ __launch_bounds__(MP == 128 ? 512 : 256) void narrow_kernel(NarrowArg
     // P Q^T of two m x m operands, times 2^-e
     auto product = [&](const _Float16* p, const _Float16* q, int e, f32x16 (&out)[BJ]) {
       f32x16 acc[BJ] = {}, low[BJ] = {};
-      multiply(Side(), Blocks(), p, LO, wm, q, LO, wn, acc, low);
+      multiply(Side(), Blocks(), p, LO, wm, q, LO, wn, deep, acc, low);
       const float f = __builtin_ldexpf(1.0f, -e);
 #pragma unroll
       for (int j = 0; j < BJ; ++j)
@@ -251,7 +271,7 @@ __global__ __launch_bounds__(MP == 128 ? 512 : 256) void narrow_kernel(NarrowArg
       }
     };
 
-    if (whole || a.part == NarrowPart::kSum) {
+    if constexpr (whole || PART == NarrowPart::kSum) {
       f32x16 acc[BJ] = {}, low[BJ] = {};
       Raw v[PER];
       fetch(v, first);
@@ -260,14 +280,20 @@ __global__ __launch_bounds__(MP == 128 ? 512 : 256) void narrow_kernel(NarrowArg
         put(v, c0, lds + b * OPERAND, false);
         __syncthreads();
         if (c0 + 64 < last) fetch(v, c0 + 64);
-        multiply(Stage(), Blocks(), lds + b * OPERAND, XLO, wm, lds + b * OPERAND, XLO, wn, acc, low);
+        multiply(Stage(), Blocks(), lds + b * OPERAND, XLO, wm, lds + b * OPERAND, XLO, wn, 4,
+                 acc, low);
       }
       __syncthreads();
       const float f = __builtin_ldexpf(1.0f, -2 * a.plan.x);
 #pragma unroll
       for (int j = 0; j < BJ; ++j)
 #pragma unroll
-        for (int k = 0; k < 16; ++k) S[j][k] = (acc[j][k] + low[j][k] * 0x1p-11f) * f;
+        for (int k = 0; k < 16; ++k) {
+          const int row = wm + 8 * (k >> 2) + 4 * (lane >> 5) + (k & 3);
+          const int col = wn + 32 * j + (lane & 31);
+          // rows past m were not written: what their sums hold is not used
+          S[j][k] = row < m && col < m ? (acc[j][k] + low[j][k] * 0x1p-11f) * f : 0.0f;
+        }
       if (!whole) {
         float* to = g.gram + (z * g.splits + split) * (MP * MP) + wave * (BJ * 1024) + lane;
 #pragma unroll
@@ -276,17 +302,31 @@ __global__ __launch_bounds__(MP == 128 ? 512 : 256) void narrow_kernel(NarrowArg
           for (int k = 0; k < 16; ++k) to[(16 * j + k) * 64] = S[j][k];
       }
     }
-    if (a.part == NarrowPart::kFactor) {
-      for (int s = 0; s < g.splits; ++s) {
-        const float* from = g.gram + (z * g.splits + s) * (MP * MP) + wave * (BJ * 1024) + lane;
+    if (PART == NarrowPart::kFactor && wm < m && wn < m) {
+      // in the parts' order; several of them on their way at once
+      constexpr int AHEAD = 4 / BJ;
+      const float* from = g.gram + z * g.splits * (MP * MP) + wave * (BJ * 1024) + lane;
+      for (int s = 0; s < g.splits; s += AHEAD) {
+        f32x16 part[AHEAD][BJ];
 #pragma unroll
-        for (int j = 0; j < BJ; ++j)
+        for (int u = 0; u < AHEAD; ++u) {
+          const int t = s + u < g.splits ? s + u : g.splits - 1;
 #pragma unroll
-          for (int k = 0; k < 16; ++k) S[j][k] += from[(16 * j + k) * 64];
+          for (int j = 0; j < BJ; ++j)
+#pragma unroll
+            for (int k = 0; k < 16; ++k) part[u][j][k] = from[t * (MP * MP) + (16 * j + k) * 64];
+        }
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+          if (s + u < g.splits)
+#pragma unroll
+            for (int j = 0; j < BJ; ++j)
+#pragma unroll
+              for (int k = 0; k < 16; ++k) S[j][k] += part[u][j][k];
       }
     }
 
-    if (whole || a.part == NarrowPart::kFactor) {
+    if constexpr (whole || PART == NarrowPart::kFactor) {
       store(S, first_operand, a.plan.step[0].s);
       __syncthreads();
 #pragma unroll 1
@@ -344,7 +384,7 @@ __global__ __launch_bounds__(MP == 128 ? 512 : 256) void narrow_kernel(NarrowArg
       }
     }
 
-    if (whole || a.part == NarrowPart::kApply) {
+    if constexpr (whole || PART == NarrowPart::kApply) {
       if (!whole) {
         const half8* from = reinterpret_cast<const half8*>(g.q + z * OPERAND);
         for (int k = tid; k < OPERAND / 8; k += THREADS)
@@ -358,6 +398,10 @@ __global__ __launch_bounds__(MP == 128 ? 512 : 256) void narrow_kernel(NarrowArg
           __builtin_ldexpf(1.0f, -(a.plan.x + a.plan.step[a.plan.steps - 1].q));
       Raw v[PER];
       fetch(v, first);
+      // the rows past m are summed over here, against zeros of Q
+      for (int k = tid; k < 4 * XLO / 8; k += THREADS)
+        reinterpret_cast<half8*>(second)[k] = half8{};
+      __syncthreads();
       int b = 0;
       for (int c0 = first; c0 < last; c0 += 64, b ^= 1) {
         _Float16* x = second + b * 2 * XLO;
@@ -365,32 +409,37 @@ __global__ __launch_bounds__(MP == 128 ? 512 : 256) void narrow_kernel(NarrowArg
         __syncthreads();
         if (c0 + 64 < last) fetch(v, c0 + 64);
         f32x16 acc[1] = {}, low[1] = {};
-        if (tall) multiply(Side(), One(), x, XLO, wj, first_operand, LO, wi, acc, low);
-        else multiply(Side(), One(), first_operand, LO, wi, x, XLO, wj, acc, low);
+        multiply(Side(), One(), tall ? x : first_operand, tall ? XLO : LO, tall ? wj : wi,
+                 tall ? first_operand : x, tall ? LO : XLO, tall ? wi : wj, deep, acc, low);
         const int rows = tall ? last : m, cols = tall ? m : last;
         const int row0 = (tall ? c0 + wj : wi) + 4 * (lane >> 5);
         const int col = (tall ? wi : c0 + wj) + (lane & 31);
+        // register k holds row row0 + 8 (k / 4) + k % 4
+        auto down = [](int k) { return 8 * (k >> 2) + (k & 3); };
+        const bool col_in = col < cols;
+        float* const master = g.master + ((z * g.rows + row0) * g.cols + col);
         float p[16];
         if (g.master != nullptr) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const int row = row0 + 8 * (k >> 2) + (k & 3);
-            p[k] = g.master[(z * g.rows + (row < rows ? row : rows - 1)) * g.cols +
-                            (col < cols ? col : cols - 1)];
-          }
+          for (int k = 0; k < 16; ++k)  // from inside the matrix, as in fetch
+            p[k] = *(col_in && row0 + down(k) < rows
+                         ? master + static_cast<int64_t>(down(k)) * g.cols
+                         : g.master);
         }
+        const int64_t stride = g.master != nullptr ? g.cols : g.out_row_stride;
+        uint16_t* const out =
+            static_cast<uint16_t*>(g.out) +
+            (g.master != nullptr ? (z * g.rows + row0) * g.cols
+                                 : z * g.out_matrix_stride + row0 * g.out_row_stride) + col;
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          const int row = row0 + 8 * (k >> 2) + (k & 3);
+          const bool in = col_in && row0 + down(k) < rows;
           float o = (acc[0][k] + low[0][k] * 0x1p-11f) * f;
-          int64_t at = z * g.out_matrix_stride + row * g.out_row_stride + col;
           if (g.master != nullptr) {
-            at = (z * g.rows + row) * g.cols + col;
             o = p[k] * a.plan.decay - g.step * o;
-            if (row < rows && col < cols) g.master[at] = o;
+            if (in) master[static_cast<int64_t>(down(k)) * g.cols] = o;
           }
-          if (g.out != nullptr && row < rows && col < cols)
-            static_cast<uint16_t*>(g.out)[at] = bits16(o, a.plan.out_type);
+          if (g.out != nullptr && in) out[down(k) * stride] = bits16(o, a.plan.out_type);
         }
       }
     }
@@ -398,14 +447,40 @@ __global__ __launch_bounds__(MP == 128 ? 512 : 256) void narrow_kernel(NarrowArg
   }
 }
 
-template <int MP, int TYPE>
+template <int MP, int TYPE, NarrowPart PART>
 hipError_t launch(NarrowArgs& a, int64_t total, hipStream_t stream, int64_t max_grid) {
   int64_t grid = total < kMaxWorkgroups ? total : kMaxWorkgroups;
   if (grid > max_grid) grid = max_grid;
   void* params[] = {&a};
-  return hipLaunchKernel(reinterpret_cast<const void*>(&narrow_kernel<MP, TYPE>),
+  return hipLaunchKernel(reinterpret_cast<const void*>(&narrow_kernel<MP, TYPE, PART>),
                          dim3(static_cast<unsigned>(grid)), dim3(MP == 128 ? 512 : 256), params, 0,
                          stream);
+}
+
+template <int MP, NarrowPart PART>
+hipError_t launch_type(NarrowArgs& a, int64_t total, int type, hipStream_t stream,
+                       int64_t max_grid) {
+  return type == kFp32   ? launch<MP, kFp32, PART>(a, total, stream, max_grid)
+         : type == kFp16 ? launch<MP, kFp16, PART>(a, total, stream, max_grid)
+                         : launch<MP, kBf16, PART>(a, total, stream, max_grid);
+}
+
+template <int MP>
+hipError_t launch_part(NarrowArgs& a, int64_t total, int type, NarrowPart part,
+                       hipStream_t stream, int64_t max_grid) {
+  switch (part) {
+    case NarrowPart::kWhole:
+      if constexpr (MP == 64)
+        return launch_type<MP, NarrowPart::kWhole>(a, total, type, stream, max_grid);
+      else
+        return hipErrorInvalidValue;
+    case NarrowPart::kSum:
+      return launch_type<MP, NarrowPart::kSum>(a, total, type, stream, max_grid);
+    case NarrowPart::kFactor:  // reads sums, not directions
+      return launch<MP, kFp32, NarrowPart::kFactor>(a, total, stream, max_grid);
+    default:
+      return launch_type<MP, NarrowPart::kApply>(a, total, type, stream, max_grid);
+  }
 }
 
 }  // namespace
@@ -424,14 +499,8 @@ hipError_t launch_narrow(const NarrowGroup* groups, int count, int side, int typ
   a.plan = plan;
   a.skip = skip;
   a.count = count;
-  a.part = part;
-  if (side == 64)
-    return type == kFp32   ? launch<64, kFp32>(a, total, stream, max_grid)
-           : type == kFp16 ? launch<64, kFp16>(a, total, stream, max_grid)
-                           : launch<64, kBf16>(a, total, stream, max_grid);
-  return type == kFp32   ? launch<128, kFp32>(a, total, stream, max_grid)
-         : type == kFp16 ? launch<128, kFp16>(a, total, stream, max_grid)
-                         : launch<128, kBf16>(a, total, stream, max_grid);
+  return side == 64 ? launch_part<64>(a, total, type, part, stream, max_grid)
+                    : launch_part<128>(a, total, type, part, stream, max_grid);
 }
 
 }  // namespace la
