@@ -169,6 +169,20 @@ __device__ __forceinline__ half8 keep(half8 h, u32x4 mask) {
   return __builtin_bit_cast(half8, __builtin_bit_cast(u32x4, h) & mask);
 }
 
+// What no later product reads passes by the caches: lo, X's reading in the
+// epilogue, the result (5120 x 17408: an update in 975 us instead of 1000). X
+// itself, in both layouts, and A and B do not: X X^T after a turned X stored so
+// took 13 % longer.
+template <typename T>
+__device__ __forceinline__ T load_once(const void* p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const T*>(p));
+}
+
+template <typename T>
+__device__ __forceinline__ void store_through(T v, void* p) {
+  __builtin_nontemporal_store(v, reinterpret_cast<T*>(p));
+}
+
 // What the epilogue reads for eight neighbours of one row: loaded ahead of the
 // sums' exchange, so that its latency is paid once for four rows of a lane.
 template <Product WHAT>
@@ -186,9 +200,13 @@ __device__ __forceinline__ void load_operands(Operands<WHAT>& x, const ProductGr
     const int r = row < g.M ? row : g.M - 1;
     const int c = col < g.ldc ? col : g.ldc - 8;
     const int64_t at = z * g.c_stride + static_cast<int64_t>(r) * g.ldc + c;
-    x.hi = *reinterpret_cast<const half8*>(reinterpret_cast<const _Float16*>(g.hi) + at);
+    const half_bits* hi = g.hi + at;
+    if constexpr (WHAT == Product::kUpdate || WHAT == Product::kOut)
+      x.hi = load_once<half8>(hi);
+    else
+      x.hi = *reinterpret_cast<const half8*>(hi);
     if constexpr (WHAT == Product::kUpdate)
-      x.lo = *reinterpret_cast<const u32x2*>(g.lo + at);
+      x.lo = load_once<u32x2>(g.lo + at);
     if (WHAT == Product::kSquare || !g.tall) x.diag = g.diag[z * g.diag_stride + r];
     if constexpr (WHAT == Product::kMuon) {
       if (row < g.M && col < g.N) {
@@ -250,7 +268,7 @@ __device__ __forceinline__ half8 finish(const ProductGroup& g, const ProductScal
       l[e >> 2] |= (static_cast<uint32_t>(low_byte(v, h[e])) & 0xFFu) << (8 * (e & 3));
     }
     if (g.c_lo != nullptr && row_in && col < g.ldc)
-      *reinterpret_cast<u32x2*>(g.c_lo + at) = l;
+      store_through(l, g.c_lo + at);
   } else if (row_in && col < g.N) {
     const bool whole = g.vectors && col + 8 <= g.N;
     float v[8];
@@ -281,7 +299,7 @@ __device__ __forceinline__ half8 finish(const ProductGroup& g, const ProductScal
     }
     if constexpr (OUT >= 0) {
       if (whole) {
-        *reinterpret_cast<u16x8*>(o) = w;
+        store_through(w, o);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
