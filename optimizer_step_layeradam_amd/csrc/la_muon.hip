@@ -184,6 +184,7 @@ struct DirectionArgs {
   const int32_t* skip;
   float scale;
   int32_t count;
+  int32_t strip;  // normalise: tiles of a workgroup
 };
 static_assert(sizeof(DirectionArgs) <= 4096, "kernel arguments");
 
@@ -247,6 +248,7 @@ __global__ __launch_bounds__(kThreads) void square_sum_kernel(DirectionArgs a) {
           sum += part;
         }
       } else {
+#pragma unroll 4
         for (int k = threadIdx.x % across; k < pieces; k += across) {
           const double x = element<TYPE>(g.in, row + k);
           sum += x * x;
@@ -258,11 +260,11 @@ __global__ __launch_bounds__(kThreads) void square_sum_kernel(DirectionArgs a) {
   }
 }
 
-// A strip of 64 rows and up to kStrip tiles of 64 columns of X_0 =
+// A strip of 64 rows and up to `strip` tiles of 64 columns of X_0 =
 // U / max(||U||_F, eps) per workgroup, in both layouts (the turned one through
 // LDS), zeros in the padding. A norm that is not finite makes every element
 // NaN, as the products would anyway. A thread takes eight neighbours of a row.
-constexpr int kStrip = 4;
+constexpr int kStrip = 4;  // one where the launch has few tiles: latency counts there
 
 template <int TYPE>
 __global__ __launch_bounds__(kThreads) void normalise_kernel(DirectionArgs a) {
@@ -277,11 +279,11 @@ __global__ __launch_bounds__(kThreads) void normalise_kernel(DirectionArgs a) {
     const DirectionGroup& g = a.g[i];
     const int64_t local = w - (i ? a.end[i - 1] : 0);
     const int tiles = g.ld_straight >> 6, down = g.ld_turned >> 6;
-    const int across = (tiles + kStrip - 1) / kStrip;
+    const int across = (tiles + a.strip - 1) / a.strip;
     const int64_t z = local / (across * down);
     const int t = static_cast<int>(local % (across * down));
-    const int r0 = (t / across) * 64, first = (t % across) * kStrip;
-    const int last = first + kStrip < tiles ? first + kStrip : tiles;
+    const int r0 = (t / across) * 64, first = (t % across) * a.strip;
+    const int last = first + a.strip < tiles ? first + a.strip : tiles;
 
     double sum = 0.0;
     for (int k = threadIdx.x; k < g.partials; k += kThreads) sum += g.partial[z * g.partials + k];
@@ -309,12 +311,13 @@ __global__ __launch_bounds__(kThreads) void normalise_kernel(DirectionArgs a) {
             for (int e = 0; e < 8; ++e) x[e] = v[e];
           } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = c0 + e < g.cols ? element<TYPE>(g.in, at + e) : 0.0f;
+            for (int e = 0; e < 8; ++e)  // from inside the row: see the zeros below
+              x[e] = element<TYPE>(g.in, at - c0 + (c0 + e < g.cols ? c0 + e : g.cols - 1));
           }
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             x[e] = static_cast<float>(static_cast<double>(x[e]) * factor);
-            if (c0 + e >= g.cols) x[e] = 0.0f;  // zero times NaN
+            if (c0 + e >= g.cols) x[e] = 0.0f;
             hi[e] = static_cast<_Float16>(x[e]);
             lo[e >> 2] |= (static_cast<uint32_t>(low_byte(x[e], hi[e])) & 0xFFu) << (8 * (e & 3));
           }
@@ -386,9 +389,14 @@ hipError_t launch_normalise(const DirectionGroup* groups, int count, int type, f
                             int64_t max_grid) {
   DirectionArgs a = {};
   int64_t total = 0;
+  for (int i = 0; i < count; ++i)
+    total += static_cast<int64_t>(groups[i].ld_straight >> 6) * (groups[i].ld_turned >> 6) *
+             groups[i].count;
+  a.strip = total < 4096 ? 1 : kStrip;
+  total = 0;
   for (int i = 0; i < count; ++i) {
     a.g[i] = groups[i];
-    const int across = ((groups[i].ld_straight >> 6) + kStrip - 1) / kStrip;
+    const int across = ((groups[i].ld_straight >> 6) + a.strip - 1) / a.strip;
     total += static_cast<int64_t>(across) * (groups[i].ld_turned >> 6) * groups[i].count;
     a.end[i] = total;
   }

@@ -3,7 +3,6 @@
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
-#include <stdlib.h>
 
 #include <algorithm>
 #include <type_traits>
@@ -563,16 +562,18 @@ __global__ __launch_bounds__(64 * WM * WN, MT * NT == 8 ? 2 : 1) void product_ke
         _Float16* to = reinterpret_cast<_Float16*>(SYM ? g.c : g.turned) +
                        static_cast<int64_t>(z) * (SYM ? g.c_stride : g.turned_stride);
         const int ld = SYM ? g.ldc : g.ld_turned;
-        const int r = (lane & 7) * 8;
+        // 64 rows (32 where the wave has no more) and a column per lane
+        constexpr int ACROSS = MT > 1 ? 8 : 4;
+        const int r = (lane % ACROSS) * 8;
 #pragma unroll 2
-        for (int p = 0; p < 8; ++p) {
-          const int k = 8 * p + (lane >> 3);
+        for (int p = 0; p < ACROSS; ++p) {
+          const int k = (64 / ACROSS) * p + lane / ACROSS;
 #pragma unroll
-          for (int c = 0; c < MT / 2; ++c) {
+          for (int c = 0; c < (MT + 1) / 2; ++c) {
             half8 h;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              h[e] = turn[(64 * c + r + e) * 128 + ((p ^ (lane & 7)) << 3) + (lane >> 3)];
+              h[e] = turn[(64 * c + r + e) * 128 + (((k >> 3) ^ (lane % ACROSS)) << 3) + (k & 7)];
             const int row = rowc + 64 * c + r;
             if (colw + k < g.N && row < ld)
               *reinterpret_cast<half8*>(to + static_cast<int64_t>(colw + k) * ld + row) = h;
@@ -623,20 +624,25 @@ template <Product WHAT, int OUT>
 hipError_t launch_one(const ProductGroup* groups, int count, const ProductScales& s,
                       const int32_t* skip, hipStream_t stream, int64_t max_grid) {
   constexpr bool SYM = WHAT == Product::kGram || WHAT == Product::kSquare;
-  // A workgroup has a compute unit to itself in either size, and one of the
-  // large tile takes 5/3 of the time of a small one (K = 4096: 84 us to 50 us):
-  // the size whose rounds over the 256 compute units take less.
-  auto rounds = [&](int64_t side) {
+  // A workgroup has a compute unit to itself, or half of one in the smallest
+  // tile. One of 256 x 256 takes 5/3 of the time of one of 128 x 128 (K = 4096:
+  // 84 us to 50 us), and that half as much again as one of 64 x 64 (K = 256: 12
+  // us to 8 us; 4096 x 2560, where 820 small tiles make two rounds and 210 of
+  // 128 one: 49 us to 61 us): the size whose rounds take least.
+  auto rounds = [&](int64_t side, int64_t slots) {
     int64_t tiles = 0;
     for (int i = 0; i < count; ++i) {
       const int64_t tm = (groups[i].M + side - 1) / side, tn = (groups[i].N + side - 1) / side;
       tiles += (SYM ? tm * (tm + 1) / 2 : tm * tn) * groups[i].count;
     }
-    return (tiles + 255) / 256;
+    return (tiles + slots - 1) / slots;
   };
-  static const int force = [] { const char* e = getenv("LA_TILE"); return e ? atoi(e) : 0; }();
-  if (force ? force == 256 : 5 * rounds(256) < 3 * rounds(128))
+  const int64_t large = 5 * rounds(256, 256), medium = 3 * rounds(128, 256),
+                small = 2 * rounds(64, 512);
+  if (large < medium && large < small)
     return launch_tile<WHAT, OUT, 4, 4, 2, 2, 64, 2>(groups, count, s, skip, stream, max_grid);
+  if (small < medium)
+    return launch_tile<WHAT, OUT, 1, 2, 2, 1, 64, 4>(groups, count, s, skip, stream, max_grid);
   return launch_tile<WHAT, OUT, 2, 2, 2, 2, 64, 4>(groups, count, s, skip, stream, max_grid);
 }
 
