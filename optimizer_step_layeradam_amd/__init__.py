@@ -793,6 +793,12 @@ def _allocate_workspace(needed: int, stream):
         return torch.empty(max(1, needed), dtype=torch.uint8, device="cuda")
 
 
+def _is_capturing(stream) -> bool:
+    import torch
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _element_type_of(tensors, what: str, allowed) -> int:
     kinds = {t.dtype for t in tensors}
     if len(kinds) == 1 and next(iter(kinds)) in allowed:
@@ -958,7 +964,8 @@ class MuonLayer:
     grads:  per tensor a list of R gradient replicas (all bf16 or all fp16).
     workspace: a uint8 CUDA tensor of at least workspace_bytes(), for layers
             that are stepped one after the other on one stream to share;
-            default: one of the layer's own, taken at the first step.
+            default: one of the layer's own, taken at the first step (a
+            captured step needs the layer as long as its graph is replayed).
     """
 
     def __init__(self, params, grads, workspace=None):
@@ -971,6 +978,7 @@ class MuonLayer:
         self._given = workspace is not None
         self._workspace = workspace
         self._stream = None
+        self._captured = []  # workspaces that captured steps use
 
     def workspace_bytes(self, *, nesterov: bool = True, coefficients=None) -> int:
         hp = make_muon_params(0.0, nesterov=nesterov, polynomial=make_polynomial(coefficients))
@@ -993,7 +1001,10 @@ class MuonLayer:
             needed = muon_workspace_bytes_raw(self._desc, hp)
             if self._workspace is None or self._workspace.numel() < needed:
                 self._workspace, self._stream = _allocate_workspace(needed, s), s
-            elif self._stream != s and not torch.cuda.is_current_stream_capturing():
+            capturing = _is_capturing(s)
+            if capturing and all(w is not self._workspace for w in self._captured):
+                self._captured.append(self._workspace)
+            elif self._stream != s and not capturing:
                 self._workspace.record_stream(s)
         muon_step_raw(self._desc, hp, _flag_ptr(overflow_flag),
                       _flag_ptr(skip_if_nonzero, "skip_if_nonzero"),

@@ -254,3 +254,23 @@ def test_step_captured_by_itself():
         graph.replay()
         torch.cuda.synchronize()
         steps.check(params, ref)
+
+
+def test_a_captured_step_keeps_its_workspace():
+    """A later step that needs more takes a new workspace; the old one stays
+    the graph's."""
+    params, grads = steps.make([(150, 260)], 1, torch.bfloat16, None, seed=240)
+    layer = la.MuonLayer(params, grads)
+    small = dict(lr=1e-2, nesterov=False, coefficients=((1.5, -0.5, 0.0),))
+    layer.step(**small)
+    size, place = layer._workspace.numel(), layer._workspace.data_ptr()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer.step(**small)
+    layer.step(lr=1e-2)
+    assert layer._workspace.numel() > size
+    others = [torch.full((size,), 0xA5, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert all(t.data_ptr() != place for t in others)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.all(t == 0xA5) for t in others)
