@@ -320,10 +320,10 @@ LA_API la_status la_direction_probe(const la_layer_desc *layer, int32_t part,
  * with s by la_lr_scale. Norm scales, biases and embeddings of a layer take
  * layer_adam_step.
  *
- * Numerics. ||U||_F is summed in FP64. X is held as a pair of FP16 numbers
- * (22 significant bits) under power-of-two scales that the host derives from
- * the coefficients, so that nothing overflows; the products multiply the
- * upper 11 bits with FP32 sums. O is within about 0.2 % (2-norm of the
+ * Numerics. ||U||_F is summed in FP64. X is held as an FP16 number and the
+ * eight bits that follow (19 significant bits) under power-of-two scales that
+ * the host derives from the coefficients, so that nothing overflows; the
+ * products multiply the FP16 parts with FP32 sums. O is within about 0.2 % (2-norm of the
  * difference over 2-norm of O, default coefficients) of the polynomial in
  * FP64, also for matrices of low rank or of a wide range of singular
  * values. The same call with the same inputs gives the same bits. Matrices

@@ -129,6 +129,14 @@ __device__ __forceinline__ void triangle(int t, int tiles_m, int& i, int& j) {
 // ahead; before the last step's products it waits for its own copies and
 // meets the others, so that the next stage's first fragments arrive under
 // these products.
+//
+// In 256 x 256 tiles a wave reads 8 fragments from LDS for 16 products, in 128 x
+// 128 ones 4 for 4; the large tile takes all of a compute unit's registers, so
+// nothing runs under its epilogue. Measured on 5120 x 17408, in 256 x 256
+// tiles: X X^T (210 tiles on 256 compute units) 415 us, 1.15 PFLOP/s of what
+// the tiles compute; B X with its update (1360 tiles) 942 us, 0.97 PFLOP/s, the
+// epilogue's 8 bytes an element among it; the last step 840 us, 1.09 PFLOP/s.
+// The matrix units are busy 50 to 58 % of the time, at 1.9 GHz.
 
 template <int MT, int NT, int WM, int WN, int DEPTH, int BUFFERS>
 struct Tile {
