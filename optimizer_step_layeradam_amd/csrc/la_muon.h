@@ -189,6 +189,16 @@ hipError_t launch_narrow(const NarrowGroup* groups, int count, int side, int typ
                          NarrowPart part, const NarrowPlan& plan, const int32_t* skip,
                          hipStream_t stream, int64_t max_grid);
 
+// x as it is in binary32, before it is split into hi and what follows. Without
+// it the compiler may form hi from x's last operation in one rounding, once for
+// the store and not for the difference x - hi: where the two roundings to
+// binary16 part, one element in some thousands, what follows is that of
+// another hi, and X is off by 2^-11 there.
+__device__ __forceinline__ float settled(float x) {
+  asm("" : "+v"(x));
+  return x;
+}
+
 // The byte that follows hi = binary16(x). Where hi is below the format's normal
 // range the byte saturates: the error stays under half of hi's spacing there,
 // 2^-25 of the scaled value.

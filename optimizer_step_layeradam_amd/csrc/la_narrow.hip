@@ -20,10 +20,10 @@
 // the accumulators' layout, and pass through LDS (two operands of 64 KiB) to be
 // multiplied. They are symmetric up to rounding, so the layout's four
 // consecutive rows of one column are stored as four consecutive columns of one
-// row. A chain of dependent products decides there: 79 us for five steps at
-// 128 x 128, some 2.5 us a product; one 64 x 64 matrix, all parts in one
-// workgroup, 41 us. The parts over X are bound by its conversion and by LDS: S
-// of 40 matrices of 128 x 5120 takes 61 us, Q X 92 us (52 MB each way).
+// row. A chain of dependent products decides there: 74 us for five steps at
+// 128 x 128, under 4 us a product; one 64 x 64 matrix, all parts in one
+// workgroup, 40 us. The parts over X are bound by its conversion and by LDS: S
+// of 40 matrices of 128 x 5120 takes 58 us, Q X 80 us (52 MB each way).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -110,21 +110,22 @@ void narrow_kernel(NarrowArgs a) {
 
     // Element e of this thread in a block of 64 columns of X (m x n): along the
     // axis on which the matrix is contiguous, a short row's 64 lanes shared by
-    // as many columns as fit. False, for the whole wave, past the block.
+    // as many columns as fit, and eight neighbours of the other axis in a row.
+    // False, for the whole wave, past the block.
     int log = 0;
     while ((1 << log) < m && log < 6) ++log;
     auto place = [&](int e, int& i, int& c) {
-      const int unit = wave + WAVES * e;
       if (!tall) {
         c = lane;
-        i = unit;
-        return unit < m;
+        i = 8 * (wave + WAVES * (e >> 3)) + (e & 7);
+        return i < m;
       }
       if (MP == 128) {
-        c = unit >> 1;
-        i = lane + 64 * (unit & 1);
+        c = 8 * wave + (e & 7);
+        i = lane + 64 * (e >> 3);
         return true;
       }
+      const int unit = wave + WAVES * e;
       c = (unit << (6 - log)) + (lane >> log);
       i = lane & ((1 << log) - 1);
       return (unit << (6 - log)) < 64;
@@ -182,21 +183,50 @@ void narrow_kernel(NarrowArgs a) {
       if (denominator > 0.0) factor = __builtin_ldexp(1.0, a.plan.x) / denominator;
       if (!(sum < __builtin_inf())) factor = __builtin_nan("");
     }
+    // As a power of two and a binary32 number in [1/2, 1): its rounding scales the
+    // whole matrix by 1 + 2^-25 at most, and no x is out of range on the way.
+    const int factor_exponent = __builtin_amdgcn_frexp_exp(factor);
+    const float factor_mantissa = static_cast<float>(__builtin_amdgcn_frexp_mant(factor));
 
     // A block of X as an operand: rows i, summed over c (turned: rows c, summed
-    // over i). Rows i past the last unit that place() gives stay as they were.
+    // over i). Rows i past the last one that place() gives stay as they were.
+    // Where a thread's neighbours are a row's, eight go to LDS at once (40 of 128
+    // x 5120: Q X in 80 us, 91 us one by one).
     auto put = [&](const Raw (&v)[PER], int c0, _Float16* to, bool turned) {
+      auto split = [&](int e, int i, int c, _Float16& hi, _Float16& lo) {
+        const float x = settled(
+            __builtin_ldexpf(value(v[e], i, c0 + c), factor_exponent) * factor_mantissa);
+        hi = static_cast<_Float16>(x);
+        lo = static_cast<_Float16>((x - static_cast<float>(hi)) * 0x1p11f);
+      };
+      if (turned ? !tall : tall && MP == 128) {
+#pragma unroll
+        for (int h = 0; h < PER / 8; ++h) {
+          half8 hi, lo;
+          int i, c;
+          if (!place(8 * h, i, c)) continue;
+          const int at = turned ? c * MP + slot<MP>(c, i >> 3) * 8
+                                : i * 64 + slot<64>(i, c >> 3) * 8;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            _Float16 a, b;
+            place(8 * h + e, i, c);
+            split(8 * h + e, i, c, a, b);
+            hi[e] = a;
+            lo[e] = b;
+          }
+          *reinterpret_cast<half8*>(to + at) = hi;
+          *reinterpret_cast<half8*>(to + XLO + at) = lo;
+        }
+        return;
+      }
 #pragma unroll
       for (int e = 0; e < PER; ++e) {
         int i, c;
         if (!place(e, i, c)) continue;
-        const float x =
-            static_cast<float>(static_cast<double>(value(v[e], i, c0 + c)) * factor);
-        const _Float16 hi = static_cast<_Float16>(x);
         const int at = turned ? c * MP + slot<MP>(c, i >> 3) * 8 + (i & 7)
                               : i * 64 + slot<64>(i, c >> 3) * 8 + (c & 7);
-        to[at] = hi;
-        to[XLO + at] = static_cast<_Float16>((x - static_cast<float>(hi)) * 0x1p11f);
+        split(e, i, c, to[at], to[XLO + at]);
       }
     };
 
@@ -263,7 +293,7 @@ void narrow_kernel(NarrowArgs a) {
           half4 hi, lo;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float x = v[j][4 * q + k] * f;
+            const float x = v[j][4 * q + k] * f;  // exact
             hi[k] = static_cast<_Float16>(x);
             lo[k] = static_cast<_Float16>((x - static_cast<float>(hi[k])) * 0x1p11f);
           }
@@ -349,21 +379,32 @@ void narrow_kernel(NarrowArgs a) {
         store(P, second, t.p);
         __syncthreads();
         if (more) {
-          // An operand stored from V holds V^T: T = S^T P, S <- P^T T, and its
-          // mirror image T^T P, which the two operands exchanged give bit for
-          // bit: their mean is symmetric.
+          // An operand stored from V holds V^T: T = S^T P, S <- P^T T; the mean
+          // of it and its mirror image, which comes turned through LDS, is
+          // symmetric.
           f32x16 T[BJ];
           product(first_operand, second, t.p + t.s, T);
           __syncthreads();
           store(T, first_operand, t.t);
           __syncthreads();
           product(second, first_operand, t.t + t.p, S);
-          product(first_operand, second, t.t + t.p, T);
+          __syncthreads();
+          float* const turn = reinterpret_cast<float*>(first_operand);
+          auto at = [&](int row, int col) { return row * MP + (col ^ (row & 31)); };
+#pragma unroll
+          for (int j = 0; j < BJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              turn[at(wm + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3),
+                      wn + 32 * j + (lane & 31))] = S[j][e];
           __syncthreads();
 #pragma unroll
           for (int j = 0; j < BJ; ++j)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) S[j][e] = 0.5f * (S[j][e] + T[j][e]);
+            for (int e = 0; e < 16; ++e)
+              S[j][e] = 0.5f * (S[j][e] + turn[at(wn + 32 * j + (lane & 31),
+                                                  wm + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3))]);
+          __syncthreads();
         }
         if (k == 0) {
 #pragma unroll

@@ -270,7 +270,8 @@ __device__ __forceinline__ half8 finish(const ProductGroup& g, const ProductScal
       const float hi = static_cast<float>(x.hi[e]);
       const int lo = static_cast<int>(x.lo[e >> 2] << (24 - 8 * (e & 3))) >> 24;
       const float d = s.diag * (g.tall ? dc[e] : x.diag);
-      const float v = fma(s.linear, with_low_byte(hi, lo), fma(d, hi, s.acc * sum[e]));
+      const float v =
+          settled(fma(s.linear, with_low_byte(hi, lo), fma(d, hi, s.acc * sum[e])));
       h[e] = static_cast<_Float16>(v);
       l[e >> 2] |= (static_cast<uint32_t>(low_byte(v, h[e])) & 0xFFu) << (8 * (e & 3));
     }
