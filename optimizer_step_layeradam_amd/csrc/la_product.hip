@@ -551,19 +551,22 @@ __global__ __launch_bounds__(64 * WM * WN, MT * NT == 8 ? 2 : 1) void product_ke
 #pragma unroll
         for (int p = 0; p < 4; ++p) x[p] = next[p];
         if (i + 1 < MT) load(i + 1);
+        float v[4][8];
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           const int r = 32 * i + 8 * p + (lane >> 3);
           const float* from = sums + r * 64 + (k8 ^ (((r >> 2) & 1) << 5));
-          float v[8];
-          *reinterpret_cast<f32x4*>(v) = *reinterpret_cast<const f32x4*>(from);
-          *reinterpret_cast<f32x4*>(v + 4) = *reinterpret_cast<const f32x4*>(from + 4);
+          *reinterpret_cast<f32x4*>(v[p]) = *reinterpret_cast<const f32x4*>(from);
+          *reinterpret_cast<f32x4*>(v[p] + 4) = *reinterpret_cast<const f32x4*>(from + 4);
+        }
+        if constexpr (TURN) wave_fence();
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const int r = 32 * i + 8 * p + (lane >> 3);
           const half8 h =
-              finish<WHAT, OUT>(g, a.s, z, rowc + r, colw + k8, v, x[p], dc, mask);
-          if constexpr (TURN) {
-            wave_fence();
+              finish<WHAT, OUT>(g, a.s, z, rowc + r, colw + k8, v[p], x[p], dc, mask);
+          if constexpr (TURN)
             *reinterpret_cast<half8*>(turn + r * 128 + (((lane & 7) ^ ((r >> 3) & 7)) << 3)) = h;
-          }
         }
       }
       if (mirror) {
