@@ -11,6 +11,7 @@ there is no fallback: without it every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -868,14 +869,17 @@ def orthogonalize(x, out=None, *, coefficients=None, eps: float = 1e-7, workspac
     coefficients: one triple (a, b, c) per step (default: NEWTON_SCHULZ).
     workspace: a uint8 CUDA tensor of at least orthogonalize_workspace_bytes()
        (default: taken from torch's allocator for the call).
-    Returns out.
+    Returns out. What the call allocates belongs to ``stream``, as if it were
+    the current one: wait for it before new outputs are used on another, and
+    record_stream() them there; the same holds for x on ``stream``.
     """
     import torch
     single = isinstance(x, torch.Tensor)
     xs = [x] if single else list(x)
     if out is None:
-        outs = [_empty_direction(t, torch.float16 if t.dtype == torch.float16 else
-                                 torch.bfloat16) for t in xs]
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            outs = [_empty_direction(t, torch.float16 if t.dtype == torch.float16 else
+                                     torch.bfloat16) for t in xs]
     else:
         outs = [out] if single else list(out)
         if len(outs) != len(xs):
