@@ -87,18 +87,16 @@ la_status derive_polynomial(const la_polynomial* p, Polynomial* out) {
         factor = std::max(factor, whole(q));
       }
     }
-    // a + 3 b q + 5 c q^2 = 0 at the inner extremes
+    // a + 3 b q + 5 c q^2 = 0 at the inner extremes. Both roots come from the sum
+    // that does not cancel: with a c far below b the other one would be lost.
     auto extreme = [&](double q) {
       if (q > 0.0 && q < end) next = std::max(next, value(q));
     };
-    if (c != 0.0) {
-      const double d = 9.0 * b * b - 20.0 * a * c;
-      if (d >= 0.0) {
-        extreme((-3.0 * b + std::sqrt(d)) / (10.0 * c));
-        extreme((-3.0 * b - std::sqrt(d)) / (10.0 * c));
-      }
-    } else if (b != 0.0) {
-      extreme(-a / (3.0 * b));
+    const double d = 9.0 * b * b - 20.0 * a * c;
+    if (d >= 0.0) {
+      const double t = -0.5 * (3.0 * b + std::copysign(std::sqrt(d), b));
+      if (c != 0.0) extreme(t / (5.0 * c));
+      if (t != 0.0) extreme(a / t);
     }
     if (!(next <= 0x1p20) || !(next >= 0x1p-20) || !(poly <= 0x1p40))
       return fail(LA_ERR_INVALID_ARGUMENT,
