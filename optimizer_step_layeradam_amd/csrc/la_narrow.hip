@@ -12,9 +12,10 @@
 // asks for is precision: an error in S grows by up to a^2 per step where the
 // singular values are small. Every operand here is a pair of binary16 numbers
 // (hi + lo / 2^11, 22 bits) under a power-of-two scale from the host's bounds,
-// every product the three hi hi + hi lo + lo hi with binary32 sums: measured
-// 1e-6 to 5e-4 of the direction over all spectra tried, less than the
-// step-by-step form's.
+// every product the three hi hi + hi lo + lo hi with binary32 sums. The long sums
+// of S_0 are binary32 over 64 columns and binary64 beyond: in binary32 alone, on
+// a matrix with one strong direction, the last bits of its sum would swallow the
+// others (520 of 4 x 20000 with a strong column: 49 % off).
 //
 // m x m matrices of up to 128 x 128 live in the registers of one workgroup, in
 // the accumulators' layout, and pass through LDS (two operands of 64 KiB) to be
@@ -305,7 +306,7 @@ void narrow_kernel(NarrowArgs a) {
     };
 
     if constexpr (whole || PART == NarrowPart::kSum) {
-      f32x16 acc[BJ] = {}, low[BJ] = {};
+      double total[BJ][16] = {};
       Raw v[PER];
       fetch(v, first);
       int b = 0;
@@ -313,11 +314,16 @@ void narrow_kernel(NarrowArgs a) {
         put(v, c0, lds + b * OPERAND, false);
         __syncthreads();
         if (c0 + 64 < last) fetch(v, c0 + 64);
+        f32x16 acc[BJ] = {}, low[BJ] = {};
         multiply(Stage(), Blocks(), lds + b * OPERAND, XLO, wm, lds + b * OPERAND, XLO, wn, 4,
                  acc, low);
+#pragma unroll
+        for (int j = 0; j < BJ; ++j)
+#pragma unroll
+          for (int k = 0; k < 16; ++k) total[j][k] += acc[j][k] + low[j][k] * 0x1p-11f;
       }
       __syncthreads();
-      const float f = __builtin_ldexpf(1.0f, -2 * a.plan.x);
+      const double f = __builtin_ldexp(1.0, -2 * a.plan.x);
 #pragma unroll
       for (int j = 0; j < BJ; ++j)
 #pragma unroll
@@ -325,7 +331,7 @@ void narrow_kernel(NarrowArgs a) {
           const int row = wm + 8 * (k >> 2) + 4 * (lane >> 5) + (k & 3);
           const int col = wn + 32 * j + (lane & 31);
           // rows past m were not written: what their sums hold is not used
-          S[j][k] = row < m && col < m ? (acc[j][k] + low[j][k] * 0x1p-11f) * f : 0.0f;
+          S[j][k] = row < m && col < m ? static_cast<float>(total[j][k] * f) : 0.0f;
         }
       if (!whole) {
         float* to = g.gram + (z * g.splits + split) * (MP * MP) + wave * (BJ * 1024) + lane;
@@ -338,6 +344,7 @@ void narrow_kernel(NarrowArgs a) {
     if (PART == NarrowPart::kFactor && wm < m && wn < m) {
       // in the parts' order; several of them on their way at once
       constexpr int AHEAD = 4 / BJ;
+      double sum[BJ][16] = {};
       const float* from = g.gram + z * g.splits * (MP * MP) + wave * (BJ * 1024) + lane;
       for (int s = 0; s < g.splits; s += AHEAD) {
         f32x16 part[AHEAD][BJ];
@@ -355,8 +362,12 @@ void narrow_kernel(NarrowArgs a) {
 #pragma unroll
             for (int j = 0; j < BJ; ++j)
 #pragma unroll
-              for (int k = 0; k < 16; ++k) S[j][k] += part[u][j][k];
+              for (int k = 0; k < 16; ++k) sum[j][k] += part[u][j][k];
       }
+#pragma unroll
+      for (int j = 0; j < BJ; ++j)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) S[j][k] = static_cast<float>(sum[j][k]);
     }
 
     if constexpr (whole || PART == NarrowPart::kFactor) {

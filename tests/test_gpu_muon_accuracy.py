@@ -1,0 +1,82 @@
+"""How far directions are from the polynomial in 64 bits, in 32 bits and on the
+spectra that are hardest on them: one singular value far above the others, so
+that what the others contribute to S = X X^T lies in its last bits.
+
+The direction comes out in FP32 as the step of a master of zeros: with lr 1, no
+scale, no decay and a momentum buffer of twice the matrix at momentum 1/2, whose
+product is exact.
+
+Tolerance of the narrow form (short side m in 17 .. 128), which iterates S in
+numbers of 22 bits: an error E in S enters a step's factor a + b S + c S^2 as b E, beside a,
+and grows by a^2 per step while S is small, so that the result is off by |b| / a
+(1 + a^2 + a^4 + a^6 + a^8) = 3.0e4 times its part along each small singular
+direction. Several roundings of half a step of 22 bits at most, adding as
+independent ones, make E's norm about one step, 2^-22 of S's; spread over m
+directions that is 2^-22 3.0e4 / m^(1/2) = 7.2e-3 / m^(1/2) of the result's norm.
+"""
+import pytest
+import torch
+
+import optimizer_step_layeradam_amd as la
+from muonhelpers import direction64
+
+pytestmark = pytest.mark.gpu
+
+A, B, _ = la.NEWTON_SCHULZ[0]
+GROWTH = abs(B) / A * sum(A ** (2 * k) for k in range(5))
+
+
+def narrow_bar(m):
+    return 2.0 ** -22 * GROWTH / m ** 0.5
+
+
+def dominated(shape, kind, eps, seed):
+    """(count, rows, cols): a matrix of rank one and noise eps times as strong."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+
+    def randn(*s):
+        return torch.randn(s, device="cuda", generator=gen)
+
+    k, r, c = shape
+    noise = randn(k, r, c)
+    if kind == "constant":
+        return 1 + eps * noise
+    if kind == "rank one":
+        return randn(k, r, 1) * randn(k, 1, c) + eps * noise
+    if kind == "column":  # of the long side: S_0's first 64 terms outweigh the rest
+        strong = (max(r, c) ** 0.5) / eps
+        if r <= c:
+            noise[:, :, 0] += strong
+        else:
+            noise[:, 0, :] += strong
+        return noise
+    return noise
+
+
+def direction(u):
+    m, p = (2 * u).contiguous(), torch.zeros_like(u)
+    g = torch.zeros_like(u, dtype=torch.bfloat16)
+    la.muon_step([(p, m)], [[g]], lr=1.0, momentum=0.5, nesterov=False, lr_scale="none")
+    return -p
+
+
+def worst(u):
+    want = direction64(u)
+    d = (direction(u).double() - want).flatten(1).norm(dim=1) / want.flatten(1).norm(dim=1)
+    return float(d.max())
+
+
+KINDS = [("constant", 0.03), ("constant", 0.01), ("constant", 0.001), ("rank one", 0.01),
+         ("column", 0.01), ("noise", 1.0)]
+
+# Long sums by one workgroup a matrix and in parts, wide and tall, sides of 64 and 128.
+NARROW = [(520, 17, 2000), (520, 64, 5120), (513, 4000, 33), (1, 20, 100000), (3, 64, 12000),
+          (8, 100, 3000), (2, 128, 30000), (1, 9000, 65), (40, 64, 64), (40, 17, 17)]
+
+
+@pytest.mark.parametrize("kind,eps", KINDS)
+@pytest.mark.parametrize("shape", NARROW, ids=str)
+def test_narrow(shape, kind, eps):
+    got, bar = worst(dominated(shape, kind, eps, sum(shape))), narrow_bar(min(shape[1:]))
+    print(f"  off {got:.2e} (bar {bar:.2e})", flush=True)
+    assert got <= bar
