@@ -148,6 +148,9 @@ hipError_t launch_product(const ProductGroup* groups, int count, Product what, i
 // Matrices whose short side is at most this take the iteration on S = X X^T.
 constexpr int kNarrow = 128;
 
+// Up to this side the iteration on S is binary64.
+constexpr int kTiny = 16;
+
 // Steps of a polynomial at most (LA_MAX_POLYNOMIAL_STEPS).
 constexpr int kMaxSteps = 16;
 
@@ -157,6 +160,7 @@ struct NarrowGroup {
   double* partial;          // count x partials sums of squares, or null: formed here
   float* gram;              // count x splits partial sums of S, in the accumulators' order
   half_bits* q;             // count x (hi, lo) of the polynomial's factor
+  double* sums;             // side kTiny: count x splits partial sums of U U^T
   void* out;                // result, or the compute copy or null
   float* master;            // the Muon step; null: the result goes to out
   int64_t row_stride, matrix_stride, out_row_stride, out_matrix_stride;
@@ -171,8 +175,9 @@ struct NarrowStep {
   int32_t s, p, t, q;  // exponents of the scales of S, P = a + b S + c S S, P S and Q = P ... P
 };
 
-// kWhole (side 64 only): all of it, one workgroup per matrix; kSum, kFactor, kApply: its
-// three parts, with as many workgroups as there is work for.
+// kWhole (sides kTiny and 64): all of it, one workgroup per matrix; kSum, kFactor, kApply:
+// its three parts, with as many workgroups as there is work for (side kTiny: kApply
+// forms the factor too).
 enum class NarrowPart { kWhole, kSum, kFactor, kApply };
 
 struct NarrowPlan {
@@ -184,7 +189,7 @@ struct NarrowPlan {
   int32_t out_type; // kBf16, kFp16, -1: none
 };
 
-// side: 64 or 128, at least every group's short side.
+// side: kTiny, 64 or 128, at least every group's short side.
 hipError_t launch_narrow(const NarrowGroup* groups, int count, int side, int type,
                          NarrowPart part, const NarrowPlan& plan, const int32_t* skip,
                          hipStream_t stream, int64_t max_grid);

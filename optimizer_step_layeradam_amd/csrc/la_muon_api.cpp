@@ -164,13 +164,13 @@ constexpr int64_t kSharedElements = int64_t(1) << 20;
 void choose_form(Stack& s, const Polynomial& p, bool beside_wide) {
   s.m = std::min(s.rows, s.cols);
   s.n = std::max(s.rows, s.cols);
-  const bool shares = beside_wide && s.n <= kWholeColumns &&
+  const bool shares = beside_wide && s.m > la::kTiny && s.n <= kWholeColumns &&
                       s.count * s.n * round_up(s.m, la::kDepth) <= kSharedElements;
   s.narrow = s.m <= la::kNarrow && p.growth <= kMostGrowth && !shares;
   if (!s.narrow) return;
-  s.side = s.m <= 64 ? 64 : 128;
+  s.side = s.m <= la::kTiny ? la::kTiny : s.m <= 64 ? 64 : 128;
   // 128 x 128 operands leave the whole form no registers
-  s.whole = s.side == 64 && (s.n <= kWholeColumns || s.count >= kWholeCount);
+  s.whole = s.side <= 64 && (s.n <= kWholeColumns || s.count >= kWholeCount);
   s.splits = std::min({(kParts + s.count - 1) / s.count, (s.n + 255) / 256, kMostParts});
   s.columns = round_up((s.n + s.splits - 1) / s.splits, 64);
   s.splits = (s.n + s.columns - 1) / s.columns;
@@ -230,8 +230,8 @@ int64_t lay_out(std::vector<Stack>& stacks, const Polynomial& p, bool direction,
       if (direction) s.direction = take(4 * k * s.numel_direction);
       if (!s.whole) {
         const int64_t square = static_cast<int64_t>(s.side) * s.side;
-        s.sums = take(4 * k * s.splits * square);
-        s.factors = take(2 * 2 * k * square);
+        s.sums = take((s.side == la::kTiny ? 8 : 4) * k * s.splits * square);
+        if (s.side != la::kTiny) s.factors = take(2 * 2 * k * square);
       }
       s.partial = take(8 * k * s.partials);
       continue;
@@ -373,7 +373,7 @@ la_status enqueue_narrow(const std::vector<Stack>& stacks, const Polynomial& p, 
     plan.step[k] = {static_cast<float>(t.a), static_cast<float>(t.b), static_cast<float>(t.c),
                     t.gram, t.factor, t.turn, t.whole};
   }
-  for (const int side : {64, 128})
+  for (const int side : {la::kTiny, 64, 128})
     for (const bool whole : {true, false}) {
       la::NarrowGroup g[la::kGroupsPerLaunch];
       int count = 0;
@@ -388,7 +388,7 @@ la_status enqueue_narrow(const std::vector<Stack>& stacks, const Polynomial& p, 
             launch(la::NarrowPart::kWhole);
           } else {
             launch(la::NarrowPart::kSum);
-            launch(la::NarrowPart::kFactor);
+            if (side != la::kTiny) launch(la::NarrowPart::kFactor);
             launch(la::NarrowPart::kApply);
           }
         }
@@ -405,6 +405,7 @@ la_status enqueue_narrow(const std::vector<Stack>& stacks, const Polynomial& p, 
         x.partial = place<double>(ws, s.partial);
         x.partials = s.partials;
         x.gram = place<float>(ws, s.sums);
+        x.sums = place<double>(ws, s.sums);
         x.q = place<uint16_t>(ws, s.factors);
         x.splits = static_cast<int32_t>(s.splits);
         x.chunk = static_cast<int32_t>(s.columns);
@@ -572,11 +573,11 @@ la_status orthogonalize(const la_matrices_desc* d, const la_polynomial* polynomi
   if ((st = check_disjoint(written, read)) != LA_OK) return st;
 
   hipStream_t stream = static_cast<hipStream_t>(hip_stream);
-  // the whole narrow form sums its squares itself
+  // the whole narrow form sums its squares itself, and so does that of side kTiny
   std::vector<Stack> wide, summed;
   for (const Stack& x : stacks) {
     if (!x.narrow) wide.push_back(x);
-    if (!x.narrow || !x.whole) summed.push_back(x);
+    if (!x.narrow || !(x.whole || x.side == la::kTiny)) summed.push_back(x);
   }
   auto directions = [&](const std::vector<Stack>& list, auto launch) -> la_status {
     for (size_t first = 0; first < list.size(); first += la::kGroupsPerLaunch) {

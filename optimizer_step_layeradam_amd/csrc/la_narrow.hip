@@ -502,14 +502,195 @@ void narrow_kernel(NarrowArgs a) {
   }
 }
 
+// ---- short sides up to 16 ----------------------------------------------------------
+// An error in S grows as above whatever the side, but on few directions it does
+// not spread: with pairs a 2 x 2 matrix comes out up to 0.4 % off, and the
+// step-by-step form's roundings up to 1.4 %. So S, its polynomial and the last
+// product are binary64 here, at 16 x 16 x 4 of a matrix instruction: lane l has
+// element (l / 16 + 4 r, l % 16) of a result in register r, and gives element (l %
+// 16, l / 16) of the left operand and (l / 16, l % 16) of the right one. Register r
+// of a symmetric result is therefore an operand as it is, for the four summed
+// positions l / 16 + 4 r: a wave multiplies 16 x 16 matrices without LDS, in four
+// dependent instructions, and every wave forms the factor for itself. The norm
+// is the trace of U U^T, so X is read twice in all.
+
+typedef double f64x4 __attribute__((ext_vector_type(4)));
+
+// P^T Q
+__device__ __forceinline__ f64x4 product16(f64x4 p, f64x4 q) {
+  f64x4 s = {};
+#pragma unroll
+  for (int r = 0; r < 4; ++r) s = __builtin_amdgcn_mfma_f64_16x16x4f64(p[r], q[r], s, 0, 0, 0);
+  return s;
+}
+
+template <int TYPE, NarrowPart PART>
+__global__ __launch_bounds__(256) void tiny_kernel(NarrowArgs a) {
+  using Raw = std::conditional_t<TYPE == kFp32, float, uint16_t>;
+  constexpr bool whole = PART == NarrowPart::kWhole;
+  constexpr int WAVES = 4, STRIP = 32;  // columns that a wave's eight instructions sum over
+  __shared__ double share[WAVES][kTiny * kTiny];
+  if (a.skip != nullptr && *a.skip != 0) return;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int down = lane >> 4, across = lane & 15;
+  const int64_t total = a.end[a.count - 1];
+
+  for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
+    int gi = 0;
+    while (w >= a.end[gi]) ++gi;
+    const NarrowGroup& g = a.g[gi];
+    const int64_t local = w - (gi ? a.end[gi - 1] : 0);
+    const bool tall = g.rows > g.cols;
+    const int m = tall ? g.cols : g.rows, n = tall ? g.rows : g.cols;
+    const int parts = whole ? 1 : g.splits;
+    const int64_t z = local / parts;
+    const int split = static_cast<int>(local % parts);
+    const int first = whole ? 0 : split * g.chunk;
+    const int last = whole || first + g.chunk > n ? n : first + g.chunk;
+    const Raw* const from = static_cast<const Raw*>(g.in) + z * g.matrix_stride;
+
+    // Element (i, c), i along the short side: loaded from inside the matrix
+    // whatever the place, so that no load waits for a condition.
+    auto fetch = [&](int i, int c) {
+      i = i < m ? i : m - 1;
+      c = c < last ? c : last - 1;
+      return from[tall ? c * g.row_stride + i : i * g.row_stride + c];
+    };
+    auto value = [&](Raw v, int i, int c) {
+      return i < m && c < last ? static_cast<double>(decode<TYPE>(v)) : 0.0;
+    };
+
+    f64x4 S = {};
+    if constexpr (whole || PART == NarrowPart::kSum) {
+      // neighbours along the axis on which the matrix is contiguous
+      auto column = [&](int e) { return tall ? 4 * e + down : 8 * down + e; };
+      Raw v[8];
+      auto load = [&](int c0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = fetch(across, c0 + column(e));
+      };
+      load(first + STRIP * wave);
+      for (int c0 = first + STRIP * wave; c0 < last; c0 += STRIP * WAVES) {
+        double x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = value(v[e], across, c0 + column(e));
+        load(c0 + STRIP * WAVES);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          S = __builtin_amdgcn_mfma_f64_16x16x4f64(x[e], x[e], S, 0, 0, 0);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) share[wave][64 * r + lane] = S[r];
+      __syncthreads();
+      if constexpr (!whole) {
+        double sum = share[0][tid];
+#pragma unroll
+        for (int k = 1; k < WAVES; ++k) sum += share[k][tid];
+        g.sums[(z * g.splits + split) * (kTiny * kTiny) + tid] = sum;
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          S[r] = share[0][64 * r + lane];
+#pragma unroll
+          for (int k = 1; k < WAVES; ++k) S[r] += share[k][64 * r + lane];
+        }
+      }
+    }
+    if constexpr (PART == NarrowPart::kApply) {
+      const double* parts_of = g.sums + z * g.splits * (kTiny * kTiny) + lane;
+#pragma unroll 4
+      for (int t = 0; t < g.splits; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[r] += parts_of[t * (kTiny * kTiny) + 64 * r];
+    }
+
+    if constexpr (whole || PART == NarrowPart::kApply) {
+      double trace = 0.0;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) trace += down + 4 * r == across ? S[r] : 0.0;
+#pragma unroll
+      for (int d = 32; d > 0; d >>= 1) trace += __shfl_xor(trace, d, 64);
+      const double norm = __builtin_sqrt(trace);
+      const double denominator = norm < a.plan.eps ? a.plan.eps : norm;  // NaN stays
+      double factor = denominator > 0.0 ? 1.0 / denominator : 0.0;
+      if (!(trace < __builtin_inf())) factor = __builtin_nan("");
+      S = S * factor * factor;
+
+      f64x4 Q = {};
+#pragma unroll 1
+      for (int k = 0; k < a.plan.steps; ++k) {
+        const NarrowStep& t = a.plan.step[k];
+        f64x4 P = static_cast<double>(t.b) * S + static_cast<double>(t.c) * product16(S, S);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          P[r] += down + 4 * r == across && across < m ? static_cast<double>(t.a) : 0.0;
+        Q = k == 0 ? P : product16(P, Q);
+        S = product16(P, product16(S, P));
+      }
+      Q = Q * factor;
+
+      // 64 columns of X at a time, whose 16 results a lane has at rows (columns
+      // where the matrix is tall) down + 4 r and columns (rows) across
+      for (int c0 = first + 64 * wave; c0 < last; c0 += 64 * WAVES) {
+        Raw v[4][4];
+        float p[4][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[k][r] = fetch(down + 4 * r, c0 + 16 * k + across);
+        auto row = [&](int k, int r) { return tall ? c0 + 16 * k + down + 4 * r : down + 4 * r; };
+        auto col = [&](int k) { return tall ? across : c0 + 16 * k + across; };
+        auto inside = [&](int k, int r) {
+          return row(k, r) < (tall ? last : m) && col(k) < (tall ? m : last);
+        };
+        auto at = [&](int k, int r) { return (z * g.rows + row(k, r)) * g.cols + col(k); };
+        if (g.master != nullptr) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) p[k][r] = g.master[inside(k, r) ? at(k, r) : 0];
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          f64x4 O = {};
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const double x = value(v[k][r], down + 4 * r, c0 + 16 * k + across);
+            O = __builtin_amdgcn_mfma_f64_16x16x4f64(tall ? x : Q[r], tall ? Q[r] : x, O, 0, 0, 0);
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            if (!inside(k, r)) continue;
+            float o = static_cast<float>(O[r]);
+            if (g.master != nullptr) {
+              o = p[k][r] * a.plan.decay - g.step * o;
+              g.master[at(k, r)] = o;
+            }
+            if (g.out != nullptr)
+              static_cast<uint16_t*>(g.out)[g.master != nullptr
+                                                ? at(k, r)
+                                                : z * g.out_matrix_stride +
+                                                      row(k, r) * g.out_row_stride + col(k)] =
+                  bits16(o, a.plan.out_type);
+          }
+        }
+      }
+    }
+    __syncthreads();  // LDS is free for the next matrix
+  }
+}
+
 template <int MP, int TYPE, NarrowPart PART>
 hipError_t launch(NarrowArgs& a, int64_t total, hipStream_t stream, int64_t max_grid) {
   int64_t grid = total < kMaxWorkgroups ? total : kMaxWorkgroups;
   if (grid > max_grid) grid = max_grid;
   void* params[] = {&a};
-  return hipLaunchKernel(reinterpret_cast<const void*>(&narrow_kernel<MP, TYPE, PART>),
-                         dim3(static_cast<unsigned>(grid)), dim3(MP == 128 ? 512 : 256), params, 0,
-                         stream);
+  const void* kernel;
+  if constexpr (MP == kTiny) kernel = reinterpret_cast<const void*>(&tiny_kernel<TYPE, PART>);
+  else kernel = reinterpret_cast<const void*>(&narrow_kernel<MP, TYPE, PART>);
+  return hipLaunchKernel(kernel, dim3(static_cast<unsigned>(grid)), dim3(MP == 128 ? 512 : 256),
+                         params, 0, stream);
 }
 
 template <int MP, NarrowPart PART>
@@ -525,14 +706,17 @@ hipError_t launch_part(NarrowArgs& a, int64_t total, int type, NarrowPart part,
                        hipStream_t stream, int64_t max_grid) {
   switch (part) {
     case NarrowPart::kWhole:
-      if constexpr (MP == 64)
+      if constexpr (MP != 128)
         return launch_type<MP, NarrowPart::kWhole>(a, total, type, stream, max_grid);
       else
         return hipErrorInvalidValue;
     case NarrowPart::kSum:
       return launch_type<MP, NarrowPart::kSum>(a, total, type, stream, max_grid);
     case NarrowPart::kFactor:  // reads sums, not directions
-      return launch<MP, kFp32, NarrowPart::kFactor>(a, total, stream, max_grid);
+      if constexpr (MP != kTiny)
+        return launch<MP, kFp32, NarrowPart::kFactor>(a, total, stream, max_grid);
+      else
+        return hipErrorInvalidValue;
     default:
       return launch_type<MP, NarrowPart::kApply>(a, total, type, stream, max_grid);
   }
@@ -554,8 +738,9 @@ hipError_t launch_narrow(const NarrowGroup* groups, int count, int side, int typ
   a.plan = plan;
   a.skip = skip;
   a.count = count;
-  return side == 64 ? launch_part<64>(a, total, type, part, stream, max_grid)
-                    : launch_part<128>(a, total, type, part, stream, max_grid);
+  return side == kTiny ? launch_part<kTiny>(a, total, type, part, stream, max_grid)
+         : side == 64  ? launch_part<64>(a, total, type, part, stream, max_grid)
+                       : launch_part<128>(a, total, type, part, stream, max_grid);
 }
 
 }  // namespace la

@@ -13,6 +13,11 @@ and grows by a^2 per step while S is small, so that the result is off by |b| / a
 direction. Several roundings of half a step of 22 bits at most, adding as
 independent ones, make E's norm about one step, 2^-22 of S's; spread over m
 directions that is 2^-22 3.0e4 / m^(1/2) = 7.2e-3 / m^(1/2) of the result's norm.
+
+Short sides up to 16 are iterated in 64 bits, with coefficients of 32: each is off
+by half a step, 2^-24 of it, at most, and a step's result by 2^-24 (a s + |b| s^3 + c
+s^5) more than the slope makes of the step before. The largest sum of these over
+all singular values, beside the result's, is the bar, and a rounding to FP32.
 """
 import pytest
 import torch
@@ -28,6 +33,17 @@ GROWTH = abs(B) / A * sum(A ** (2 * k) for k in range(5))
 
 def narrow_bar(m):
     return 2.0 ** -22 * GROWTH / m ** 0.5
+
+
+def tiny_bar():
+    a, b, c = la.NEWTON_SCHULZ[0]
+    s = torch.logspace(-9, 0, 200001, dtype=torch.float64)
+    e = torch.zeros_like(s)
+    for _ in range(5):
+        e = (a + 3 * b * s ** 2 + 5 * c * s ** 4).abs() * e + \
+            2.0 ** -24 * (a * s - b * s ** 3 + c * s ** 5)
+        s = (a * s + b * s ** 3 + c * s ** 5).abs()
+    return float((e / s).max()) + 2.0 ** -24
 
 
 def dominated(shape, kind, eps, seed):
@@ -80,3 +96,27 @@ def test_narrow(shape, kind, eps):
     got, bar = worst(dominated(shape, kind, eps, sum(shape))), narrow_bar(min(shape[1:]))
     print(f"  off {got:.2e} (bar {bar:.2e})", flush=True)
     assert got <= bar
+
+
+# Whole and in parts, squares, vectors, tall and wide, the largest side.
+TINY = [(600, 2, 2), (300, 3, 5), (40, 16, 16), (7, 1, 1), (1, 1, 40000), (3, 2, 12000),
+        (520, 4, 20000), (5, 30000, 7), (1, 3, 1048576), (2, 513, 16), (2, 16, 512), (9, 9, 200),
+        (2, 13, 4)]
+
+
+@pytest.mark.parametrize("kind,eps", KINDS)
+@pytest.mark.parametrize("shape", TINY, ids=str)
+def test_tiny(shape, kind, eps):
+    got, bar = worst(dominated(shape, kind, eps, sum(shape))), tiny_bar()
+    print(f"  off {got:.2e} (bar {bar:.2e})", flush=True)
+    assert got <= bar
+
+
+@pytest.mark.parametrize("shape", [(2, 2), (3, 2, 300), (16, 30), (150, 9)], ids=str)
+def test_tiny_beside_wide(shape):
+    """A large matrix in the same call does not change how a tiny one is done."""
+    u = dominated((1, *shape)[-3:], "rank one", 0.01, 3).view(shape)
+    big = dominated((1, 200, 300), "noise", 1.0, 4)[0]
+    alone = la.orthogonalize(u)
+    for together in (la.orthogonalize([u, big])[0], la.orthogonalize([big, u])[1]):
+        assert torch.equal(alone.view(torch.int16), together.view(torch.int16))
