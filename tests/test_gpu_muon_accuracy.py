@@ -18,12 +18,22 @@ Short sides up to 16 are iterated in 64 bits, with coefficients of 32: each is o
 by half a step, 2^-24 of it, at most, and a step's result by 2^-24 (a s + |b| s^3 + c
 s^5) more than the slope makes of the step before. The largest sum of these over
 all singular values, beside the result's, is the bar, and a rounding to FP32.
+
+The step-by-step form rounds X as the products read it, A and B off their
+diagonals to binary16, with a root mean square of 2^-11 / 3^(1/2) of a value at the
+low end of its binade and 0.735 times that over a binade. For a singular value s of
+X and l = s^2, to first order, an X off by a part d moves the step's result by s (b
+l + c l^2 + 2 (b l + 2 c l^2)) d, the last step's by a s d more (it reads X in 16
+bits in its linear term too), an A by s (b l + 2 c l^2) d, a B by s (b l + c l^2) d.
+These add as independent ones to what the slope makes of the step before. The
+root mean square over the matrix's singular values is the bar: the roundings of
+many elements move each of them by less than those of one number would.
 """
 import pytest
 import torch
 
 import optimizer_step_layeradam_amd as la
-from muonhelpers import direction64
+from muonhelpers import direction64, matrices
 
 pytestmark = pytest.mark.gpu
 
@@ -44,6 +54,21 @@ def tiny_bar():
             2.0 ** -24 * (a * s - b * s ** 3 + c * s ** 5)
         s = (a * s + b * s ** 3 + c * s ** 5).abs()
     return float((e / s).max()) + 2.0 ** -24
+
+
+def wide_bar(u):
+    """Of the worst matrix in the stack u."""
+    a, b, c = la.NEWTON_SCHULZ[0]
+    s = torch.linalg.svdvals(u.double().cpu())
+    s = s / s.norm(dim=-1, keepdim=True)
+    v = torch.zeros_like(s)
+    unit = 0.735 * 2.0 ** -11 / 3 ** 0.5
+    for k in range(5):
+        p, q = b * s ** 2 + c * s ** 4, b * s ** 2 + 2 * c * s ** 4
+        of_x = p + 2 * q + (a if k == 4 else 0.0)
+        v = (a + p + 2 * q) ** 2 * v + (unit * s) ** 2 * (of_x ** 2 + q ** 2 + p ** 2)
+        s = (a * s + p * s).abs()
+    return float((v.sum(dim=-1) / s.square().sum(dim=-1)).sqrt().max())
 
 
 def dominated(shape, kind, eps, seed):
@@ -69,16 +94,16 @@ def dominated(shape, kind, eps, seed):
     return noise
 
 
-def direction(u):
-    m, p = (2 * u).contiguous(), torch.zeros_like(u)
-    g = torch.zeros_like(u, dtype=torch.bfloat16)
-    la.muon_step([(p, m)], [[g]], lr=1.0, momentum=0.5, nesterov=False, lr_scale="none")
-    return -p
+def direction(u, *beside):
+    params = [(torch.zeros_like(x), (2 * x).contiguous()) for x in (u, *beside)]
+    grads = [[torch.zeros_like(x, dtype=torch.bfloat16)] for x in (u, *beside)]
+    la.muon_step(params, grads, lr=1.0, momentum=0.5, nesterov=False, lr_scale="none")
+    return -params[0][0]
 
 
-def worst(u):
+def worst(u, *beside):
     want = direction64(u)
-    d = (direction(u).double() - want).flatten(1).norm(dim=1) / want.flatten(1).norm(dim=1)
+    d = (direction(u, *beside).double() - want).flatten(1).norm(dim=1) / want.flatten(1).norm(dim=1)
     return float(d.max())
 
 
@@ -120,3 +145,32 @@ def test_tiny_beside_wide(shape):
     alone = la.orthogonalize(u)
     for together in (la.orthogonalize([u, big])[0], la.orthogonalize([big, u])[1]):
         assert torch.equal(alone.view(torch.int16), together.view(torch.int16))
+
+
+SPECTRA = ["gauss", "lowrank", "spiked", "outliers"]
+
+
+@pytest.mark.parametrize("kind", SPECTRA)
+@pytest.mark.parametrize("shape", [(255, 257), (129, 1500), (300, 129), (513, 515), (3, 130, 200),
+                                   (2, 700, 300)], ids=str)
+def test_wide_spectra(shape, kind):
+    u = matrices(shape, kind, seed=sum(shape)).cuda()
+    u = u if u.dim() == 3 else u[None]
+    got, bar = worst(u), wide_bar(u)
+    print(f"  off {got:.2e} (bar {bar:.2e})", flush=True)
+    assert got <= bar
+
+
+@pytest.mark.parametrize("kind", SPECTRA)
+@pytest.mark.parametrize("shape", [(31, 33), (65, 63), (64, 64), (100, 260), (128, 128),
+                                   (7, 33, 70), (5, 17, 1030), (3, 1000, 24)], ids=str)
+def test_narrow_spectra_alone_and_beside_a_wide_matrix(shape, kind):
+    u = matrices(shape, kind, seed=sum(shape)).cuda()
+    u = u if u.dim() == 3 else u[None]
+    got, bar = worst(u), narrow_bar(min(u.shape[1:]))
+    print(f"  off {got:.2e} (bar {bar:.2e})", flush=True)
+    assert got <= bar
+    wide = matrices((1, 200, 300), seed=1).cuda()  # in whose launches small stacks share
+    got, bar = worst(u, wide), max(bar, wide_bar(u))
+    print(f"  off {got:.2e} (bar {bar:.2e})", flush=True)
+    assert got <= bar
