@@ -138,13 +138,13 @@ __device__ __forceinline__ void triangle(int t, int tiles_m, int& i, int& j) {
 // epilogue's 8 bytes an element among it; the last step 840 us, 1.09 PFLOP/s.
 // The matrix units are busy 50 to 58 % of the time, at 1.9 GHz.
 
-template <int MT, int NT, int WM, int WN, int DEPTH, int BUFFERS>
+template <int MT, int NT, int WM, int WN, int BUFFERS>
 struct Tile {
   static constexpr int waves = WM * WN;
   static constexpr int threads = 64 * waves;
   static constexpr int rows = 32 * MT * WM, cols = 32 * NT * WN;
-  static constexpr int stage = (rows + cols) * DEPTH;  // elements
-  static constexpr int pieces = DEPTH / 8;             // of 16 bytes in a row
+  static constexpr int stage = (rows + cols) * kDepth;  // elements
+  static constexpr int pieces = kDepth / 8;             // of 16 bytes in a row
   static constexpr int copy_rows = 64 / pieces;        // rows that one copy of a wave brings
   static constexpr int p_copies = rows / (copy_rows * waves);
   static constexpr int q_copies = cols / (copy_rows * waves);
@@ -152,12 +152,9 @@ struct Tile {
   static_assert(BUFFERS * stage * 2 >= waves * 32 * MT * 256, "the epilogue's part of LDS");
   static_assert(rows % (copy_rows * waves) == 0 && cols % (copy_rows * waves) == 0,
                 "whole rows per copy");
-  static_assert(kDepth % DEPTH == 0 && (DEPTH == 32 || DEPTH == 64), "whole stages");
-  // Where piece p of row r is kept: 64 banks hold 256 bytes, two rows of 128
-  // bytes or four of 64.
-  static __device__ __forceinline__ int slot(int r, int p) {
-    return DEPTH == 64 ? p ^ ((r >> 1) & 7) : p ^ ((r >> 2) & 3);
-  }
+  static_assert(kDepth == 64, "slot()");
+  // Where piece p of row r is kept: 64 banks hold 256 bytes, two rows.
+  static __device__ __forceinline__ int slot(int r, int p) { return p ^ ((r >> 1) & 7); }
 };
 
 template <int MT, int NT>
@@ -325,9 +322,9 @@ __device__ __forceinline__ half8 finish(const ProductGroup& g, const ProductScal
   return half8{};
 }
 
-template <Product WHAT, int OUT, int MT, int NT, int WM, int WN, int DEPTH, int BUFFERS>
-__global__ __launch_bounds__(64 * WM * WN, MT * NT == 8 ? 2 : 1) void product_kernel(ProductArgs a) {
-  using T = Tile<MT, NT, WM, WN, DEPTH, BUFFERS>;
+template <Product WHAT, int OUT, int MT, int NT, int WM, int WN, int BUFFERS>
+__global__ __launch_bounds__(64 * WM * WN, 1) void product_kernel(ProductArgs a) {
+  using T = Tile<MT, NT, WM, WN, BUFFERS>;
   constexpr bool SYM = WHAT == Product::kGram || WHAT == Product::kSquare;
   constexpr bool TURN = SYM || WHAT == Product::kUpdate;
   __shared__ __align__(1024) _Float16 lds[BUFFERS * T::stage];
@@ -377,12 +374,12 @@ __global__ __launch_bounds__(64 * WM * WN, MT * NT == 8 ? 2 : 1) void product_ke
     for (int c = 0; c < T::q_copies; ++c) qo[c] = offset(c, g.N - 1 - col0, g.ldq);
     // copies [from, to) of stage k
     auto copy = [&](int k, int buffer, int from, int to) {
-      _Float16* base = lds + buffer * T::stage + wave * T::copy_rows * DEPTH;
+      _Float16* base = lds + buffer * T::stage + wave * T::copy_rows * kDepth;
 #pragma unroll
       for (int c = from; c < to; ++c) {
         const bool p = c < T::p_copies;
-        copy_to_lds(p ? rp : rq, base + c * T::waves * T::copy_rows * DEPTH,
-                    p ? po[p ? c : 0] : qo[p ? 0 : c - T::p_copies], k * DEPTH * 2);
+        copy_to_lds(p ? rp : rq, base + c * T::waves * T::copy_rows * kDepth,
+                    p ? po[p ? c : 0] : qo[p ? 0 : c - T::p_copies], k * kDepth * 2);
       }
     };
     auto read = [&](Fragments<MT, NT>& f, int buffer, int step) {
@@ -391,13 +388,13 @@ __global__ __launch_bounds__(64 * WM * WN, MT * NT == 8 ? 2 : 1) void product_ke
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         const int r = wm + 32 * i + (lane & 31);
-        f.p[i] = *reinterpret_cast<const half8*>(from + r * DEPTH + (T::slot(r, piece) << 3));
+        f.p[i] = *reinterpret_cast<const half8*>(from + r * kDepth + (T::slot(r, piece) << 3));
       }
-      from += T::rows * DEPTH;
+      from += T::rows * kDepth;
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         const int r = wn + 32 * j + (lane & 31);
-        f.q[j] = *reinterpret_cast<const half8*>(from + r * DEPTH + (T::slot(r, piece) << 3));
+        f.q[j] = *reinterpret_cast<const half8*>(from + r * kDepth + (T::slot(r, piece) << 3));
       }
     };
     f32x16 acc[MT][NT] = {};
@@ -435,7 +432,7 @@ __global__ __launch_bounds__(64 * WM * WN, MT * NT == 8 ? 2 : 1) void product_ke
     using Bcopies = std::integral_constant<int, B>;
     using Ccopies = std::integral_constant<int, C>;
     using None = std::integral_constant<int, 0>;
-    const int stages = g.K / DEPTH;
+    const int stages = g.K / kDepth;
     Fragments<MT, NT> f[2];
     if constexpr (BUFFERS == 2) {
       // Stage k + 2 takes stage k's buffer: its copies start behind the meeting
@@ -482,7 +479,7 @@ __global__ __launch_bounds__(64 * WM * WN, MT * NT == 8 ? 2 : 1) void product_ke
         const bool more = k + BUFFERS - 1 < stages;
         if (more) copy(k + BUFFERS - 1, last, 0, ALL);
 #pragma unroll
-        for (int step = 1; step < DEPTH / 16; ++step) {
+        for (int step = 1; step < kDepth / 16; ++step) {
           read(f[step & 1], buffer, step);
           multiply(f[(step - 1) & 1]);
           interleave(None());
@@ -598,10 +595,10 @@ __global__ __launch_bounds__(64 * WM * WN, MT * NT == 8 ? 2 : 1) void product_ke
   }
 }
 
-template <Product WHAT, int OUT, int MT, int NT, int WM, int WN, int DEPTH, int BUFFERS>
+template <Product WHAT, int OUT, int MT, int NT, int WM, int WN, int BUFFERS>
 hipError_t launch_tile(const ProductGroup* groups, int count, const ProductScales& s,
                        const int32_t* skip, hipStream_t stream, int64_t max_grid) {
-  using T = Tile<MT, NT, WM, WN, DEPTH, BUFFERS>;
+  using T = Tile<MT, NT, WM, WN, BUFFERS>;
   constexpr bool SYM = WHAT == Product::kGram || WHAT == Product::kSquare;
   // The tiles of the longest sums first: the short ones fill the last round's
   // gaps (the 14B-shaped layer's X X^T: 2.05 -> 1.4 ms).
@@ -628,7 +625,7 @@ hipError_t launch_tile(const ProductGroup* groups, int count, const ProductScale
   int64_t grid = total < kMaxWorkgroups ? total : kMaxWorkgroups;
   if (grid > max_grid) grid = max_grid;
   void* params[] = {&a};
-  return hipLaunchKernel(reinterpret_cast<const void*>(&product_kernel<WHAT, OUT, MT, NT, WM, WN, DEPTH, BUFFERS>),
+  return hipLaunchKernel(reinterpret_cast<const void*>(&product_kernel<WHAT, OUT, MT, NT, WM, WN, BUFFERS>),
                          dim3(static_cast<unsigned>(grid)), dim3(T::threads), params, 0, stream);
 }
 
@@ -652,10 +649,10 @@ hipError_t launch_one(const ProductGroup* groups, int count, const ProductScales
   const int64_t large = 5 * rounds(256, 256), medium = 3 * rounds(128, 256),
                 small = 2 * rounds(64, 512);
   if (large < medium && large < small)
-    return launch_tile<WHAT, OUT, 4, 4, 2, 2, 64, 2>(groups, count, s, skip, stream, max_grid);
+    return launch_tile<WHAT, OUT, 4, 4, 2, 2, 2>(groups, count, s, skip, stream, max_grid);
   if (small < medium)
-    return launch_tile<WHAT, OUT, 1, 2, 2, 1, 64, 4>(groups, count, s, skip, stream, max_grid);
-  return launch_tile<WHAT, OUT, 2, 2, 2, 2, 64, 4>(groups, count, s, skip, stream, max_grid);
+    return launch_tile<WHAT, OUT, 1, 2, 2, 1, 4>(groups, count, s, skip, stream, max_grid);
+  return launch_tile<WHAT, OUT, 2, 2, 2, 2, 4>(groups, count, s, skip, stream, max_grid);
 }
 
 }  // namespace
