@@ -306,7 +306,9 @@ void narrow_kernel(NarrowArgs a) {
     };
 
     if constexpr (whole || PART == NarrowPart::kSum) {
+      // hi hi, block by block: low is 2^11 times finer than what its sums lose
       double total[BJ][16] = {};
+      f32x16 low[BJ] = {};
       Raw v[PER];
       fetch(v, first);
       int b = 0;
@@ -314,13 +316,13 @@ void narrow_kernel(NarrowArgs a) {
         put(v, c0, lds + b * OPERAND, false);
         __syncthreads();
         if (c0 + 64 < last) fetch(v, c0 + 64);
-        f32x16 acc[BJ] = {}, low[BJ] = {};
+        f32x16 acc[BJ] = {};
         multiply(Stage(), Blocks(), lds + b * OPERAND, XLO, wm, lds + b * OPERAND, XLO, wn, 4,
                  acc, low);
 #pragma unroll
         for (int j = 0; j < BJ; ++j)
 #pragma unroll
-          for (int k = 0; k < 16; ++k) total[j][k] += acc[j][k] + low[j][k] * 0x1p-11f;
+          for (int k = 0; k < 16; ++k) total[j][k] += acc[j][k];
       }
       __syncthreads();
       const double f = __builtin_ldexp(1.0, -2 * a.plan.x);
@@ -331,7 +333,8 @@ void narrow_kernel(NarrowArgs a) {
           const int row = wm + 8 * (k >> 2) + 4 * (lane >> 5) + (k & 3);
           const int col = wn + 32 * j + (lane & 31);
           // rows past m were not written: what their sums hold is not used
-          S[j][k] = row < m && col < m ? static_cast<float>(total[j][k] * f) : 0.0f;
+          const double sum = (total[j][k] + low[j][k] * 0x1p-11f) * f;
+          S[j][k] = row < m && col < m ? static_cast<float>(sum) : 0.0f;
         }
       if (!whole) {
         float* to = g.gram + (z * g.splits + split) * (MP * MP) + wave * (BJ * 1024) + lane;
