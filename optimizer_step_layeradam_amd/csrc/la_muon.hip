@@ -239,7 +239,7 @@ __global__ __launch_bounds__(kThreads) void square_sum_kernel(DirectionArgs a) {
         for (int k = threadIdx.x % across; k < pieces; k += across) {
           Eight<TYPE> v;
           v.load(g.in, row + 8 * k);
-          // pairs of squares in binary64, their sum once per eight
+          // added up for themselves: eight squares to one of the long sum
           double part = 0.0;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {

@@ -154,11 +154,15 @@ constexpr int64_t kParts = 512;
 constexpr int64_t kMostParts = 32;  // of one matrix: one workgroup adds them up
 
 // Beside wide stacks, whose launches it can share, a small narrow stack does
-// not get one of its own: sides up to kWholeColumns (a longer side makes the
-// step-by-step form's few tiles of X X^T long: 6 of 6566 x 12 and 12 of 770 x 2
-// beside 4 of 2160 x 246 take 558 us in shared launches, 362 us in their own)
-// and up to this many elements as that form pads them (a layer of 256 x 256, 2
-// of 256 x 64 and 688 x 256: 186 us in shared launches, 258 us apart).
+// not get its own: with sides up to kWholeColumns and up to this many elements as
+// the step-by-step form pads them. Shared and in launches of its own, us: 8 of 64 x
+// 256 beside one of 256 x 256 116 and 180, beside 8 of 2048 x 2048 2103 and 2117; on
+// the other side of the borders, 4 of 64 x 4096 beside one of 256 x 256 218 and 181
+// (a longer side makes the few tiles of X X^T long; at 1024 it is still 134 and
+// 177), 128 of 64 x 256 beside one of
+// 4096 x 2560 878 and 823. Sides up to kTiny do not share: the step-by-step form's
+// roundings do not average there (4 of 16 x 300 beside one of 300 x 300: 123 and
+// 139).
 constexpr int64_t kSharedElements = int64_t(1) << 20;
 
 void choose_form(Stack& s, const Polynomial& p, bool beside_wide) {
