@@ -519,9 +519,9 @@ void narrow_kernel(NarrowArgs a) {
 // positions l / 16 + 4 r: a wave multiplies 16 x 16 matrices without LDS, in four
 // dependent instructions, and every wave forms the factor for itself. The norm
 // is the trace of U U^T, so X is read twice in all. Off by 2e-7 at most over the
-// spectra tried. 1 x 1 in 9 us, most of it start and loads; 520 of 8 x 8192 in 300
+// spectra tried. 1 x 1 in 9 us, most of it start and loads; 520 of 8 x 8192 in 280
 // us (0.7 TB/s: 16 rows' worth of element-wise loads and matrix instructions for 8),
-// 64 of 16 x 4096 in 12 us for S and 24 us for the factor and the result.
+// 64 of 16 x 4096 in 13 us for S and 21 us for the factor and the result.
 
 typedef double f64x4 __attribute__((ext_vector_type(4)));
 
@@ -629,11 +629,10 @@ __global__ __launch_bounds__(256) void tiny_kernel(NarrowArgs a) {
       f64x4 Q = {};
 #pragma unroll 1
       for (int k = 0; k < a.plan.steps; ++k) {
-        const NarrowStep& t = a.plan.step[k];
-        f64x4 P = static_cast<double>(t.b) * S + static_cast<double>(t.c) * product16(S, S);
+        const double ta = a.plan.step[k].a, tb = a.plan.step[k].b, tc = a.plan.step[k].c;
+        f64x4 P = tb * S + tc * product16(S, S);
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          P[r] += down + 4 * r == across && across < m ? static_cast<double>(t.a) : 0.0;
+        for (int r = 0; r < 4; ++r) P[r] += down + 4 * r == across && across < m ? ta : 0.0;
         Q = k == 0 ? P : product16(P, Q);
         S = product16(P, product16(S, P));
       }
@@ -641,25 +640,29 @@ __global__ __launch_bounds__(256) void tiny_kernel(NarrowArgs a) {
 
       // 64 columns of X at a time, whose 16 results a lane has at rows (columns
       // where the matrix is tall) down + 4 r and columns (rows) across
+      float* const master = g.master;
+      uint16_t* const out = static_cast<uint16_t*>(g.out);
+      const int64_t base = master != nullptr ? z * g.rows * g.cols : z * g.out_matrix_stride;
+      const int64_t stride = master != nullptr ? g.cols : g.out_row_stride;
+      const int rows = tall ? last : m, cols = tall ? m : last;
       for (int c0 = first + 64 * wave; c0 < last; c0 += 64 * WAVES) {
         Raw v[4][4];
-        float p[4][4];
+        float p[4][4] = {};
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll
           for (int r = 0; r < 4; ++r) v[k][r] = fetch(down + 4 * r, c0 + 16 * k + across);
-        auto row = [&](int k, int r) { return tall ? c0 + 16 * k + down + 4 * r : down + 4 * r; };
-        auto col = [&](int k) { return tall ? across : c0 + 16 * k + across; };
-        auto inside = [&](int k, int r) {
-          return row(k, r) < (tall ? last : m) && col(k) < (tall ? m : last);
-        };
-        auto at = [&](int k, int r) { return (z * g.rows + row(k, r)) * g.cols + col(k); };
-        if (g.master != nullptr) {
+        auto row = [&](int k, int r) { return (tall ? c0 + 16 * k : 0) + down + 4 * r; };
+        auto col = [&](int k) { return (tall ? 0 : c0 + 16 * k) + across; };
+        auto inside = [&](int k, int r) { return row(k, r) < rows && col(k) < cols; };
+        auto at = [&](int k, int r) { return base + row(k, r) * stride + col(k); };
+        if (master != nullptr) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) p[k][r] = g.master[inside(k, r) ? at(k, r) : 0];
+            for (int r = 0; r < 4; ++r) p[k][r] = master[inside(k, r) ? at(k, r) : 0];
         }
+        float o[4][4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           f64x4 O = {};
@@ -670,19 +673,23 @@ __global__ __launch_bounds__(256) void tiny_kernel(NarrowArgs a) {
           }
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            if (!inside(k, r)) continue;
-            float o = static_cast<float>(O[r]);
-            if (g.master != nullptr) {
-              o = p[k][r] * a.plan.decay - g.step * o;
-              g.master[at(k, r)] = o;
-            }
-            if (g.out != nullptr)
-              static_cast<uint16_t*>(g.out)[g.master != nullptr
-                                                ? at(k, r)
-                                                : z * g.out_matrix_stride +
-                                                      row(k, r) * g.out_row_stride + col(k)] =
-                  bits16(o, a.plan.out_type);
+            o[k][r] = static_cast<float>(O[r]);
+            if (master != nullptr) o[k][r] = p[k][r] * a.plan.decay - g.step * o[k][r];
           }
+        }
+        if (master != nullptr) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (inside(k, r)) master[at(k, r)] = o[k][r];
+        }
+        if (out != nullptr) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (inside(k, r)) out[at(k, r)] = bits16(o[k][r], a.plan.out_type);
         }
       }
     }
