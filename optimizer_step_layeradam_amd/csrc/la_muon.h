@@ -1,6 +1,6 @@
 // Internal interface between the C ABI of the orthogonalised update
-// (la_muon_api.cpp) and its kernels (la_muon.hip, la_product.hip). Not
-// installed; callers use include/layeradam.h.
+// (la_muon_api.cpp) and its kernels (la_muon.hip, la_product.hip,
+// la_narrow.hip). Not installed; callers use include/layeradam.h.
 //
 // The iteration, on a matrix U of rows x cols with m = min(rows, cols) and
 // n = max(rows, cols): X_0 = U / max(||U||_F, eps), held so that its short
