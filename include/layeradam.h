@@ -465,6 +465,91 @@ LA_API la_status layer_muon_step(const la_muon_layer_desc *layer, const la_muon_
                                  int32_t *overflow_flag, const int32_t *skip_if_nonzero,
                                  void *workspace, int64_t workspace_bytes, void *hip_stream);
 
+/* ---------------------------------------------------------------------------
+ * Layer norm and RMS norm, forward and backward, whose parameters' gradients
+ * are gradient replicas of layer_adam_step as they lie.
+ *
+ *     s = x + residual, rounded to the type (without a residual: x)
+ *     mean = sum(s) / cols (RMS norm: 0)
+ *     rstd = 1 / sqrt(sum((s - mean)^2) / cols + eps)
+ *     h = (s - mean) * rstd;  y = h * weight + bias
+ * and back, with g = dy * weight and means over the row:
+ *     dx = rstd * (g - mean(g) - h * mean(g * h)) + residual_grad
+ *                                                 (RMS norm: no mean(g))
+ *     dweight = sum over rows of dy * h;  dbias = sum over rows of dy
+ * dx is the gradient of x and of the residual alike.
+ *
+ * Numerics: everything between the inputs and the outputs is FP32, sums
+ * included; each output is rounded once, to the nearest even. The same call
+ * with the same inputs gives the same bits. A row that holds an Inf or NaN
+ * gives NaN in its own results and in the sums over rows, nowhere else.
+ *
+ * Memory: calls are asynchronous on the given stream, allocate nothing,
+ * synchronise nothing and can be captured in a HIP graph; the workspace is as
+ * for the orthogonalised update, and calls that may run at once need one each.
+ * ------------------------------------------------------------------------- */
+
+typedef enum { LA_NORM_LAYER = 0, LA_NORM_RMS = 1 } la_norm_kind;
+
+/* Rows of a tensor: row (i, j), 0 <= i < outer, 0 <= j < inner, starts at
+ * element i * outer_stride + j * inner_stride of data and is contiguous; a
+ * stride that no second row uses is ignored. Strides are in elements and not
+ * negative; those of a tensor that is only read may make rows overlap (0: the
+ * same row again), those of a written one may not. data is aligned to its
+ * element. */
+typedef struct {
+  void *data;
+  int64_t outer_stride, inner_stride;
+} la_rows;
+
+/* A norm over outer * inner rows of cols (0..LA_MAX_SIDE) elements of `type`;
+ * weight and bias have cols contiguous elements of weight_type, NULL standing
+ * for ones and zeros. eps: finite and >= 0. */
+typedef struct {
+  int64_t outer, inner, cols;
+  int32_t kind;        /* a la_norm_kind                                     */
+  int32_t type;        /* a la_element_type                                  */
+  int32_t weight_type; /* a la_element_type                                  */
+  const void *weight;
+  const void *bias;
+  double eps;
+} la_norm_desc;
+
+/* residual and sum are given together or not at all (data NULL); mean (layer
+ * norm only) and rstd have one FP32 number a row, each NULL where it is not
+ * wanted; the backward pass needs them. */
+typedef struct {
+  la_rows x, residual, y, sum;
+  float *mean, *rstd;
+} la_norm_forward_io;
+
+/* x: what was normalised (the sum, where there was a residual).
+ * residual_grad: the gradient that reaches the sum by another way, data NULL
+ * where there is none. dx (data), dweight, dbias: NULL where not wanted;
+ * dweight and dbias have cols contiguous elements of grad_type. */
+typedef struct {
+  la_rows dy, x, residual_grad, dx;
+  const float *mean, *rstd;
+  void *dweight, *dbias;
+  int32_t grad_type; /* a la_element_type                                    */
+} la_norm_backward_io;
+
+/* Enqueue the forward pass on `hip_stream`. Outputs may not overlap inputs or
+ * each other. Every argument is checked on the host before anything is
+ * enqueued; on failure nothing is enqueued. */
+LA_API la_status la_norm_forward(const la_norm_desc *norm, const la_norm_forward_io *io,
+                                 void *hip_stream);
+
+/* Workspace of one la_norm_backward; -1 if the descriptor is invalid. Pointers
+ * are not looked at. Host only. */
+LA_API int64_t la_norm_backward_workspace_bytes(const la_norm_desc *norm);
+
+/* Enqueue the backward pass on `hip_stream`: without rows, dweight and dbias
+ * are set to zero. norm->bias and norm->eps are not looked at. Checks as
+ * above. */
+LA_API la_status la_norm_backward(const la_norm_desc *norm, const la_norm_backward_io *io,
+                                  void *workspace, int64_t workspace_bytes, void *hip_stream);
+
 /* Bytes of mixed-precision Adam state the layer stands for: 16 per
  * parameter (2 BF16 weight + 2 gradient + 4 FP32 master + 8 FP32 m and v).
  * -1 if the descriptor is invalid. Host only. */

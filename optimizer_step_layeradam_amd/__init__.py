@@ -30,6 +30,7 @@ GRAD_BF16, GRAD_FP16 = 0, 1
 OUT_BF16, OUT_FP16, OUT_NONE = 0, 1, 2
 PROBE_READS, PROBE_WRITES = 0, 1
 TYPE_BF16, TYPE_FP16, TYPE_FP32 = 0, 1, 2
+NORM_LAYER, NORM_RMS = 0, 1
 LR_SCALES = {"none": 0, "original": 1, "match_rms_adamw": 2}
 MAX_SIDE = 1048576
 MAX_POLYNOMIAL_STEPS = 16
@@ -44,6 +45,7 @@ EXPORTS = ("layer_adam_step", "layer_adam_step_range", "layer_adam_step_gated",
            "la_direction_probe", "la_copy_reference",
            "la_orthogonalize", "la_orthogonalize_workspace_bytes", "layer_muon_step",
            "layer_muon_workspace_bytes",
+           "la_norm_forward", "la_norm_backward", "la_norm_backward_workspace_bytes",
            "la_state_bytes", "la_traffic_bytes", "la_last_error", "la_version")
 
 
@@ -134,6 +136,39 @@ class MuonParams(ctypes.Structure):
                 ("nesterov", ctypes.c_int32),
                 ("lr_scale", ctypes.c_int32),
                 ("polynomial", ctypes.POINTER(Polynomial))]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p),
+                ("outer_stride", ctypes.c_int64),
+                ("inner_stride", ctypes.c_int64)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("outer", ctypes.c_int64),
+                ("inner", ctypes.c_int64),
+                ("cols", ctypes.c_int64),
+                ("kind", ctypes.c_int32),
+                ("type", ctypes.c_int32),
+                ("weight_type", ctypes.c_int32),
+                ("weight", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p),
+                ("eps", ctypes.c_double)]
+
+
+class NormForwardIO(ctypes.Structure):
+    _fields_ = [("x", Rows), ("residual", Rows), ("y", Rows), ("sum", Rows),
+                ("mean", ctypes.c_void_p),
+                ("rstd", ctypes.c_void_p)]
+
+
+class NormBackwardIO(ctypes.Structure):
+    _fields_ = [("dy", Rows), ("x", Rows), ("residual_grad", Rows), ("dx", Rows),
+                ("mean", ctypes.c_void_p),
+                ("rstd", ctypes.c_void_p),
+                ("dweight", ctypes.c_void_p),
+                ("dbias", ctypes.c_void_p),
+                ("grad_type", ctypes.c_int32)]
 
 
 class LayerAdamError(RuntimeError):
@@ -265,6 +300,14 @@ def load(path: Optional[str] = None):
     lib.layer_muon_workspace_bytes.argtypes = [ctypes.POINTER(MuonLayerDesc),
                                                ctypes.POINTER(MuonParams)]
     lib.layer_muon_workspace_bytes.restype = ctypes.c_int64
+    lib.la_norm_forward.argtypes = [ctypes.POINTER(NormDesc), ctypes.POINTER(NormForwardIO),
+                                    ctypes.c_void_p]
+    lib.la_norm_forward.restype = ctypes.c_int
+    lib.la_norm_backward.argtypes = [ctypes.POINTER(NormDesc), ctypes.POINTER(NormBackwardIO),
+                                     ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]
+    lib.la_norm_backward.restype = ctypes.c_int
+    lib.la_norm_backward_workspace_bytes.argtypes = [ctypes.POINTER(NormDesc)]
+    lib.la_norm_backward_workspace_bytes.restype = ctypes.c_int64
     lib.la_state_bytes.argtypes = [ctypes.POINTER(LayerDesc)]
     lib.la_state_bytes.restype = ctypes.c_int64
     lib.la_traffic_bytes.argtypes = [ctypes.POINTER(LayerDesc)]
@@ -1041,6 +1084,267 @@ def muon_step(params, grads, *, lr: float, momentum: float = 0.95, weight_decay:
         lr=lr, momentum=momentum, weight_decay=weight_decay, nesterov=nesterov,
         grad_unscale=grad_unscale, lr_scale=lr_scale, coefficients=coefficients, eps=eps,
         overflow_flag=overflow_flag, skip_if_nonzero=skip_if_nonzero, stream=stream)
+
+
+# ---------------------------------------------------------------------------
+# Layer norm and RMS norm
+# ---------------------------------------------------------------------------
+def make_norm(kind: int, outer: int, inner: int, cols: int, type: int, weight_type: int,
+              weight: int = 0, bias: int = 0, eps: float = 0.0) -> NormDesc:
+    """A NormDesc; weight and bias are integer pointers (0: ones, zeros)."""
+    return NormDesc(outer, inner, cols, kind, type, weight_type, weight or None, bias or None,
+                    float(eps))
+
+
+def norm_forward_raw(desc: NormDesc, io: NormForwardIO, stream: int = 0) -> None:
+    """la_norm_forward on raw descriptors; raises LayerAdamError on failure."""
+    lib = load()
+    _raise_on(lib.la_norm_forward(ctypes.byref(desc), ctypes.byref(io), stream or None), lib)
+
+
+def norm_backward_workspace_bytes_raw(desc: NormDesc) -> int:
+    return load().la_norm_backward_workspace_bytes(ctypes.byref(desc))
+
+
+def norm_backward_raw(desc: NormDesc, io: NormBackwardIO, workspace: int = 0,
+                      workspace_bytes: int = 0, stream: int = 0) -> None:
+    """la_norm_backward on raw descriptors; raises LayerAdamError on failure."""
+    lib = load()
+    _raise_on(lib.la_norm_backward(ctypes.byref(desc), ctypes.byref(io), workspace or None,
+                                   workspace_bytes, stream or None), lib)
+
+
+def _element_types():
+    import torch
+    return {torch.bfloat16: TYPE_BF16, torch.float16: TYPE_FP16, torch.float32: TYPE_FP32}
+
+
+def _element_type(t, what: str) -> int:
+    types = _element_types()
+    if t.dtype not in types:
+        raise TypeError(f"{what} must be one of {[str(k) for k in types]}, got {t.dtype}")
+    return types[t.dtype]
+
+
+def _one_stride(shape, strides):
+    """The stride that takes every index of these axes, in order, to its place
+    (0 where there is one place alone), or None."""
+    axes = [(n, s) for n, s in zip(shape, strides) if n != 1]
+    for (_, s), (m, t) in zip(axes, axes[1:]):
+        if s != m * t:
+            return None
+    return axes[-1][1] if axes else 0
+
+
+class _RowLayout:
+    """How a call's tensors of one shape divide into rows with two strides:
+    (outer, inner) counts, and each tensor's strides."""
+
+    def __init__(self, x, what: str = "x"):
+        if x.dim() < 1:
+            raise ValueError(f"{what} needs at least one dimension")
+        self.shape, self.dtype = x.shape, x.dtype
+        self.cols = x.shape[-1]
+        lead = x.shape[:-1]
+        self.rows = 1
+        for n in lead:
+            self.rows *= n
+        self.inner = lead[-1] if len(lead) > 1 else 1
+        self.outer = self.rows // self.inner if self.inner else 0
+
+    def __call__(self, t, what: str) -> Rows:
+        if t.shape != self.shape or t.dtype != self.dtype:
+            raise ValueError(f"{what} is {tuple(t.shape)} {t.dtype}, expected "
+                             f"{tuple(self.shape)} {self.dtype}")
+        if self.rows == 0 or self.cols == 0:
+            return Rows(0, 0, 0)
+        if self.cols > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{what} must be contiguous along its last axis")
+        if len(self.shape) < 3:
+            return Rows(device_address(t), t.stride(0) if len(self.shape) == 2 else 0, 0)
+        outer = _one_stride(self.shape[:-2], t.stride()[:-2])
+        if outer is None:
+            raise ValueError(f"{what}: the axes before the last two must be one stride apart, got "
+                             f"strides {t.stride()} of shape {tuple(t.shape)}")
+        return Rows(device_address(t), outer, t.stride(-2))
+
+
+def _parameter(t, cols: int, what: str, dtype=None) -> int:
+    """Address of a contiguous vector of cols elements; 0 for None."""
+    if t is None:
+        return 0
+    if t.dim() != 1 or t.shape[0] != cols or not (t.is_contiguous() or cols <= 1):
+        raise ValueError(f"{what} must be a contiguous vector of {cols} elements, got "
+                         f"{tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    return device_address(t) if cols else 0
+
+
+def _check_statistics(stats, rows: int, layer: bool) -> None:
+    import torch
+    wanted = (2 if layer else 1, rows)
+    if stats.dtype != torch.float32 or tuple(stats.shape) != wanted or not stats.is_contiguous():
+        raise ValueError(f"stats must be a contiguous float32 tensor of shape {wanted}, got "
+                         f"{tuple(stats.shape)} {stats.dtype}")
+
+
+def _statistics(stats, rows: int, layer: bool):
+    """(mean, rstd) addresses of a statistics tensor."""
+    if rows == 0:
+        return 0, 0
+    p = device_address(stats)
+    return (p, p + 4 * rows) if layer else (0, p)
+
+
+def _on(stream):
+    """The context in which a call takes new tensors: they belong to its stream."""
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _norm(kind, x, weight, bias, eps, residual, out, sum_out, stats, stream):
+    import torch
+    layout = _RowLayout(x)
+    layer = kind == NORM_LAYER
+    type_ = _element_type(x, "x")
+    weight_type = type_ if weight is None else _element_type(weight, "weight")
+    if weight is None and bias is not None:
+        weight_type = _element_type(bias, "bias")
+    if sum_out is not None and residual is None:
+        raise ValueError("sum_out is the sum of x and a residual: give the residual too")
+    if stats is not None:
+        _check_statistics(stats, layout.rows, layer)
+    with _on(stream):
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if sum_out is None and residual is not None:
+            sum_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if stats is None:
+            stats = torch.empty((2 if layer else 1, layout.rows), dtype=torch.float32,
+                                device=x.device)
+    none = Rows(0, 0, 0)
+    desc = make_norm(kind, layout.outer, layout.inner, layout.cols, type_, weight_type,
+                     _parameter(weight, layout.cols, "weight"),
+                     _parameter(bias, layout.cols, "bias",
+                                None if weight is None else weight.dtype), eps)
+    mean, rstd = _statistics(stats, layout.rows, layer)
+    io = NormForwardIO(layout(x, "x"), none if residual is None else layout(residual, "residual"),
+                       layout(out, "out"), none if residual is None else layout(sum_out, "sum_out"),
+                       mean or None, rstd or None)
+    s = stream if stream is not None else torch.cuda.current_stream()
+    norm_forward_raw(desc, io, s.cuda_stream)
+    return (out, stats) if residual is None else (out, stats, sum_out)
+
+
+def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, residual=None, out=None,
+               sum_out=None, stats=None, stream=None):
+    """la_norm_forward: layer norm over the last axis, enqueued on ``stream``
+    (default: the current torch stream).
+
+    x: a CUDA tensor in bf16, fp16 or fp32, contiguous along its last axis;
+       the axis before it may have any stride, those before that must be one
+       stride apart (the heads of a projection, say).
+    weight, bias: contiguous vectors of one type out of the three, or None.
+    residual: a tensor like x that is added first; the sum, rounded to x's
+       type, is what is normalised, and goes to sum_out.
+    out, sum_out: like x (default: new contiguous ones); they may not overlap
+       the inputs.
+    stats: a float32 tensor of shape (2, rows), mean and 1 / spread, for the
+       backward pass (default: a new one).
+    Returns (out, stats), with a residual (out, stats, sum_out). What the call
+    allocates belongs to ``stream``, as for orthogonalize().
+    """
+    return _norm(NORM_LAYER, x, weight, bias, eps, residual, out, sum_out, stats, stream)
+
+
+def rms_norm(x, weight=None, *, eps: float = 1e-6, residual=None, out=None, sum_out=None,
+             stats=None, stream=None):
+    """la_norm_forward: RMS norm over the last axis; as layer_norm(), without
+    the mean and the bias. stats has shape (1, rows): 1 / spread."""
+    return _norm(NORM_RMS, x, weight, None, eps, residual, out, sum_out, stats, stream)
+
+
+def _norm_backward(kind, dy, x, weight, stats, residual_grad, dx, dweight, dbias, weight_grad,
+                   bias_grad, workspace, stream):
+    import torch
+    layout = _RowLayout(x)
+    type_ = _element_type(x, "x")
+    weight_type = type_ if weight is None else _element_type(weight, "weight")
+    _check_statistics(stats, layout.rows, kind == NORM_LAYER)
+    with _on(stream):
+        if dx is None:
+            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        grad_dtype = x.dtype if weight is None else weight.dtype
+        if dweight is not None:
+            grad_dtype = dweight.dtype
+        elif dbias is not None:
+            grad_dtype = dbias.dtype
+        if dweight is None and weight_grad:
+            dweight = torch.empty(layout.cols, dtype=grad_dtype, device=x.device)
+        if dbias is None and bias_grad:
+            dbias = torch.empty(layout.cols, dtype=grad_dtype, device=x.device)
+    grads = [t for t in (dweight, dbias) if t is not None]
+    grad_type = _element_type_of(grads, "dweight and dbias", _element_types()) if grads else type_
+    desc = make_norm(kind, layout.outer, layout.inner, layout.cols, type_, weight_type,
+                     _parameter(weight, layout.cols, "weight"))
+    mean, rstd = _statistics(stats, layout.rows, kind == NORM_LAYER)
+    none = Rows(0, 0, 0)
+    io = NormBackwardIO(layout(dy, "dy"), layout(x, "x"),
+                        none if residual_grad is None else layout(residual_grad, "residual_grad"),
+                        layout(dx, "dx"), mean or None, rstd or None,
+                        _parameter(dweight, layout.cols, "dweight") or None,
+                        _parameter(dbias, layout.cols, "dbias") or None, grad_type)
+    s = stream if stream is not None else torch.cuda.current_stream()
+    if workspace is None:
+        needed = norm_backward_workspace_bytes_raw(desc)
+        workspace = _allocate_workspace(needed, s)
+    norm_backward_raw(desc, io, _workspace_ptr(workspace), workspace.numel(), s.cuda_stream)
+    return dx, dweight, dbias
+
+
+def layer_norm_backward(dy, x, weight, stats, *, residual_grad=None, dx=None, dweight=None,
+                        dbias=None, weight_grad: bool = True, bias_grad: bool = True,
+                        workspace=None, stream=None):
+    """la_norm_backward: the gradients of layer_norm(), enqueued on ``stream``
+    (default: the current torch stream).
+
+    dy: the gradient of its output; x: what it normalised (sum_out, where
+       there was a residual); weight, stats: as there. Strides as there.
+    residual_grad: the gradient that reaches sum_out by another way, like x;
+       it is added to dx, which is the gradient of x and the residual alike.
+    dx: like x (default: a new one). dweight, dbias: vectors of one type (new
+       ones have weight's type), None with weight_grad or bias_grad False:
+       gradient replicas for step() as they lie.
+    workspace: a uint8 CUDA tensor of at least norm_backward_workspace_bytes()
+       (default: taken from torch's allocator for the call).
+    Returns (dx, dweight, dbias).
+    """
+    return _norm_backward(NORM_LAYER, dy, x, weight, stats, residual_grad, dx, dweight, dbias,
+                          weight_grad, bias_grad, workspace, stream)
+
+
+def rms_norm_backward(dy, x, weight, stats, *, residual_grad=None, dx=None, dweight=None,
+                      weight_grad: bool = True, workspace=None, stream=None):
+    """la_norm_backward: the gradients of rms_norm(), as layer_norm_backward().
+    Returns (dx, dweight)."""
+    return _norm_backward(NORM_RMS, dy, x, weight, stats, residual_grad, dx, dweight, None,
+                          weight_grad, False, workspace, stream)[:2]
+
+
+def norm_backward_workspace_bytes(shape, dtype) -> int:
+    """Bytes of workspace of one backward pass over a tensor of this shape and
+    type, of either norm."""
+    if dtype not in _element_types():
+        raise TypeError(f"dtype must be one of {[str(k) for k in _element_types()]}, got {dtype}")
+    rows = 1
+    for n in shape[:-1]:
+        rows *= n
+    needed = norm_backward_workspace_bytes_raw(
+        make_norm(NORM_LAYER, rows, 1, shape[-1], _element_types()[dtype], TYPE_FP32))
+    if needed < 0:
+        raise LayerAdamError(1, last_error())
+    return needed
 
 
 def copy_reference(dst, src, stream=None) -> None:

@@ -10,21 +10,28 @@
 
 #include <algorithm>
 #include <cmath>
-#include <exception>
 #include <vector>
 
+#include "la_checks.h"
 #include "la_error.h"
 #include "la_muon.h"
 #include "layeradam.h"
 
 namespace {
 
+using la::aligned;
+using la::check_disjoint;
+using la::check_workspace;
 using la::fail;
+using la::guarded;
 using la::ok;
+using la::place;
+using la::Range;
+using la::range;
+using la::round_up;
+using la::type_bytes;
 
-bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 bool finite_nonneg(double x) { return std::isfinite(x) && x >= 0.0; }
-int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 
 // ---- the polynomial ----------------------------------------------------------------
 
@@ -261,11 +268,6 @@ int64_t lay_out(std::vector<Stack>& stacks, const Polynomial& p, bool direction,
   return at;
 }
 
-template <typename T>
-T* place(void* workspace, int64_t at) {
-  return reinterpret_cast<T*>(static_cast<char*>(workspace) + at);
-}
-
 // ---- the stages ----------------------------------------------------------------------
 
 // The products of all steps. `last` fills in the output of the last one.
@@ -440,55 +442,7 @@ la::DirectionGroup direction_group(const Stack& s, void* ws) {
   return d;
 }
 
-la_status check_workspace(const void* ws, int64_t given, int64_t needed) {
-  if (needed == 0) return LA_OK;
-  if (ws == nullptr) return fail(LA_ERR_INVALID_ARGUMENT, "workspace is NULL");
-  if (!aligned(ws, LA_WORKSPACE_ALIGNMENT))
-    return fail(LA_ERR_MISALIGNED, "workspace is not %d-byte aligned", LA_WORKSPACE_ALIGNMENT);
-  if (given < needed)
-    return fail(LA_ERR_INVALID_ARGUMENT, "workspace_bytes = %lld, need %lld",
-                static_cast<long long>(given), static_cast<long long>(needed));
-  return LA_OK;
-}
-
-// ---- aliasing --------------------------------------------------------------------------
-
-struct Range {
-  uintptr_t begin, end;  // [begin, end)
-  const char* what;
-  int tensor;
-};
-
-Range range(const void* p, int64_t bytes, const char* what, int tensor) {
-  const uintptr_t b = reinterpret_cast<uintptr_t>(p);
-  return {b, b + static_cast<uintptr_t>(bytes), what, tensor};
-}
-
-// Written ranges must be pairwise disjoint and disjoint from every range that
-// is only read.
-la_status check_disjoint(std::vector<Range>& written, const std::vector<Range>& read) {
-  auto meet = [](const Range& a, const Range& b) { return a.begin < b.end && b.begin < a.end; };
-  auto refuse = [](const Range& a, const Range& b) {
-    return fail(LA_ERR_ALIASING, "%s of tensor %d overlaps %s of tensor %d", a.what, a.tensor,
-                b.what, b.tensor);
-  };
-  std::sort(written.begin(), written.end(),
-            [](const Range& a, const Range& b) { return a.begin < b.begin; });
-  for (size_t k = 1; k < written.size(); ++k)
-    if (meet(written[k - 1], written[k])) return refuse(written[k - 1], written[k]);
-  for (const Range& r : read) {
-    // the first written range that ends after r begins: the ranges are
-    // disjoint and sorted, so their ends are sorted too
-    auto it = std::lower_bound(written.begin(), written.end(), r.begin,
-                               [](const Range& w, uintptr_t x) { return w.end <= x; });
-    if (it != written.end() && meet(*it, r)) return refuse(r, *it);
-  }
-  return LA_OK;
-}
-
 // ---- orthogonalize -----------------------------------------------------------------
-
-int64_t type_bytes(int type) { return type == LA_TYPE_FP32 ? 4 : 2; }
 
 la_status plan_matrices(const la_matrices_desc* d, const la_polynomial* polynomial,
                         Polynomial* p, std::vector<Stack>* stacks, int64_t* bytes) {
@@ -821,17 +775,6 @@ la_status muon_step(const la_muon_layer_desc* layer, const la_muon_params* hp, i
         x.step = step(s);
       },
       ws, skip, stream);
-}
-
-// No exception leaves the C ABI (a host allocation may fail).
-template <typename F>
-auto guarded(F f, decltype(f()) on_failure) -> decltype(f()) {
-  try {
-    return f();
-  } catch (const std::exception& e) {
-    fail(LA_ERR_INVALID_ARGUMENT, "%s", e.what());
-    return on_failure;
-  }
 }
 
 }  // namespace

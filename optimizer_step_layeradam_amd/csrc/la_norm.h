@@ -1,0 +1,46 @@
+// Internal interface between the C ABI of the norms (la_norm_api.cpp) and
+// their kernels (la_norm.hip). Not installed; callers use
+// include/layeradam.h.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace la {
+
+// Rows of a tensor: row i * inner + j at p + i * outer_stride + j * inner_stride.
+struct NormRows {
+  void* p;
+  int64_t outer_stride, inner_stride;
+};
+
+struct NormArgs {
+  NormRows x, residual, y, sum;              // forward; backward: x alone
+  NormRows dy, dsum, dx;                     // backward
+  const void* weight;                        // null: ones
+  const void* bias;                          // null: none
+  float* mean;                               // layer norm
+  float* rstd;                               // 1 / spread
+  float* partial;                            // backward: parts x (1 or 2) x cols
+  float* coefficients;                       // backward of long rows: two per row
+  void *dweight, *dbias;                     // null: not wanted
+  int64_t rows, inner;
+  int64_t parts;                             // backward: partial sums of the parameters' gradients
+  int64_t rows_per_part;
+  int32_t cols;
+  int32_t layer;                             // 1: layer norm, 0: RMS norm
+  int32_t type, weight_type, grad_type;      // la_element_type
+  float eps, inverse_cols;
+};
+
+// Rows up to this many bytes are held in a workgroup's registers.
+constexpr int kNormRegisterBytes = 32768;
+
+// The backward pass' parts: how many sums over rows are formed side by side,
+// and of how many rows each.
+void norm_parts(int64_t rows, int64_t cols, int type, int64_t* parts, int64_t* rows_per_part);
+
+hipError_t launch_norm_forward(const NormArgs& a, hipStream_t stream, int64_t max_grid);
+hipError_t launch_norm_backward(const NormArgs& a, hipStream_t stream, int64_t max_grid);
+
+}  // namespace la
