@@ -550,6 +550,84 @@ LA_API int64_t la_norm_backward_workspace_bytes(const la_norm_desc *norm);
 LA_API la_status la_norm_backward(const la_norm_desc *norm, const la_norm_backward_io *io,
                                   void *workspace, int64_t workspace_bytes, void *hip_stream);
 
+/* ---------------------------------------------------------------------------
+ * The loss of an output projection: softmax cross entropy of x weight^T over
+ * the vocabulary, with the gradients of x and of the weight, in pieces of the
+ * vocabulary, without a T x V matrix of logits (the pages' fused
+ * linear-cross-entropy: "An Efficient Heterogeneous Co-Design for Fine-Tuning
+ * on a Single GPU" (SlideFormer), section 2.3). dweight is a gradient replica
+ * of layer_adam_step or layer_muon_step as it lies.
+ *
+ *     z[t][v] = sum_h x[t][h] * weight[v][h]
+ *     losses[t] = log(sum_v exp(z[t][v])) - z[t][targets[t]]
+ *     loss = sum_t losses[t] (LA_REDUCE_SUM), or that over n (LA_REDUCE_MEAN),
+ *            n being the tokens whose target is not ignore_index
+ *     g[t][v] = softmax(z[t])[v] - (v == targets[t])
+ *     c = grad_scale (LA_REDUCE_SUM) or grad_scale / n (LA_REDUCE_MEAN)
+ *     dx[t] = c * sum_v g[t][v] * weight[v]
+ *     dweight[v] = c * sum_t g[t][v] * x[t]
+ * Tokens whose target is ignore_index have loss 0 and dx 0 and take part in
+ * nothing else: not even an Inf or NaN in their x reaches another result, and
+ * they cost no product. Without any other token, the loss and the gradients are
+ * 0. A target that is neither ignore_index nor in 0..vocab-1 makes its token's
+ * loss and dx, the loss and dweight NaN (check_gradients and the overflow flag
+ * find that). grad_scale is the loss scale of FP16 gradients, whose inverse is
+ * the step's grad_unscale; it does not change the loss.
+ *
+ * Numerics. Logits, softmax and sums over tokens, columns and hidden are FP32,
+ * the loss' sum over tokens FP64. g is rounded to the type of x and weight
+ * for the products (FP16 with a scale of 2^14; exp(z) before it is normalised
+ * to 11 bits), the target's entry from expm1 of its loss; dx and dweight are
+ * rounded once. The same call with the same inputs gives the same bits.
+ *
+ * Memory. The workspace holds one piece of the T x V matrix, 2 bytes an
+ * element. A piece of the whole vocabulary costs three products (6 n hidden
+ * vocab flops); where the workspace holds less, the logits of every piece
+ * behind the first are formed a second time. The call takes the largest pieces
+ * that the workspace given to it holds. Rules as for the orthogonalised
+ * update: asynchronous, no allocation, calls that may run at once need a
+ * workspace each, every call can be captured in a HIP graph (the targets, and
+ * with them n, may change between replays).
+ * ------------------------------------------------------------------------- */
+
+typedef enum { LA_INDEX_INT64 = 0, LA_INDEX_INT32 = 1 } la_index_type;
+typedef enum { LA_REDUCE_MEAN = 0, LA_REDUCE_SUM = 1 } la_reduction;
+
+/* x: tokens (0..LA_MAX_SIDE) rows of hidden (1..) elements; weight: vocab (1..)
+ * rows; both of `type`, LA_TYPE_BF16 or LA_TYPE_FP16, as dx and dweight. Rows
+ * are contiguous, row strides in elements: at least hidden, those of x 0 or
+ * more; all buffers are aligned to their element. targets: tokens indices of
+ * target_type. A weight whose rows are not 16-byte aligned, or hidden not a
+ * multiple of 64, costs a padded copy of it in the workspace and a pass over
+ * it. loss: one FP32; losses: tokens of them, or NULL. dx, dweight: NULL where
+ * not wanted. Outputs may not overlap inputs or each other. */
+typedef struct {
+  const void *x, *weight, *targets;
+  int64_t tokens, hidden, vocab;
+  int64_t x_row_stride, weight_row_stride;
+  int32_t type;        /* LA_TYPE_BF16 or LA_TYPE_FP16                       */
+  int32_t target_type; /* a la_index_type                                    */
+  int64_t ignore_index;
+  int32_t reduction;   /* a la_reduction                                     */
+  double grad_scale;   /* finite                                             */
+  float *loss, *losses;
+  void *dx, *dweight;
+  int64_t dx_row_stride, dweight_row_stride;
+} la_cross_entropy_desc;
+
+/* Workspace of one la_linear_cross_entropy with pieces of at most
+ * piece_columns columns, rounded up to a multiple of 256; 0: as many as 4 GiB hold.
+ * -1 if the descriptor is invalid. Of the pointers only whether dx and dweight
+ * are NULL and the alignment of weight is looked at. Host only. */
+LA_API int64_t la_linear_cross_entropy_workspace_bytes(const la_cross_entropy_desc *loss,
+                                                       int64_t piece_columns);
+
+/* Enqueue the loss, and the gradients that are not NULL, on `hip_stream`.
+ * Every argument is checked on the host before anything is enqueued; on
+ * failure nothing is enqueued. */
+LA_API la_status la_linear_cross_entropy(const la_cross_entropy_desc *loss, void *workspace,
+                                         int64_t workspace_bytes, void *hip_stream);
+
 /* Bytes of mixed-precision Adam state the layer stands for: 16 per
  * parameter (2 BF16 weight + 2 gradient + 4 FP32 master + 8 FP32 m and v).
  * -1 if the descriptor is invalid. Host only. */

@@ -31,6 +31,8 @@ OUT_BF16, OUT_FP16, OUT_NONE = 0, 1, 2
 PROBE_READS, PROBE_WRITES = 0, 1
 TYPE_BF16, TYPE_FP16, TYPE_FP32 = 0, 1, 2
 NORM_LAYER, NORM_RMS = 0, 1
+INDEX_INT64, INDEX_INT32 = 0, 1
+REDUCTIONS = {"mean": 0, "sum": 1}
 LR_SCALES = {"none": 0, "original": 1, "match_rms_adamw": 2}
 MAX_SIDE = 1048576
 MAX_POLYNOMIAL_STEPS = 16
@@ -46,6 +48,7 @@ EXPORTS = ("layer_adam_step", "layer_adam_step_range", "layer_adam_step_gated",
            "la_orthogonalize", "la_orthogonalize_workspace_bytes", "layer_muon_step",
            "layer_muon_workspace_bytes",
            "la_norm_forward", "la_norm_backward", "la_norm_backward_workspace_bytes",
+           "la_linear_cross_entropy", "la_linear_cross_entropy_workspace_bytes",
            "la_state_bytes", "la_traffic_bytes", "la_last_error", "la_version")
 
 
@@ -169,6 +172,28 @@ class NormBackwardIO(ctypes.Structure):
                 ("dweight", ctypes.c_void_p),
                 ("dbias", ctypes.c_void_p),
                 ("grad_type", ctypes.c_int32)]
+
+
+class CrossEntropyDesc(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p),
+                ("targets", ctypes.c_void_p),
+                ("tokens", ctypes.c_int64),
+                ("hidden", ctypes.c_int64),
+                ("vocab", ctypes.c_int64),
+                ("x_row_stride", ctypes.c_int64),
+                ("weight_row_stride", ctypes.c_int64),
+                ("type", ctypes.c_int32),
+                ("target_type", ctypes.c_int32),
+                ("ignore_index", ctypes.c_int64),
+                ("reduction", ctypes.c_int32),
+                ("grad_scale", ctypes.c_double),
+                ("loss", ctypes.c_void_p),
+                ("losses", ctypes.c_void_p),
+                ("dx", ctypes.c_void_p),
+                ("dweight", ctypes.c_void_p),
+                ("dx_row_stride", ctypes.c_int64),
+                ("dweight_row_stride", ctypes.c_int64)]
 
 
 class LayerAdamError(RuntimeError):
@@ -308,6 +333,12 @@ def load(path: Optional[str] = None):
     lib.la_norm_backward.restype = ctypes.c_int
     lib.la_norm_backward_workspace_bytes.argtypes = [ctypes.POINTER(NormDesc)]
     lib.la_norm_backward_workspace_bytes.restype = ctypes.c_int64
+    lib.la_linear_cross_entropy.argtypes = [ctypes.POINTER(CrossEntropyDesc), ctypes.c_void_p,
+                                            ctypes.c_int64, ctypes.c_void_p]
+    lib.la_linear_cross_entropy.restype = ctypes.c_int
+    lib.la_linear_cross_entropy_workspace_bytes.argtypes = [ctypes.POINTER(CrossEntropyDesc),
+                                                            ctypes.c_int64]
+    lib.la_linear_cross_entropy_workspace_bytes.restype = ctypes.c_int64
     lib.la_state_bytes.argtypes = [ctypes.POINTER(LayerDesc)]
     lib.la_state_bytes.restype = ctypes.c_int64
     lib.la_traffic_bytes.argtypes = [ctypes.POINTER(LayerDesc)]
@@ -1342,6 +1373,176 @@ def norm_backward_workspace_bytes(shape, dtype) -> int:
         rows *= n
     needed = norm_backward_workspace_bytes_raw(
         make_norm(NORM_LAYER, rows, 1, shape[-1], _element_types()[dtype], TYPE_FP32))
+    if needed < 0:
+        raise LayerAdamError(1, last_error())
+    return needed
+
+
+# ---------------------------------------------------------------------------
+# The loss of an output projection
+# ---------------------------------------------------------------------------
+def make_cross_entropy(**fields) -> CrossEntropyDesc:
+    """A CrossEntropyDesc from its fields (integer pointers); row strides are
+    hidden unless given."""
+    hidden = fields["hidden"]
+    d = dict(x_row_stride=hidden, weight_row_stride=hidden, dx_row_stride=hidden,
+             dweight_row_stride=hidden, ignore_index=-100, grad_scale=1.0)
+    d.update(fields)
+    desc = CrossEntropyDesc()
+    for name, value in d.items():
+        setattr(desc, name, value)
+    return desc
+
+
+def linear_cross_entropy_workspace_bytes_raw(desc: CrossEntropyDesc,
+                                             piece_columns: int = 0) -> int:
+    return load().la_linear_cross_entropy_workspace_bytes(ctypes.byref(desc), piece_columns)
+
+
+def linear_cross_entropy_raw(desc: CrossEntropyDesc, workspace: int = 0, workspace_bytes: int = 0,
+                             stream: int = 0) -> None:
+    """la_linear_cross_entropy on a raw descriptor; raises LayerAdamError on failure."""
+    lib = load()
+    _raise_on(lib.la_linear_cross_entropy(ctypes.byref(desc), workspace or None, workspace_bytes,
+                                          stream or None), lib)
+
+
+def _check_matrix(t, shape, dtype, what: str) -> None:
+    if t.dim() != 2 or tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{what} is {tuple(t.shape)} {t.dtype}, expected {tuple(shape)} {dtype}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} must be contiguous along its last axis")
+
+
+def _address(t) -> int:
+    """Address of a tensor; 0 where there is none, or nothing in it."""
+    return device_address(t) if t is not None and t.numel() else 0
+
+
+def _cross_entropy(x, weight, targets, ignore_index, reduction, grad_scale, loss, losses, dx,
+                   dweight, input_grad, weight_grad, workspace, stream):
+    import torch
+    if reduction not in REDUCTIONS:
+        raise ValueError(f"reduction must be one of {sorted(REDUCTIONS)}, got {reduction!r}")
+    if x.dim() < 1 or weight.dim() != 2:
+        raise ValueError("x needs at least one dimension, the weight two")
+    hidden, vocab = x.shape[-1], weight.shape[0]
+    types = {torch.bfloat16: TYPE_BF16, torch.float16: TYPE_FP16}
+    type_ = _element_type_of([x, weight], "x and the weight", types)
+    indices = {torch.int64: INDEX_INT64, torch.int32: INDEX_INT32}
+    if targets.dtype not in indices:
+        raise TypeError(f"targets must be int64 or int32, got {targets.dtype}")
+    if targets.shape != x.shape[:-1]:
+        raise ValueError(f"targets are {tuple(targets.shape)}, expected {tuple(x.shape[:-1])}")
+    if not targets.is_contiguous():
+        raise ValueError("targets must be contiguous")
+    tokens = targets.numel()
+    lead = tuple(targets.shape)
+    if x.dim() != 2:
+        x = _token_rows(x, "x")
+    _check_matrix(x, (tokens, hidden), x.dtype, "x")
+    _check_matrix(weight, (vocab, hidden), x.dtype, "weight")
+    for t, n, what in ((loss, 1, "loss"), (losses, tokens, "losses")):
+        if t is not None and (t.dtype != torch.float32 or t.numel() != n or
+                              not t.is_contiguous()):
+            raise ValueError(f"{what} must be a contiguous float32 tensor of {n} elements")
+    with _on(stream):
+        if loss is None:
+            loss = torch.empty((), dtype=torch.float32, device=x.device)
+        if dx is None and input_grad:
+            dx = torch.empty((*lead, hidden), dtype=x.dtype, device=x.device)
+        if dweight is None and weight_grad:
+            dweight = torch.empty((vocab, hidden), dtype=x.dtype, device=x.device)
+    rows = dx
+    if dx is not None:
+        if tuple(dx.shape) != (*lead, hidden):
+            raise ValueError(f"dx is {tuple(dx.shape)}, expected {(*lead, hidden)}")
+        rows = dx if dx.dim() == 2 else _token_rows(dx, "dx")
+        _check_matrix(rows, (tokens, hidden), x.dtype, "dx")
+    if dweight is not None:
+        _check_matrix(dweight, (vocab, hidden), x.dtype, "dweight")
+    desc = CrossEntropyDesc(
+        _address(x), _address(weight), _address(targets), tokens, hidden, vocab, x.stride(0),
+        weight.stride(0), type_, indices[targets.dtype], int(ignore_index), REDUCTIONS[reduction],
+        float(grad_scale), _address(loss), _address(losses), _address(rows), _address(dweight),
+        0 if rows is None else rows.stride(0), 0 if dweight is None else dweight.stride(0))
+    s = stream if stream is not None else torch.cuda.current_stream()
+    if workspace is None:
+        needed = linear_cross_entropy_workspace_bytes_raw(desc)
+        if needed < 0:
+            raise LayerAdamError(1, last_error())
+        workspace = _allocate_workspace(needed, s)
+    linear_cross_entropy_raw(desc, _workspace_ptr(workspace), workspace.numel(), s.cuda_stream)
+    return loss, dx, dweight
+
+
+def _token_rows(t, what: str):
+    """The matrix of a tensor's rows, without a copy."""
+    stride = _one_stride(t.shape[:-1], t.stride()[:-1])
+    if stride is None:
+        raise ValueError(f"{what}: the axes before the last must be one stride apart, got strides "
+                         f"{t.stride()} of shape {tuple(t.shape)}")
+    rows = 1
+    for n in t.shape[:-1]:
+        rows *= n
+    return t.as_strided((rows, t.shape[-1]), (stride, t.stride(-1)))
+
+
+def linear_cross_entropy(x, weight, targets, *, ignore_index: int = -100, reduction: str = "mean",
+                         loss=None, losses=None, workspace=None, stream=None):
+    """la_linear_cross_entropy without gradients: the softmax cross entropy of
+    x weight^T, enqueued on ``stream`` (default: the current torch stream).
+
+    x: CUDA tensor of hidden states (..., hidden), bf16 or fp16, contiguous
+       along its last axis, the axes before it one stride apart.
+    weight: (vocab, hidden) of the same type, contiguous along its last axis.
+    targets: contiguous int64 or int32 tensor of x's leading shape; tokens
+       whose target is ignore_index do not count.
+    reduction: "mean" over the tokens that count, or "sum".
+    loss: float32 tensor of one element for the result (default: a new one).
+    losses: optional float32 tensor that gets each token's loss.
+    workspace: a uint8 CUDA tensor of at least
+       linear_cross_entropy_workspace_bytes() (default: taken from torch's
+       allocator for the call).
+    Returns the loss, a tensor; nothing is synchronised. What the call
+    allocates belongs to ``stream``, as for orthogonalize().
+    """
+    return _cross_entropy(x, weight, targets, ignore_index, reduction, 1.0, loss, losses, None,
+                          None, False, False, workspace, stream)[0]
+
+
+def linear_cross_entropy_gradients(x, weight, targets, *, ignore_index: int = -100,
+                                   reduction: str = "mean", grad_scale: float = 1.0, loss=None,
+                                   losses=None, dx=None, dweight=None, input_grad: bool = True,
+                                   weight_grad: bool = True, workspace=None, stream=None):
+    """la_linear_cross_entropy with the gradients of x and the weight; as
+    linear_cross_entropy().
+
+    grad_scale: factor of the gradients (the loss scale of FP16, or one over
+       the micro-batches), not of the loss.
+    dx, dweight: like x and weight (default: new contiguous ones), None with
+       input_grad or weight_grad False. dweight is a gradient replica for
+       step() or MuonLayer as it lies.
+    workspace: the larger, the fewer pieces; see
+       linear_cross_entropy_workspace_bytes().
+    Returns (loss, dx, dweight).
+    """
+    return _cross_entropy(x, weight, targets, ignore_index, reduction, grad_scale, loss, losses,
+                          dx, dweight, input_grad, weight_grad, workspace, stream)
+
+
+def linear_cross_entropy_workspace_bytes(tokens: int, hidden: int, vocab: int, *,
+                                         piece_columns: int = 0, input_grad: bool = True,
+                                         weight_grad: bool = True, packed: bool = False) -> int:
+    """Bytes of workspace of one linear_cross_entropy_gradients() (without
+    either gradient: of one linear_cross_entropy()) that holds pieces of up to
+    piece_columns columns of the vocabulary (default: what 4 GiB hold).
+    packed: the weight's rows are not 16-byte aligned."""
+    desc = make_cross_entropy(
+        tokens=tokens, hidden=hidden, vocab=vocab, type=TYPE_BF16, target_type=INDEX_INT64,
+        reduction=REDUCTIONS["mean"], weight=2 if packed else 0, dx=2 if input_grad else 0,
+        dweight=2 if weight_grad else 0)
+    needed = linear_cross_entropy_workspace_bytes_raw(desc, piece_columns)
     if needed < 0:
         raise LayerAdamError(1, last_error())
     return needed
