@@ -59,9 +59,9 @@ struct LossRows {
   int32_t* count;           // n
   int32_t* index;           // of the gathered tokens: where they come from
   int32_t* target;          // their targets, -1 where out of range
-  uint16_t* xc;             // gathered, rows x ldx, zeros behind
-  int32_t ldx;              // hidden, up to whole depths
-  float2* sums;             // tokens x chunks: maximum and sum of exp(z - maximum)
+  uint16_t* xc;             // gathered, rows x width, zeros behind hidden
+  int32_t width;            // hidden, up to whole depths
+  float2* sums;             // chunks x tokens: maximum and sum of exp(z - maximum)
   int32_t chunks;           // of vocab columns
   int32_t chunk_shift;      // log2 of a chunk's columns
   float* target_logit;
@@ -86,9 +86,9 @@ enum class LossProduct { kKeep, kSums, kAgain, kInput, kWeight };
 struct LossProductArgs {
   LossRows r;
   LossPiece piece;
-  const uint16_t* w;        // weight, rows ldw elements apart, zeros behind hidden up to ldx
+  const uint16_t* w;        // weight, rows ldw elements apart, zeros behind hidden up to width
   int64_t ldw;
-  float* partial;           // kInput: splits x tokens x ldx
+  float* partial;           // kInput: splits x tokens x width
   int32_t splits;           // kInput: parts of the sum over the piece
   int32_t depth;            // kInput: columns of one part, a multiple of 64
   int32_t add;              // kInput: to what is there
@@ -98,13 +98,15 @@ struct LossProductArgs {
 };
 
 // log2 of a chunk's columns in the tile that a call of this size takes.
-int loss_chunk_shift(int64_t tokens);
+int loss_chunk_shift(int64_t tokens, int64_t vocab);
 
 hipError_t launch_loss_gather(const LossRows& r, hipStream_t stream, int64_t max_grid);
 hipError_t launch_pack(const uint16_t* from, int64_t stride, int64_t rows, int cols, uint16_t* to,
-                       int ld, hipStream_t stream, int64_t max_grid);
-// lse and losses; with a piece, e becomes g in it.
-hipError_t launch_loss_softmax(const LossRows& r, const LossPiece* piece, hipStream_t stream,
+                       int width, hipStream_t stream, int64_t max_grid);
+// lse and losses from the chunks.
+hipError_t launch_loss_lse(const LossRows& r, hipStream_t stream, int64_t max_grid);
+// e becomes g in the first piece.
+hipError_t launch_loss_softmax(const LossRows& r, const LossPiece& piece, hipStream_t stream,
                                int64_t max_grid);
 hipError_t launch_loss_sum(const LossRows& r, hipStream_t stream);
 hipError_t launch_loss_input(const LossRows& r, const float* partial, int splits,

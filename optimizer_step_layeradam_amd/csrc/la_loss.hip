@@ -62,10 +62,10 @@ __global__ __launch_bounds__(256) void gather_kernel(LossRows r) {
   for (int row = blockIdx.x; row < padded; row += gridDim.x) {
     const uint16_t* from = row < n ? r.x + r.index[row] * r.x_stride : r.x;
     const int cols = row < n ? r.hidden : 0;
-    uint16_t* to = r.xc + static_cast<int64_t>(row) * r.ldx;
-    for (int at = threadIdx.x * 8; at < r.ldx; at += 2048) {
+    uint16_t* to = r.xc + static_cast<int64_t>(row) * r.width;
+    for (int at = threadIdx.x * 8; at < r.width; at += 2048) {
       const Vector<Bf16> v = load_vector<Bf16>(from, at, cols);
-      store_vector<Bf16>(to, at, r.ldx, v);
+      store_vector<Bf16>(to, at, r.width, v);
     }
   }
   if (r.dx == nullptr || n == r.tokens) return;
@@ -79,29 +79,15 @@ __global__ __launch_bounds__(256) void gather_kernel(LossRows r) {
 }
 
 // A copy of rows whose length or alignment the products cannot read: zeros up
-// to ld.
+// to width.
 __global__ __launch_bounds__(256) void pack_kernel(const uint16_t* from, int64_t stride,
-                                                   int64_t rows, int cols, uint16_t* to, int ld) {
+                                                   int64_t rows, int cols, uint16_t* to, int width) {
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x)
-    for (int at = threadIdx.x * 8; at < ld; at += 2048)
-      store_vector<Bf16>(to + row * ld, at, ld, load_vector<Bf16>(from + row * stride, at, cols));
+    for (int at = threadIdx.x * 8; at < width; at += 2048)
+      store_vector<Bf16>(to + row * width, at, width, load_vector<Bf16>(from + row * stride, at, cols));
 }
 
 // ---- softmax --------------------------------------------------------------------------
-
-template <int THREADS>
-__device__ __forceinline__ float block_max(float x) {
-  __shared__ float part[THREADS / 64];
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) x = __builtin_fmaxf(x, __shfl_xor(x, d, 64));
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
-  __syncthreads();
-  x = part[0];
-#pragma unroll
-  for (int i = 1; i < THREADS / 64; ++i) x = __builtin_fmaxf(x, part[i]);
-  __syncthreads();
-  return x;
-}
 
 template <int THREADS, typename S>
 __device__ __forceinline__ S block_sum(S x) {
@@ -117,67 +103,55 @@ __device__ __forceinline__ S block_sum(S x) {
   return x;
 }
 
-constexpr int kSoftmaxThreads = 256;
-
-// A workgroup joins its row's chunks (each its maximum and its sum of
-// exponentials below it) to lse, then turns its share of e into g. Where a row
-// has several workgroups each joins the chunks again: they are few beside e.
-template <typename T, bool PIECE>
-__global__ __launch_bounds__(kSoftmaxThreads) void softmax_kernel(LossRows r, LossPiece piece,
-                                                                  int shares) {
+// The chunks of a row (each its maximum and its sum of exponentials below it)
+// joined to lse. A workgroup takes ROWS rows at a time, 1024 / ROWS threads
+// to each, whose reads are whole lines where ROWS is 16.
+template <int ROWS>
+__global__ __launch_bounds__(1024) void lse_kernel(LossRows r) {
+  constexpr int SHARES = 1024 / ROWS;
+  __shared__ float2 parts[SHARES][ROWS];
   const int n = *r.count;
-  const int padded = PIECE ? (n + kLossDepth - 1) / kLossDepth * kLossDepth : n;
-  const int width = PIECE ? (piece.cols + kLossDepth - 1) / kLossDepth * kLossDepth : 0;
-  const int share = ((width / 8 + shares - 1) / shares + 255) / 256 * 256;  // vectors
-  for (int64_t k = blockIdx.x; k < static_cast<int64_t>(padded) * shares; k += gridDim.x) {
-    const int row = static_cast<int>(k / shares), part = static_cast<int>(k - static_cast<int64_t>(row) * shares);
-    uint16_t* g = PIECE ? piece.g + static_cast<int64_t>(row) * piece.ld : nullptr;
-    const int begin = part * share * 8, end = min(width, begin + share * 8);
-    if (row >= n) {  // rows behind the last one are read as zeros
-      const Vector<Bf16> zero = {};
-      if constexpr (PIECE)
-        for (int at = begin + threadIdx.x * 8; at < end; at += kSoftmaxThreads * 8)
-          store_vector<Bf16>(g, at, end, zero);
-      continue;
+  const int share = threadIdx.x / ROWS, lane = threadIdx.x % ROWS;
+  for (int first = blockIdx.x * ROWS; first < n; first += gridDim.x * ROWS) {
+    const int row = min(first + lane, n - 1);
+    float most = -__builtin_inff(), sum = 0.0f;
+    auto join = [](float& most, float& sum, float2 x) {
+      const float top = __builtin_fmaxf(most, x.x);
+      // nothing so far, or nothing here: exp(-inf - top) is 0, unless top is too
+      const float point = top == -__builtin_inff() ? 0.0f : top;
+      sum = sum * __builtin_amdgcn_exp2f((most - point) * kLog2e) +
+            x.y * __builtin_amdgcn_exp2f((x.x - point) * kLog2e);
+      most = top;
+    };
+    const float2* sums = r.sums + row;
+    int k = share;
+    for (; k + 3 * SHARES < r.chunks; k += 4 * SHARES) {
+      float2 x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = sums[static_cast<int64_t>(k + i * SHARES) * r.tokens];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) join(most, sum, x[i]);
     }
-    const float2* sums = r.sums + static_cast<int64_t>(row) * r.chunks;
-    float most = -__builtin_inff();
-    for (int i = threadIdx.x; i < r.chunks; i += kSoftmaxThreads)
-      most = __builtin_fmaxf(most, sums[i].x);
-    most = block_max<kSoftmaxThreads>(most);
-    float sum = 0.0f;
-    for (int i = threadIdx.x; i < r.chunks; i += kSoftmaxThreads)
-      sum += sums[i].y * __builtin_amdgcn_exp2f((sums[i].x - most) * kLog2e);
-    sum = block_sum<kSoftmaxThreads>(sum);
-    const int target = r.target[row];
-    const float log_sum = __builtin_logf(sum);
-    // a target outside the vocabulary makes all of its token's results NaN
-    const float loss = target < 0 ? __builtin_nanf("")
-                                  : (most - r.target_logit[row]) + log_sum;
-    if (part == 0 && threadIdx.x == 0) {
-      r.lse[row] = target < 0 ? __builtin_nanf("") : most + log_sum;
+    for (; k < r.chunks; k += SHARES) join(most, sum, sums[static_cast<int64_t>(k) * r.tokens]);
+    parts[share][lane] = make_float2(most, sum);
+    __syncthreads();
+    for (int step = SHARES / 2; step > 0; step >>= 1) {
+      if (share < step) {
+        join(most, sum, parts[share + step][lane]);
+        parts[share][lane] = make_float2(most, sum);
+      }
+      __syncthreads();
+    }
+    if (share == 0 && first + lane < n) {
+      // a target outside the vocabulary makes all of its token's results NaN
+      const bool outside = r.target[row] < 0;
+      const float log_sum = __builtin_logf(sum), nan = __builtin_nanf("");
+      const float loss = outside ? nan : (most - r.target_logit[row]) + log_sum;
+      r.lse[row] = outside ? nan : most + log_sum;
       r.compact_losses[row] = loss;
       if (r.losses != nullptr) r.losses[r.index[row]] = loss;
     }
-    if constexpr (PIECE) {
-      constexpr float scale = T::encode_scale;
-      const float inverse = target < 0 ? loss : scale / (sum * kLossScale);
-      const int own = target - piece.first;
-      // not 1 - p, whose difference loses what a well predicted token has
-      const float at_target = scale * expm1f(-loss);
-      for (int at = begin + threadIdx.x * 8; at < end; at += kSoftmaxThreads * 8) {
-        const Vector<Fp16> e = load_vector<Fp16>(g, at, end);
-        const float f =
-            __builtin_amdgcn_exp2f((sums[at >> r.chunk_shift].x - most) * kLog2e) * inverse;
-        Vector<Bf16> o;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float p = Fp16::decode(e.e[i]) * f;
-          o.e[i] = T::encode(at + i == own ? at_target : p);
-        }
-        store_vector<Bf16>(g, at, end, o);
-      }
-    }
+    __syncthreads();
   }
 }
 
@@ -187,6 +161,47 @@ struct ScaledBf16 : Bf16 {
 struct ScaledFp16 : Fp16 {
   static constexpr float encode_scale = kLossScale;
 };
+
+// e of the held piece becomes g, in place: 16 rows of 2048 columns a workgroup.
+constexpr int kSoftmaxRows = 16, kSoftmaxCols = 2048;
+
+template <typename T>
+__global__ __launch_bounds__(256) void softmax_kernel(LossRows r, LossPiece piece) {
+  constexpr float scale = T::encode_scale;
+  const int n = *r.count;
+  const int padded = (n + kLossDepth - 1) / kLossDepth * kLossDepth;
+  const int width = (piece.cols + kLossDepth - 1) / kLossDepth * kLossDepth;
+  const int across = (width + kSoftmaxCols - 1) / kSoftmaxCols;
+  const int64_t total = static_cast<int64_t>((padded + kSoftmaxRows - 1) / kSoftmaxRows) * across;
+  for (int64_t k = blockIdx.x; k < total; k += gridDim.x) {
+    const int first = static_cast<int>(k / across) * kSoftmaxRows;
+    const int at = static_cast<int>(k % across) * kSoftmaxCols + threadIdx.x * 8;
+    if (at >= width) continue;
+    const float2* sums = r.sums + static_cast<int64_t>(at >> r.chunk_shift) * r.tokens;
+    uint16_t* g = piece.g + static_cast<int64_t>(first) * piece.ld + at;
+#pragma unroll 8
+    for (int i = 0; i < kSoftmaxRows; ++i) {
+      const int row = first + i;  // padded is a multiple of kSoftmaxRows
+      Vector<Bf16> o = {};        // rows behind the last one are read as zeros
+      if (row < n) {
+        Vector<Fp16> e;
+        __builtin_memcpy(&e, g + static_cast<int64_t>(i) * piece.ld, 16);
+        const float f = __builtin_amdgcn_exp2f((sums[row].x - r.lse[row]) * kLog2e) *
+                        (scale / kLossScale);
+        const int own = r.target[row] - piece.first - at;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o.e[j] = T::encode(Fp16::decode(e.e[j]) * f);
+        if (own >= 0 && own < 8) {
+          // not 1 - p, whose difference loses what a well predicted token has
+          const uint16_t t = T::encode(scale * expm1f(-r.compact_losses[row]));
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o.e[j] = own == j ? t : o.e[j];
+        }
+      }
+      __builtin_memcpy(g + static_cast<int64_t>(i) * piece.ld, &o, 16);
+    }
+  }
+}
 
 // The loss of all tokens, summed in binary64 in a fixed order.
 __global__ __launch_bounds__(1024) void sum_kernel(LossRows r) {
@@ -203,15 +218,15 @@ template <typename T>
 __global__ __launch_bounds__(256) void input_kernel(LossRows r, const float* partial, int splits) {
   const int n = *r.count;
   const float c = (r.mean && n > 1 ? r.scale / static_cast<float>(n) : r.scale) / T::encode_scale;
-  const int64_t stride = static_cast<int64_t>(r.tokens) * r.ldx;
+  const int64_t stride = static_cast<int64_t>(r.tokens) * r.width;
   for (int row = blockIdx.x; row < n; row += gridDim.x) {
     uint16_t* to = r.dx + r.index[row] * r.dx_stride;
-    const float* from = partial + static_cast<int64_t>(row) * r.ldx;
+    const float* from = partial + static_cast<int64_t>(row) * r.width;
     for (int at = threadIdx.x * 8; at < r.hidden; at += 2048) {
       float s[8] = {};
       for (int k = 0; k < splits; ++k) {
         float v[8];
-        __builtin_memcpy(v, from + k * stride + at, 32);  // ldx is a multiple of 8
+        __builtin_memcpy(v, from + k * stride + at, 32);  // width is a multiple of 8
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[i] += v[i];
       }
@@ -242,24 +257,23 @@ hipError_t launch_loss_gather(const LossRows& r, hipStream_t stream, int64_t max
 }
 
 hipError_t launch_pack(const uint16_t* from, int64_t stride, int64_t rows, int cols, uint16_t* to,
-                       int ld, hipStream_t stream, int64_t max_grid) {
-  return launch(pack_kernel, rows, 256, stream, max_grid, from, stride, rows, cols, to, ld);
+                       int width, hipStream_t stream, int64_t max_grid) {
+  return launch(pack_kernel, rows, 256, stream, max_grid, from, stride, rows, cols, to, width);
 }
 
-hipError_t launch_loss_softmax(const LossRows& r, const LossPiece* piece, hipStream_t stream,
+hipError_t launch_loss_lse(const LossRows& r, hipStream_t stream, int64_t max_grid) {
+  // few rows: a workgroup to each
+  if (r.tokens <= 64) return launch(lse_kernel<1>, r.tokens, 1024, stream, max_grid, r);
+  return launch(lse_kernel<16>, (r.tokens + 15) / 16, 1024, stream, max_grid, r);
+}
+
+hipError_t launch_loss_softmax(const LossRows& r, const LossPiece& piece, hipStream_t stream,
                                int64_t max_grid) {
-  const int64_t rows = std::max<int64_t>(
-      1, (static_cast<int64_t>(r.tokens) + kLossDepth - 1) / kLossDepth * kLossDepth);
-  // about 2048 workgroups, of at least 4096 columns each
-  const int64_t width = piece != nullptr ? piece->cols : 0;
-  const int shares = static_cast<int>(std::max<int64_t>(
-      1, std::min<int64_t>((2048 + rows - 1) / rows, width / 4096)));
-  const LossPiece p = piece != nullptr ? *piece : LossPiece{};
-  if (piece == nullptr)
-    return launch(softmax_kernel<ScaledBf16, false>, rows, kSoftmaxThreads, stream, max_grid, r, p,
-                  1);
-  return launch(r.bf16 ? softmax_kernel<ScaledBf16, true> : softmax_kernel<ScaledFp16, true>,
-                rows * shares, kSoftmaxThreads, stream, max_grid, r, p, shares);
+  const int64_t rows = (static_cast<int64_t>(r.tokens) + kLossDepth - 1) / kLossDepth * kLossDepth;
+  const int64_t grid = rows / kSoftmaxRows *
+                       ((static_cast<int64_t>(piece.cols) + kSoftmaxCols - 1) / kSoftmaxCols);
+  return launch(r.bf16 ? softmax_kernel<ScaledBf16> : softmax_kernel<ScaledFp16>, grid, 256, stream,
+                max_grid, r, piece);
 }
 
 hipError_t launch_loss_sum(const LossRows& r, hipStream_t stream) {

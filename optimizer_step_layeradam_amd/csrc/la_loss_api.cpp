@@ -28,7 +28,7 @@ constexpr int64_t kDefaultPieceBytes = int64_t(4) << 30;
 
 struct Plan {
   bool gradients, pack;
-  int64_t rows, ldx;          // padded to whole depths
+  int64_t rows, width;        // padded to whole depths
   int64_t chunks;
   int64_t columns, pieces;    // of a piece; 0 without gradients
   int64_t splits;
@@ -78,12 +78,12 @@ la_status check(const la_cross_entropy_desc* d) {
 void lay_out(const la_cross_entropy_desc& d, int64_t pieces, Plan* p) {
   p->gradients = d.dx != nullptr || d.dweight != nullptr;
   p->rows = round_up(d.tokens, la::kLossDepth);
-  p->ldx = round_up(d.hidden, la::kLossDepth);
+  p->width = round_up(d.hidden, la::kLossDepth);
   // the products read the weight as it lies where its rows are whole depths of
   // aligned pieces, and a padded copy otherwise
   const int64_t ldw = d.vocab > 1 ? d.weight_row_stride : d.hidden;
-  p->pack = p->ldx != d.hidden || ldw % 8 != 0 || ldw > LA_MAX_SIDE || !aligned(d.weight, 16);
-  const int shift = la::loss_chunk_shift(d.tokens);
+  p->pack = p->width != d.hidden || ldw % 8 != 0 || ldw > LA_MAX_SIDE || !aligned(d.weight, 16);
+  const int shift = la::loss_chunk_shift(d.tokens, d.vocab);
   p->chunks = (d.vocab + (int64_t(1) << shift) - 1) >> shift;
   p->columns = p->gradients ? round_up((d.vocab + pieces - 1) / pieces, la::kPieceUnit) : 0;
   p->pieces = p->gradients ? (d.vocab + p->columns - 1) / p->columns : 0;
@@ -92,14 +92,14 @@ void lay_out(const la_cross_entropy_desc& d, int64_t pieces, Plan* p) {
   p->count = take(4);
   p->index = take(4 * d.tokens);
   p->target = take(4 * d.tokens);
-  p->xc = take(2 * p->rows * p->ldx);
-  p->wc = take(p->pack ? 2 * d.vocab * p->ldx : 0);
+  p->xc = take(2 * p->rows * p->width);
+  p->wc = take(p->pack ? 2 * d.vocab * p->width : 0);
   p->sums = take(8 * d.tokens * p->chunks);
   p->target_logit = take(4 * d.tokens);
   p->lse = take(4 * d.tokens);
   p->losses = take(4 * d.tokens);
   p->piece = take(2 * p->rows * p->columns);
-  p->partial = take(4 * p->splits * d.tokens * p->ldx);
+  p->partial = take(4 * p->splits * d.tokens * p->width);
   p->bytes = take.at;
 }
 
@@ -177,10 +177,10 @@ la_status cross_entropy(const la_cross_entropy_desc* d, void* ws, int64_t ws_byt
   r.index = place<int32_t>(ws, p.index);
   r.target = place<int32_t>(ws, p.target);
   r.xc = place<uint16_t>(ws, p.xc);
-  r.ldx = static_cast<int32_t>(p.ldx);
+  r.width = static_cast<int32_t>(p.width);
   r.sums = place<float2>(ws, p.sums);
   r.chunks = static_cast<int32_t>(p.chunks);
-  r.chunk_shift = la::loss_chunk_shift(d->tokens);
+  r.chunk_shift = la::loss_chunk_shift(d->tokens, d->vocab);
   r.target_logit = place<float>(ws, p.target_logit);
   r.lse = place<float>(ws, p.lse);
   r.losses = d->losses;
@@ -200,10 +200,10 @@ la_status cross_entropy(const la_cross_entropy_desc* d, void* ws, int64_t ws_byt
   if (e != hipSuccess) return launch_failed(e);
   if (p.pack) {
     uint16_t* wc = place<uint16_t>(ws, p.wc);
-    e = la::launch_pack(a.w, a.ldw, d->vocab, r.hidden, wc, r.ldx, stream, max_grid);
+    e = la::launch_pack(a.w, a.ldw, d->vocab, r.hidden, wc, r.width, stream, max_grid);
     if (e != hipSuccess) return launch_failed(e);
     a.w = wc;
-    a.ldw = p.ldx;
+    a.ldw = p.width;
   }
   auto product = [&](LossProduct what, int64_t first, int64_t columns) {
     a.piece.g = place<uint16_t>(ws, p.piece);
@@ -217,8 +217,7 @@ la_status cross_entropy(const la_cross_entropy_desc* d, void* ws, int64_t ws_byt
   };
   if (!p.gradients) {
     if ((e = product(LossProduct::kSums, 0, d->vocab)) != hipSuccess) return launch_failed(e);
-    e = la::launch_loss_softmax(r, nullptr, stream, max_grid);
-    if (e != hipSuccess) return launch_failed(e);
+    if ((e = la::launch_loss_lse(r, stream, max_grid)) != hipSuccess) return launch_failed(e);
     if ((e = la::launch_loss_sum(r, stream)) != hipSuccess) return launch_failed(e);
     return ok();
   }
@@ -226,7 +225,8 @@ la_status cross_entropy(const la_cross_entropy_desc* d, void* ws, int64_t ws_byt
       (e = product(LossProduct::kSums, p.columns, d->vocab)) != hipSuccess)
     return launch_failed(e);
   if ((e = product(LossProduct::kKeep, 0, p.columns)) != hipSuccess) return launch_failed(e);
-  e = la::launch_loss_softmax(r, &a.piece, stream, max_grid);
+  if ((e = la::launch_loss_lse(r, stream, max_grid)) != hipSuccess) return launch_failed(e);
+  e = la::launch_loss_softmax(r, a.piece, stream, max_grid);
   if (e != hipSuccess) return launch_failed(e);
   if ((e = la::launch_loss_sum(r, stream)) != hipSuccess) return launch_failed(e);
   for (int64_t k = 0; k < p.pieces; ++k) {

@@ -52,6 +52,28 @@ __device__ __forceinline__ s16x8 rounded(const float (&v)[8]) {
   }
 }
 
+// A lane's value joined with those of the others in its group of 8 or 16, by
+// exchanges within a row of lanes (a sum's order is then the same everywhere).
+template <int CONTROL>
+__device__ __forceinline__ float moved(float x) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CONTROL, 0xF, 0xF, true));
+}
+
+template <int LANES, int SIDE, typename F>
+__device__ __forceinline__ void over_lanes(float (&x)[SIDE], F join) {
+  static_assert(LANES == 8 || LANES == 16, "");
+#pragma unroll
+  for (int u = 0; u < SIDE; ++u) x[u] = join(x[u], moved<0xB1>(x[u]));   // lane ^ 1
+#pragma unroll
+  for (int u = 0; u < SIDE; ++u) x[u] = join(x[u], moved<0x4E>(x[u]));   // lane ^ 2
+#pragma unroll
+  for (int u = 0; u < SIDE; ++u) x[u] = join(x[u], moved<0x141>(x[u]));  // 7 - lane of 8
+  if constexpr (LANES == 16) {
+#pragma unroll
+    for (int u = 0; u < SIDE; ++u) x[u] = join(x[u], moved<0x140>(x[u]));  // 15 - lane of 16
+  }
+}
+
 // ---- the kernel ----------------------------------------------------------------------
 // A workgroup of WM x WN waves forms a tile of (32 MT WM) x (32 NT WN)
 // elements of C = P Q, each wave MT x NT blocks of 32 x 32, as in the products
@@ -75,12 +97,16 @@ struct LossTile {
   static constexpr int threads = 64 * waves;
   static constexpr int rows = 32 * MT * WM, cols = 32 * NT * WN;
   static constexpr int stage = (rows + cols) * kLossDepth;  // elements
+  // BUFFERS 5: five halves of a stage, one operand each (rows == cols)
+  static constexpr bool halves = BUFFERS == 5;
+  static constexpr int elements = halves ? 5 * rows * kLossDepth : BUFFERS * stage;
   static constexpr int p_copies = rows / (8 * waves), q_copies = cols / (8 * waves);
   static constexpr int in_flight = (BUFFERS - 2) * (p_copies + q_copies);
   // the epilogue's part of LDS: blocks of 32 rows that a wave exchanges at once
-  static constexpr int lds = BUFFERS * stage * 2;
+  static constexpr int lds = elements * 2;
   static constexpr int at_once =
       std::min(MT, lds / (waves * 32 * 32 * NT * 4)) >= MT ? MT : lds / (waves * 32 * 32 * NT * 4);
+  static_assert(!halves || rows == cols, "halves of one size");
   static_assert(at_once >= 1 && MT % at_once == 0, "the epilogue's part of LDS");
   static_assert(rows % (8 * waves) == 0 && cols % (8 * waves) == 0, "whole rows per copy");
 };
@@ -98,6 +124,17 @@ __device__ __forceinline__ void place_of(int at, int& row, int& piece) {
   }
 }
 
+typedef const __attribute__((address_space(3))) s16x4* lds_s16x4;
+
+// Four elements of a lane's column from the rows that its 16 lanes address.
+// Without `restrict` the compiler knows nothing about what the read may alias,
+// takes every copy into LDS that is under way for it and waits for all of them
+// before each read; the meetings of the stages order the two.
+__device__ __forceinline__ s16x4 read_turned(lds_s16x4 __restrict__ p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      const_cast<__attribute__((address_space(3))) s16x4*>(p));
+}
+
 // Fragment of 32 rows of the tile from `first` on, step `step` of a stage.
 template <bool TURNED, int SIDE>
 __device__ __forceinline__ s16x8 fragment(const uint16_t* from, int first, int step, int lane) {
@@ -106,10 +143,8 @@ __device__ __forceinline__ s16x8 fragment(const uint16_t* from, int first, int s
     const int row = 16 * step + 8 * (g >> 1) + (i >> 2);
     const int slot = ((first >> 4) + (g & 1)) ^ (((i >> 2) << 1) | (g >> 1));
     const uint16_t* p = from + row * SIDE + slot * 16 + (i & 3) * 4;
-    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (__attribute__((address_space(3))) s16x4*)const_cast<uint16_t*>(p));
-    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (__attribute__((address_space(3))) s16x4*)const_cast<uint16_t*>(p + 4 * SIDE));
+    const s16x4 a = read_turned((lds_s16x4)p);
+    const s16x4 b = read_turned((lds_s16x4)(p + 4 * SIDE));
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
   } else {
     const int row = first + (lane & 31), piece = 2 * step + (lane >> 5);
@@ -124,7 +159,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void loss_product_kernel(LossProdu
   constexpr bool INPUT = WHAT == LossProduct::kInput, WEIGHT = WHAT == LossProduct::kWeight;
   constexpr bool PT = WEIGHT, QT = INPUT || WEIGHT;
   constexpr bool LOGITS = !INPUT && !WEIGHT;
-  __shared__ __align__(1024) uint16_t lds[BUFFERS * G::stage];
+  __shared__ __align__(1024) uint16_t lds[G::elements];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = (wave / WN) * 32 * MT, wn = (wave % WN) * 32 * NT;
@@ -138,8 +173,8 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void loss_product_kernel(LossProdu
   const int whole = (a.piece.cols + kLossDepth - 1) / kLossDepth * kLossDepth;
   const uint16_t* P = LOGITS ? r.xc : a.piece.g;
   const uint16_t* Q = WEIGHT ? r.xc : a.w + a.piece.first * a.ldw;
-  const int ldp = LOGITS ? r.ldx : a.piece.ld;
-  const int ldq = WEIGHT ? r.ldx : static_cast<int>(a.ldw);
+  const int ldp = LOGITS ? r.width : a.piece.ld;
+  const int ldq = WEIGHT ? r.width : static_cast<int>(a.ldw);
   const int tiles_m = (M + G::rows - 1) / G::rows, tiles_n = (N + G::cols - 1) / G::cols;
   const int64_t tiles = static_cast<int64_t>(tiles_m) * tiles_n;
   const int64_t total = tiles * (INPUT ? a.splits : 1);
@@ -151,7 +186,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void loss_product_kernel(LossProdu
     rectangle(static_cast<int>(local - split * tiles), tiles_m, tiles_n, ti, tj);
     const int row0 = ti * G::rows, col0 = tj * G::cols;
     const int k0 = INPUT ? split * a.depth : 0;
-    const int depth = LOGITS ? r.ldx : WEIGHT ? padded : min(a.depth, whole - k0);
+    const int depth = LOGITS ? r.width : WEIGHT ? padded : min(a.depth, whole - k0);
     const int stages = depth > 0 ? depth / kLossDepth : 0;
 
     // Copies of an operand that is contiguous along the sum: rows past its
@@ -177,18 +212,22 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void loss_product_kernel(LossProdu
       place_of<QT, G::cols>((c * G::waves + wave) * 64 + lane, row, piece);
       if constexpr (QT) {
         qo[c] = row * ldq * 2;
-        qc[c] = min(col0 / 8 + piece, r.ldx / 8 - 1) * 16;
+        qc[c] = min(col0 / 8 + piece, r.width / 8 - 1) * 16;
       } else {
         qo[c] = min(row, N - 1 - col0) * ldq * 2 + piece * 16;
       }
     }
     const int64_t p_step = PT ? static_cast<int64_t>(kLossDepth) * ldp : kLossDepth;
     const int64_t q_step = QT ? static_cast<int64_t>(kLossDepth) * ldq : kLossDepth;
-    // copies [from, to) of stage k
-    auto copy = [&](int k, int buffer, int from, int to) {
-      uint16_t* base = lds + buffer * G::stage + wave * 512;
+    // copies [from, to) of an operand's part of stage k
+    auto copy_p = [&](int k, uint16_t* to, int from, int end) {
       const __amdgpu_buffer_rsrc_t rp = __builtin_amdgcn_make_buffer_rsrc(
           const_cast<uint16_t*>(p_first + k * p_step), 0, kRsrcRange, kRsrcWord3);
+#pragma unroll
+      for (int c = from; c < end; ++c)
+        copy_to_lds(rp, to + (c * G::waves + wave) * 512, po[c], 0);
+    };
+    auto copy_q = [&](int k, uint16_t* to, int from, int end) {
       const __amdgpu_buffer_rsrc_t rq = __builtin_amdgcn_make_buffer_rsrc(
           const_cast<uint16_t*>(q_first + k * q_step), 0, kRsrcRange, kRsrcWord3);
       // the last row of w that there is, from the stage's first
@@ -198,30 +237,32 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void loss_product_kernel(LossProdu
         if (rows < kLossDepth) last = static_cast<int>(rows) * ldq * 2;
       }
 #pragma unroll
-      for (int c = from; c < to; ++c) {
-        uint16_t* at = base + c * G::waves * 512;
-        if (c < G::p_copies) {
-          copy_to_lds(rp, at, po[c < G::p_copies ? c : 0], 0);
-        } else {
-          const int j = c - G::p_copies;
-          if constexpr (QT)
-            copy_to_lds(rq, at, (INPUT ? min(qo[j], last) : qo[j]) + qc[j], 0);
-          else
-            copy_to_lds(rq, at, qo[j], 0);
-        }
-      }
+      for (int c = from; c < end; ++c)
+        copy_to_lds(rq, to + (c * G::waves + wave) * 512,
+                    QT ? (INPUT ? min(qo[c], last) : qo[c]) + qc[QT ? c : 0] : qo[c], 0);
     };
     struct Fragments {
       s16x8 p[MT], q[NT];
     };
-    auto read = [&](Fragments& f, int buffer, int step) {
-      const uint16_t* from = lds + buffer * G::stage;
+    auto read = [&](Fragments& f, const uint16_t* p, const uint16_t* q, int step) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i) f.p[i] = fragment<PT, G::rows>(from, wm + 32 * i, step, lane);
-      from += G::rows * kLossDepth;
+      for (int i = 0; i < MT; ++i) f.p[i] = fragment<PT, G::rows>(p, wm + 32 * i, step, lane);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) f.q[j] = fragment<QT, G::cols>(from, wn + 32 * j, step, lane);
+      for (int j = 0; j < NT; ++j) f.q[j] = fragment<QT, G::cols>(q, wn + 32 * j, step, lane);
     };
+    // The targets and lse of the wave's rows, a lane to a row.
+    struct {
+      int target[MT > 2 ? 2 : 1];
+      float lse[MT > 2 ? 2 : 1];
+    } mine = {};
+    if constexpr (LOGITS) {
+#pragma unroll
+      for (int i = 0; i < (MT > 2 ? 2 : 1); ++i) {
+        const int row = min(row0 + wm + 64 * i + lane, M - 1);
+        mine.target[i] = r.target[row];
+        if constexpr (WHAT == LossProduct::kAgain) mine.lse[i] = r.lse[row];
+      }
+    }
     f32x16 acc[MT][NT] = {};
     auto multiply = [&](const Fragments& f) {
 #pragma unroll
@@ -229,160 +270,273 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void loss_product_kernel(LossProdu
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[i][j] = mfma<T>(f.p[i], f.q[j], acc[i][j]);
     };
-    constexpr int ALL = G::p_copies + G::q_copies;
-    Fragments f[2];
+    // Deals a step's reads of LDS, and behind them `copies` copies, out among
+    // its products (as in la_product.hip: issued in a row they hold the products up).
+    auto interleave = [&](auto copies) {
+      constexpr int reads = (PT ? 2 : 1) * MT + (QT ? 2 : 1) * NT, products = MT * NT;
+      constexpr int n = decltype(copies)::value;
+      constexpr int pairs = reads + n > products ? 2 : 1;  // reads beside one product
+      constexpr int each = n == 0 && products > reads ? products / reads : 1;
 #pragma unroll
-    for (int k = 0; k < BUFFERS - 1; ++k)
-      if (k < stages) copy(k, k, 0, ALL);
-    if (stages >= BUFFERS - 1) wait_and_meet<G::in_flight>();
-    else wait_and_meet<0>();
-    if (stages > 0) read(f[0], 0, 0);
-    int buffer = 0;
-    for (int k = 0; k < stages; ++k) {
-      const int next = buffer + 1 == BUFFERS ? 0 : buffer + 1;
-      const int last = buffer == 0 ? BUFFERS - 1 : buffer - 1;
-      const bool more = k + BUFFERS - 1 < stages;
-      if (more) copy(k + BUFFERS - 1, last, 0, ALL);
-#pragma unroll
-      for (int step = 1; step < kLossDepth / 16; ++step) {
-        read(f[step & 1], buffer, step);
-        multiply(f[(step - 1) & 1]);
+      for (int i = 0; i < reads / pairs; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x100, pairs, 0);  // LDS read
+        __builtin_amdgcn_sched_group_barrier(0x008, each, 0);   // MFMA
       }
-      if (more) wait_and_meet<G::in_flight>();
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);  // copy
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      }
+      if constexpr (products > reads / pairs * each + n)
+        __builtin_amdgcn_sched_group_barrier(0x008, products - reads / pairs * each - n, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    using None = std::integral_constant<int, 0>;
+    Fragments f[2];
+    if constexpr (G::halves) {
+      // LDS holds five operands' parts, P_0 Q_0 P_1 Q_1 P_2, then Q_2 in the place of
+      // P_0 and so on: part i lies at i % 5. Behind the meeting after stage k's
+      // last reads its places take Q of stage k + 2, at once, and P of stage k + 3,
+      // which has a whole stage more to arrive: the meeting waits for older copies
+      // only. The loop has no branch that would part the products: past the end the
+      // last stage is copied again, into places that nobody reads.
+      if (stages > 0) {
+        auto stage = [&](int k) { return k < stages ? k : stages - 1; };
+        constexpr int half = G::rows * kLossDepth;
+        copy_p(0, lds, 0, G::p_copies);
+        copy_q(0, lds + half, 0, G::q_copies);
+        copy_p(stage(1), lds + 2 * half, 0, G::p_copies);
+        copy_q(stage(1), lds + 3 * half, 0, G::q_copies);
+        wait_and_meet<G::p_copies + G::q_copies>();
+        read(f[0], lds, lds + half, 0);
+        using Qcopies = std::integral_constant<int, G::q_copies>;
+        using Phalf = std::integral_constant<int, G::p_copies / 2>;
+        int at = 0;  // place of P_k
+        for (int k = 0; k < stages; ++k) {
+          auto place = [&](int i) { return lds + (at + i < 5 ? at + i : at + i - 5) * half; };
+          uint16_t *p = place(0), *q = place(1), *later = place(4);
+          read(f[1], p, q, 1);
+          copy_p(stage(k + 2), later, 0, G::p_copies / 2);
+          multiply(f[0]);
+          interleave(Phalf());
+          read(f[0], p, q, 2);
+          copy_p(stage(k + 2), later, G::p_copies / 2, G::p_copies);
+          multiply(f[1]);
+          interleave(Phalf());
+          read(f[1], p, q, 3);
+          multiply(f[0]);
+          interleave(None());
+          wait_and_meet<G::p_copies>();
+          read(f[0], place(2), place(3), 0);
+          copy_q(stage(k + 2), p, 0, G::q_copies);
+          multiply(f[1]);
+          interleave(Qcopies());
+          at = at + 2 < 5 ? at + 2 : at - 3;
+        }
+      }
+      wait_and_meet<0>();
+    } else {
+      auto copy = [&](int k, int buffer) {
+        uint16_t* to = lds + buffer * G::stage;
+        copy_p(k, to, 0, G::p_copies);
+        copy_q(k, to + G::rows * kLossDepth, 0, G::q_copies);
+      };
+      auto part = [&](Fragments& to, int buffer, int step) {
+        const uint16_t* from = lds + buffer * G::stage;
+        read(to, from, from + G::rows * kLossDepth, step);
+      };
+#pragma unroll
+      for (int k = 0; k < BUFFERS - 1; ++k)
+        if (k < stages) copy(k, k);
+      if (stages >= BUFFERS - 1) wait_and_meet<G::in_flight>();
       else wait_and_meet<0>();
-      if (k + 1 < stages) read(f[0], next, 0);
-      multiply(f[1]);
-      buffer = next;
+      if (stages > 0) part(f[0], 0, 0);
+      int buffer = 0;
+      for (int k = 0; k < stages; ++k) {
+        const int next = buffer + 1 == BUFFERS ? 0 : buffer + 1;
+        const int last = buffer == 0 ? BUFFERS - 1 : buffer - 1;
+        const bool more = k + BUFFERS - 1 < stages;
+        if (more) copy(k + BUFFERS - 1, last);
+#pragma unroll
+        for (int step = 1; step < kLossDepth / 16; ++step) {
+          part(f[step & 1], buffer, step);
+          multiply(f[(step - 1) & 1]);
+          interleave(None());
+        }
+        if (more) wait_and_meet<G::in_flight>();
+        else wait_and_meet<0>();
+        if (k + 1 < stages) part(f[0], next, 0);
+        multiply(f[1]);
+        buffer = next;
+      }
     }
     // Every wave is past its last read of LDS, and no copy is under way.
-    if constexpr (INPUT) {
-      // The accumulators as they lie (lane l: column l % 32; register e: row 8 (e / 4) + 4
-      // (l / 32) + e % 4): 32 lanes store 128 bytes of a row.
-      float* to = a.partial + static_cast<int64_t>(split) * r.tokens * r.ldx;
+    // The sums change to eight neighbours of a row per lane through the wave's own
+    // part of LDS, at_once blocks of 32 rows at a time; every four rows the halves
+    // of 64 columns are exchanged, so that both halves of a wave store to banks of
+    // their own.
+    constexpr int WIDTH = 32 * NT, LANES = WIDTH / 8, TOGETHER = 64 / LANES;
+    // rows of a lane that are worked on side by side: alone, a row is a chain of
+    // exchanges that the wave would wait for
+    constexpr int SIDE = 4, PASSES = 32 * G::at_once / TOGETHER;
+    static_assert(PASSES % SIDE == 0, "whole passes");
+    float* sums = reinterpret_cast<float*>(lds) + wave * (32 * G::at_once * WIDTH);
+    const int k8 = (lane % LANES) * 8, col = col0 + wn + k8;
+    const float c_out = WEIGHT ? (r.mean && n > 1 ? r.scale / static_cast<float>(n) : r.scale) /
+                                     (std::is_same<T, Bf16>::value ? 1.0f : kLossScale)
+                               : 0.0f;
+    const bool edge = col0 + G::cols > N;
+    const int chunk = LOGITS ? (a.piece.first + col0 + wn) >> r.chunk_shift : 0;
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+    for (int part = 0; part < MT / G::at_once; ++part) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const int col = col0 + wn + 32 * j + (lane & 31);
+      for (int i = 0; i < G::at_once; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const int row = row0 + wm + 32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-            if (row < M && col < r.ldx) {
-              float* at = to + static_cast<int64_t>(row) * r.ldx + col;
-              *at = a.add ? *at + acc[i][j][e] : acc[i][j][e];
+            const int row = 32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
+            sums[row * WIDTH + ((32 * j + (lane & 31)) ^ ((lane >> 5) << 5))] =
+                acc[part * G::at_once + i][j][e];
+          }
+      wave_fence();
+#pragma unroll 1
+      for (int p = 0; p < PASSES; p += SIDE) {
+        float v[SIDE][8];
+        int row[SIDE];
+#pragma unroll
+        for (int u = 0; u < SIDE; ++u) {
+          const int local_row = (p + u) * TOGETHER + lane / LANES;
+          row[u] = row0 + wm + 32 * G::at_once * part + local_row;
+          const float* from = sums + local_row * WIDTH + (k8 ^ (((local_row >> 2) & 1) << 5));
+          *reinterpret_cast<f32x4*>(v[u]) = *reinterpret_cast<const f32x4*>(from);
+          *reinterpret_cast<f32x4*>(v[u] + 4) = *reinterpret_cast<const f32x4*>(from + 4);
+        }
+        if constexpr (INPUT) {
+#pragma unroll
+          for (int u = 0; u < SIDE; ++u) {
+            if (row[u] >= M || col >= r.width) continue;
+            float* to =
+                a.partial + (static_cast<int64_t>(split) * r.tokens + row[u]) * r.width + col;
+            f32x4 lo = *reinterpret_cast<const f32x4*>(v[u]);
+            f32x4 hi = *reinterpret_cast<const f32x4*>(v[u] + 4);
+            if (a.add) {
+              lo += *reinterpret_cast<const f32x4*>(to);
+              hi += *reinterpret_cast<const f32x4*>(to + 4);
+            }
+            *reinterpret_cast<f32x4*>(to) = lo;
+            *reinterpret_cast<f32x4*>(to + 4) = hi;
+          }
+        } else if constexpr (WEIGHT) {
+#pragma unroll
+          for (int u = 0; u < SIDE; ++u) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[u][e] *= c_out;
+            const s16x8 o = rounded<T>(v[u]);
+            if (row[u] >= M || col >= N) continue;
+            uint16_t* to = a.dw + (a.piece.first + row[u]) * a.dw_stride + col;
+            if (a.dw_vectors && col + 8 <= N) {
+              *reinterpret_cast<s16x8*>(to) = o;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (col + e < N) to[e] = o[e];
             }
           }
-        }
-    } else {
-      // The sums change to eight neighbours of a row per lane through the wave's own
-      // part of LDS, at_once blocks of 32 rows at a time; every four rows the halves
-      // of 64 columns are exchanged, so that both halves of a wave store to banks of
-      // their own.
-      constexpr int WIDTH = 32 * NT, LANES = WIDTH / 8, TOGETHER = 64 / LANES;
-      float* sums = reinterpret_cast<float*>(lds) + wave * (32 * G::at_once * WIDTH);
-      const int k8 = (lane % LANES) * 8, col = col0 + wn + k8;
-      const float c_out = WEIGHT ? (r.mean && n > 1 ? r.scale / static_cast<float>(n) : r.scale) /
-                                       (std::is_same<T, Bf16>::value ? 1.0f : kLossScale)
-                                 : 0.0f;
+        } else {
+          int own[SIDE];      // the target's place among the lane's columns
+          float lse[SIDE];
 #pragma unroll
-      for (int part = 0; part < MT / G::at_once; ++part) {
-#pragma unroll
-        for (int i = 0; i < G::at_once; ++i)
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int row = 32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-              sums[row * WIDTH + ((32 * j + (lane & 31)) ^ ((lane >> 5) << 5))] =
-                  acc[part * G::at_once + i][j][e];
+          for (int u = 0; u < SIDE; ++u) {
+            // lanes hold what belongs to the wave's rows
+            const int at = row[u] - row0 - wm;
+            own[u] = __shfl(mine.target[0], at & 63, 64);
+            if constexpr (MT == 4) {
+              const int other = __shfl(mine.target[1], at & 63, 64);
+              own[u] = at < 64 ? own[u] : other;
             }
-        wave_fence();
-#pragma unroll 2
-        for (int p = 0; p < 32 * G::at_once / TOGETHER; ++p) {
-          const int local_row = p * TOGETHER + lane / LANES;
-          const int row = row0 + wm + 32 * G::at_once * part + local_row;
-          const float* from = sums + local_row * WIDTH + (k8 ^ (((local_row >> 2) & 1) << 5));
-          float v[8];
-          *reinterpret_cast<f32x4*>(v) = *reinterpret_cast<const f32x4*>(from);
-          *reinterpret_cast<f32x4*>(v + 4) = *reinterpret_cast<const f32x4*>(from + 4);
-          if constexpr (WEIGHT) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] *= c_out;
-            const s16x8 o = rounded<T>(v);
-            if (row < M && col < N) {
-              uint16_t* to = a.dw + (a.piece.first + row) * a.dw_stride + col;
-              if (a.dw_vectors && col + 8 <= N) {
-                *reinterpret_cast<s16x8*>(to) = o;
-              } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  if (col + e < N) to[e] = o[e];
-              }
-            }
-          } else {
-            // columns behind the piece count as exp(-inf)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (col + e >= N) v[e] = -__builtin_inff();
-            const bool kept = row < M;
-            const int own = kept ? r.target[row] - a.piece.first - col : -1;
+            own[u] -= a.piece.first + col;
             if constexpr (WHAT == LossProduct::kAgain) {
-              if (kept && col0 + wn < whole) {
-                const float lse = r.lse[row];
-                constexpr float scale = std::is_same<T, Bf16>::value ? 1.0f : kLossScale;
-                float at_target = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  if (own == e) at_target = scale * expm1f(v[e] - lse);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  v[e] = scale * __builtin_amdgcn_exp2f((v[e] - lse) * kLog2e);
-                  if (own == e) v[e] = at_target;
-                }
-                if (col < a.piece.ld)
-                  *reinterpret_cast<s16x8*>(a.piece.g + static_cast<int64_t>(row) * a.piece.ld +
-                                            col) = rounded<T>(v);
+              lse[u] = __shfl(mine.lse[0], at & 63, 64);
+              if constexpr (MT == 4) {
+                const float other = __shfl(mine.lse[1], at & 63, 64);
+                lse[u] = at < 64 ? lse[u] : other;
               }
-            } else {
-              if (own >= 0 && own < 8) {
-                float z = v[0];
+            }
+            if (edge) {  // columns behind the piece count as exp(-inf)
 #pragma unroll
-                for (int e = 1; e < 8; ++e) z = own == e ? v[e] : z;
-                r.target_logit[row] = z;
+              for (int e = 0; e < 8; ++e)
+                if (col + e >= N) v[u][e] = -__builtin_inff();
+            }
+          }
+          if constexpr (WHAT == LossProduct::kAgain) {
+#pragma unroll
+            for (int u = 0; u < SIDE; ++u) {
+              constexpr float scale = std::is_same<T, Bf16>::value ? 1.0f : kLossScale;
+              float at_target = 0.0f;
+              if (own[u] >= 0 && own[u] < 8) {
+                float z = v[u][0];
+#pragma unroll
+                for (int e = 1; e < 8; ++e) z = own[u] == e ? v[u][e] : z;
+                at_target = scale * expm1f(z - lse[u]);
               }
-              float most = v[0];
-#pragma unroll
-              for (int e = 1; e < 8; ++e) most = __builtin_fmaxf(most, v[e]);
-#pragma unroll
-              for (int d = LANES / 2; d > 0; d >>= 1)
-                most = __builtin_fmaxf(most, __shfl_xor(most, d, 64));
-              // nothing in these columns: their exponentials are 0 from any point
-              const float from_here = most == -__builtin_inff() ? 0.0f : most;
-              float sum = 0.0f;
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                v[e] = __builtin_amdgcn_exp2f((v[e] - from_here) * kLog2e);
-                sum += v[e];
+                v[u][e] = scale * __builtin_amdgcn_exp2f((v[u][e] - lse[u]) * kLog2e);
+                v[u][e] = own[u] == e ? at_target : v[u][e];
               }
+              if (row[u] < M && col < a.piece.ld)
+                *reinterpret_cast<s16x8*>(a.piece.g + static_cast<int64_t>(row[u]) * a.piece.ld +
+                                          col) = rounded<T>(v[u]);
+            }
+          } else {
+            float most[SIDE], sum[SIDE];
 #pragma unroll
-              for (int d = LANES / 2; d > 0; d >>= 1) sum += __shfl_xor(sum, d, 64);
-              const int chunk = (a.piece.first + col0 + wn) >> r.chunk_shift;
-              if (kept && lane % LANES == 0 && chunk < r.chunks)
-                r.sums[static_cast<int64_t>(row) * r.chunks + chunk] = make_float2(most, sum);
+            for (int u = 0; u < SIDE; ++u) {
+              if (own[u] >= 0 && own[u] < 8 && row[u] < M) {
+                float z = v[u][0];
+#pragma unroll
+                for (int e = 1; e < 8; ++e) z = own[u] == e ? v[u][e] : z;
+                r.target_logit[row[u]] = z;
+              }
+              most[u] = v[u][0];
+#pragma unroll
+              for (int e = 1; e < 8; ++e) most[u] = __builtin_fmaxf(most[u], v[u][e]);
+            }
+            over_lanes<LANES, SIDE>(most, [](float x, float y) { return __builtin_fmaxf(x, y); });
+#pragma unroll
+            for (int u = 0; u < SIDE; ++u) {
+              // nothing in these columns: their exponentials are 0 from any point
+              const float from_here = most[u] == -__builtin_inff() ? 0.0f : most[u];
+              sum[u] = 0.0f;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                v[u][e] = __builtin_amdgcn_exp2f((v[u][e] - from_here) * kLog2e);
+                sum[u] += v[u][e];
+              }
+            }
+            over_lanes<LANES, SIDE>(sum, [](float x, float y) { return x + y; });
+#pragma unroll
+            for (int u = 0; u < SIDE; ++u) {
+              if (row[u] < M && lane % LANES == 0 && chunk < r.chunks)
+                r.sums[static_cast<int64_t>(chunk) * r.tokens + row[u]] =
+                    make_float2(most[u], sum[u]);
               if constexpr (WHAT == LossProduct::kKeep) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] *= kLossScale;
-                if (kept && col < a.piece.ld)
-                  *reinterpret_cast<s16x8*>(a.piece.g + static_cast<int64_t>(row) * a.piece.ld +
-                                            col) = rounded<Fp16>(v);
+                for (int e = 0; e < 8; ++e) v[u][e] *= kLossScale;
+                if (row[u] < M && col < a.piece.ld)
+                  *reinterpret_cast<s16x8*>(a.piece.g + static_cast<int64_t>(row[u]) * a.piece.ld +
+                                            col) = rounded<Fp16>(v[u]);
               }
             }
           }
         }
-        wave_fence();
       }
+      wave_fence();
     }
-    wait_and_meet<0>();  // LDS is free for the next tile, and no store is counted with its copies
+    // LDS is free for the next tile, and no store is counted with its copies; the last
+    // tile's stores need nobody to wait for them
+    if (w + gridDim.x < total) wait_and_meet<0>();
   }
 }
 
@@ -403,9 +557,23 @@ hipError_t launch_tile(const LossProductArgs& a, hipStream_t stream, int64_t max
       dim3(static_cast<unsigned>(grid)), dim3(G::threads), params, 0, stream);
 }
 
+// Whether a product of m x n, taken `times` over, goes in 256 x 256 tiles: one
+// takes 5/3 of the time of one of 128 x 128, on 256 compute units.
+bool large_tiles(int64_t m, int64_t n, int64_t times) {
+  auto rounds = [&](int64_t side) {
+    return (((m + side - 1) / side) * ((n + side - 1) / side) * times + 255) / 256;
+  };
+  return 5 * rounds(256) < 3 * rounds(128);
+}
+
 template <typename T, LossProduct WHAT>
 hipError_t launch_one(const LossProductArgs& a, hipStream_t stream, int64_t max_grid) {
-  return launch_tile<T, WHAT, 2, 2, 2, 2, 4>(a, stream, max_grid);
+  constexpr bool INPUT = WHAT == LossProduct::kInput, WEIGHT = WHAT == LossProduct::kWeight;
+  const bool large = INPUT    ? large_tiles(a.r.tokens, a.r.hidden, a.splits)
+                     : WEIGHT ? large_tiles(a.piece.cols, a.r.hidden, 1)
+                              : a.r.chunk_shift == 7;
+  return large ? launch_tile<T, WHAT, 4, 4, 2, 2, 5>(a, stream, max_grid)
+               : launch_tile<T, WHAT, 2, 2, 2, 2, 4>(a, stream, max_grid);
 }
 
 template <typename T>
@@ -422,12 +590,24 @@ hipError_t launch_type(const LossProductArgs& a, LossProduct what, hipStream_t s
 
 }  // namespace
 
-int loss_chunk_shift(int64_t) { return 6; }
+int loss_chunk_shift(int64_t tokens, int64_t vocab) {
+  return large_tiles(tokens, vocab, 1) ? 7 : 6;
+}
 
 int loss_splits(int64_t tokens, int64_t hidden, int64_t columns) {
-  const int64_t tiles = std::max<int64_t>(1, (tokens + 127) / 128) * ((hidden + 127) / 128);
-  return static_cast<int>(
-      std::max<int64_t>(1, std::min<int64_t>((512 + tiles - 1) / tiles, columns / 1024)));
+  // as many parts as fill the last round of tiles best, of at least 2048 columns
+  const int64_t tiles = std::max<int64_t>(1, (tokens + 255) / 256) * ((hidden + 255) / 256);
+  int64_t best = 1;
+  double best_fill = 0.0;
+  for (int64_t s = 1; s <= 32 && (s == 1 || columns / s >= 2048); ++s) {
+    const int64_t work = tiles * s, rounds = (work + 255) / 256;
+    const double fill = static_cast<double>(work) / static_cast<double>(rounds * 256);
+    if (fill > best_fill + 0.02) {
+      best_fill = fill;
+      best = s;
+    }
+  }
+  return static_cast<int>(best);
 }
 
 hipError_t launch_loss_product(const LossProductArgs& a, LossProduct what, hipStream_t stream,
