@@ -90,6 +90,7 @@ struct LossProductArgs {
   int64_t ldw;
   float* partial;           // kInput: splits x tokens x width
   int32_t splits;           // kInput: parts of the sum over the piece
+  int32_t large_input;      // kInput: in 256 x 256 tiles
   int32_t depth;            // kInput: columns of one part, a multiple of 64
   int32_t add;              // kInput: to what is there
   uint16_t* dw;             // kWeight
@@ -103,18 +104,21 @@ int loss_chunk_shift(int64_t tokens, int64_t vocab);
 hipError_t launch_loss_gather(const LossRows& r, hipStream_t stream, int64_t max_grid);
 hipError_t launch_pack(const uint16_t* from, int64_t stride, int64_t rows, int cols, uint16_t* to,
                        int width, hipStream_t stream, int64_t max_grid);
-// lse and losses from the chunks.
+// lse and losses from the chunks, and the loss from those.
 hipError_t launch_loss_lse(const LossRows& r, hipStream_t stream, int64_t max_grid);
 // e becomes g in the first piece.
 hipError_t launch_loss_softmax(const LossRows& r, const LossPiece& piece, hipStream_t stream,
                                int64_t max_grid);
-hipError_t launch_loss_sum(const LossRows& r, hipStream_t stream);
 hipError_t launch_loss_input(const LossRows& r, const float* partial, int splits,
                              hipStream_t stream, int64_t max_grid);
 
 hipError_t launch_loss_product(const LossProductArgs& a, LossProduct what, hipStream_t stream,
                                int64_t max_grid);
-// Parts of the sum of kInput that fill the GPU.
-int loss_splits(int64_t tokens, int64_t hidden, int64_t columns);
+// Parts of the sum of kInput, and its tiles.
+struct LossSplits {
+  int parts;
+  bool large;
+};
+LossSplits loss_splits(int64_t tokens, int64_t hidden, int64_t columns);
 
 }  // namespace la

@@ -46,35 +46,84 @@ __global__ __launch_bounds__(1024) void index_kernel(LossRows r) {
     if (counts) {
       r.index[at] = t;
       r.target[at] = y >= 0 && y < r.vocab ? static_cast<int>(y) : -1;
-    } else if (t < r.tokens && r.losses != nullptr) {
-      r.losses[t] = 0.0f;
     }
     __syncthreads();
   }
   if (threadIdx.x == 0) *r.count = before;
 }
 
-// Rows of x that count, one after the other, zeros behind each and behind the
-// last; dx rows of the others become zeros.
+// A token that does not count: its loss and its dx.
+__device__ __forceinline__ void clear_token(const LossRows& r, int t) {
+  if (threadIdx.x == 0 && r.losses != nullptr) r.losses[t] = 0.0f;
+  if (r.dx == nullptr) return;
+  const Vector<Bf16> zero = {};
+  for (int at = threadIdx.x * 8; at < r.hidden; at += 2048)
+    store_vector<Bf16>(r.dx + t * r.dx_stride, at, r.hidden, zero);
+}
+
+// Row `row` of the gathered x: token t's, zeros behind it; t < 0: zeros.
+__device__ __forceinline__ void gather_row(const LossRows& r, int row, int t) {
+  const uint16_t* from = t < 0 ? r.x : r.x + t * r.x_stride;
+  uint16_t* to = r.xc + static_cast<int64_t>(row) * r.width;
+  for (int at = threadIdx.x * 8; at < r.width; at += 2048)
+    store_vector<Bf16>(to, at, r.width, load_vector<Bf16>(from, at, t < 0 ? 0 : r.hidden));
+}
+
+// Rows of x that count, one after the other, zeros behind the last up to a
+// whole depth.
 __global__ __launch_bounds__(256) void gather_kernel(LossRows r) {
   const int n = *r.count;
   const int padded = (n + kLossDepth - 1) / kLossDepth * kLossDepth;
-  for (int row = blockIdx.x; row < padded; row += gridDim.x) {
-    const uint16_t* from = row < n ? r.x + r.index[row] * r.x_stride : r.x;
-    const int cols = row < n ? r.hidden : 0;
-    uint16_t* to = r.xc + static_cast<int64_t>(row) * r.width;
-    for (int at = threadIdx.x * 8; at < r.width; at += 2048) {
-      const Vector<Bf16> v = load_vector<Bf16>(from, at, cols);
-      store_vector<Bf16>(to, at, r.width, v);
+  for (int row = blockIdx.x; row < padded; row += gridDim.x)
+    gather_row(r, row, row < n ? r.index[row] : -1);
+  if (n == r.tokens || (r.dx == nullptr && r.losses == nullptr)) return;
+  for (int t = blockIdx.x; t < r.tokens; t += gridDim.x)
+    if (target_of(r, t) == r.ignore_index) clear_token(r, t);
+}
+
+// Both in one launch where there are few tokens: every workgroup counts all
+// targets, those before its own token apart. Workgroups past the tokens fill
+// the last depth.
+constexpr int kCountedTokens = 2048;
+
+__global__ __launch_bounds__(256) void index_gather_kernel(LossRows r) {
+  __shared__ int parts[2][4];
+  for (int t = blockIdx.x; t < r.tokens + kLossDepth; t += gridDim.x) {
+    int before = 0, all = 0;
+    for (int i = threadIdx.x; i < r.tokens; i += 256) {
+      const bool counts = target_of(r, i) != r.ignore_index;
+      all += counts;
+      before += counts && i < t;
     }
-  }
-  if (r.dx == nullptr || n == r.tokens) return;
-  for (int t = blockIdx.x; t < r.tokens; t += gridDim.x) {
-    if (target_of(r, t) != r.ignore_index) continue;
-    uint16_t* to = r.dx + t * r.dx_stride;
-    const Vector<Bf16> zero = {};
-    for (int at = threadIdx.x * 8; at < r.hidden; at += 2048)
-      store_vector<Bf16>(to, at, r.hidden, zero);
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) {
+      before += __shfl_xor(before, d, 64);
+      all += __shfl_xor(all, d, 64);
+    }
+    __syncthreads();  // the last token's parts have been read
+    if ((threadIdx.x & 63) == 0) {
+      parts[0][threadIdx.x >> 6] = before;
+      parts[1][threadIdx.x >> 6] = all;
+    }
+    __syncthreads();
+    before = parts[0][0] + parts[0][1] + parts[0][2] + parts[0][3];
+    all = parts[1][0] + parts[1][1] + parts[1][2] + parts[1][3];
+    if (t >= r.tokens) {
+      const int row = all + t - r.tokens;
+      if (row < (all + kLossDepth - 1) / kLossDepth * kLossDepth) gather_row(r, row, -1);
+      if (t == r.tokens && threadIdx.x == 0) *r.count = all;
+      continue;
+    }
+    const int64_t y = target_of(r, t);
+    if (y == r.ignore_index) {
+      clear_token(r, t);
+      continue;
+    }
+    if (threadIdx.x == 0) {
+      r.index[before] = t;
+      r.target[before] = y >= 0 && y < r.vocab ? static_cast<int>(y) : -1;
+    }
+    gather_row(r, before, t);
   }
 }
 
@@ -86,6 +135,14 @@ __global__ __launch_bounds__(256) void pack_kernel(const uint16_t* from, int64_t
     for (int at = threadIdx.x * 8; at < width; at += 2048)
       store_vector<Bf16>(to + row * width, at, width, load_vector<Bf16>(from + row * stride, at, cols));
 }
+
+// The types of g, and their scale.
+struct ScaledBf16 : Bf16 {
+  static constexpr float encode_scale = 1.0f;
+};
+struct ScaledFp16 : Fp16 {
+  static constexpr float encode_scale = kLossScale;
+};
 
 // ---- softmax --------------------------------------------------------------------------
 
@@ -110,6 +167,7 @@ template <int ROWS>
 __global__ __launch_bounds__(1024) void lse_kernel(LossRows r) {
   constexpr int SHARES = 1024 / ROWS;
   __shared__ float2 parts[SHARES][ROWS];
+  __shared__ float own[ROWS];
   const int n = *r.count;
   const int share = threadIdx.x / ROWS, lane = threadIdx.x % ROWS;
   for (int first = blockIdx.x * ROWS; first < n; first += gridDim.x * ROWS) {
@@ -148,19 +206,30 @@ __global__ __launch_bounds__(1024) void lse_kernel(LossRows r) {
       const float log_sum = __builtin_logf(sum), nan = __builtin_nanf("");
       const float loss = outside ? nan : (most - r.target_logit[row]) + log_sum;
       r.lse[row] = outside ? nan : most + log_sum;
-      r.compact_losses[row] = loss;
+      r.compact_losses[row] = own[lane] = loss;
       if (r.losses != nullptr) r.losses[r.index[row]] = loss;
     }
     __syncthreads();
   }
+  // The one workgroup of a call of few tokens adds their losses up itself.
+  if (r.tokens <= ROWS && threadIdx.x == 0) {
+    double s = 0.0;
+    for (int i = 0; i < n; ++i) s += static_cast<double>(own[i]);
+    *r.loss = static_cast<float>(r.mean && n > 1 ? s / static_cast<double>(n) : s);
+  }
 }
 
-struct ScaledBf16 : Bf16 {
-  static constexpr float encode_scale = 1.0f;
-};
-struct ScaledFp16 : Fp16 {
-  static constexpr float encode_scale = kLossScale;
-};
+// The loss of all tokens, summed in binary64 in a fixed order. (Not by the last
+// workgroup of lse_kernel: the fence that it would take writes back what L2
+// holds of e, 150 us where e is 2.4 GB.)
+__global__ __launch_bounds__(1024) void sum_kernel(LossRows r) {
+  const int n = *r.count;
+  double s = 0.0;
+  for (int i = threadIdx.x; i < n; i += 1024) s += static_cast<double>(r.compact_losses[i]);
+  s = block_sum<1024>(s);
+  if (threadIdx.x == 0)
+    *r.loss = static_cast<float>(r.mean && n > 1 ? s / static_cast<double>(n) : s);
+}
 
 // e of the held piece becomes g, in place: 16 rows of 2048 columns a workgroup.
 constexpr int kSoftmaxRows = 16, kSoftmaxCols = 2048;
@@ -203,37 +272,36 @@ __global__ __launch_bounds__(256) void softmax_kernel(LossRows r, LossPiece piec
   }
 }
 
-// The loss of all tokens, summed in binary64 in a fixed order.
-__global__ __launch_bounds__(1024) void sum_kernel(LossRows r) {
-  const int n = *r.count;
-  double s = 0.0;
-  for (int i = threadIdx.x; i < n; i += 1024) s += static_cast<double>(r.compact_losses[i]);
-  s = block_sum<1024>(s);
-  if (threadIdx.x == 0)
-    *r.loss = static_cast<float>(r.mean && n > 1 ? s / static_cast<double>(n) : s);
-}
-
-// dx of the gathered tokens from the parts of their sums, in order.
+// dx of the gathered tokens from the parts of their sums, in order: 1024
+// columns of a row a workgroup.
 template <typename T>
 __global__ __launch_bounds__(256) void input_kernel(LossRows r, const float* partial, int splits) {
-  const int n = *r.count;
+  const int n = *r.count, across = (r.width + 1023) / 1024;
   const float c = (r.mean && n > 1 ? r.scale / static_cast<float>(n) : r.scale) / T::encode_scale;
   const int64_t stride = static_cast<int64_t>(r.tokens) * r.width;
-  for (int row = blockIdx.x; row < n; row += gridDim.x) {
-    uint16_t* to = r.dx + r.index[row] * r.dx_stride;
-    const float* from = partial + static_cast<int64_t>(row) * r.width;
-    for (int at = threadIdx.x * 8; at < r.hidden; at += 2048) {
-      float s[8] = {};
-      for (int k = 0; k < splits; ++k) {
-        float v[8];
-        __builtin_memcpy(v, from + k * stride + at, 32);  // width is a multiple of 8
+  for (int64_t k = blockIdx.x; k < static_cast<int64_t>(n) * across; k += gridDim.x) {
+    const int row = static_cast<int>(k / across);
+    const int at = static_cast<int>(k - static_cast<int64_t>(row) * across) * 1024 + threadIdx.x * 4;
+    if (at >= r.hidden) continue;
+    const float* from = partial + static_cast<int64_t>(row) * r.width + at;
+    float4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int i = 0; i < splits; ++i) {  // width is a multiple of 4
+      const float4 v = *reinterpret_cast<const float4*>(from + i * stride);
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+    uint16_t* to = r.dx + r.index[row] * r.dx_stride + at;
+    const uint16_t o[4] = {T::encode(s.x * c), T::encode(s.y * c), T::encode(s.z * c),
+                           T::encode(s.w * c)};
+    if (at + 4 <= r.hidden) {
+      __builtin_memcpy(to, o, 8);
+    } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] += v[i];
-      }
-      Vector<Bf16> o;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o.e[i] = T::encode(s[i] * c);
-      store_vector<Bf16>(to, at, r.hidden, o);
+      for (int i = 0; i < 4; ++i)
+        if (at + i < r.hidden) to[i] = o[i];
     }
   }
 }
@@ -250,6 +318,8 @@ hipError_t launch(void (*kernel)(P...), int64_t grid, int threads, hipStream_t s
 }  // namespace
 
 hipError_t launch_loss_gather(const LossRows& r, hipStream_t stream, int64_t max_grid) {
+  if (r.tokens <= kCountedTokens)
+    return launch(index_gather_kernel, r.tokens + kLossDepth, 256, stream, max_grid, r);
   const hipError_t e = launch(index_kernel, 1, 1024, stream, max_grid, r);
   if (e != hipSuccess) return e;
   const int64_t rows = (static_cast<int64_t>(r.tokens) + kLossDepth - 1) / kLossDepth * kLossDepth;
@@ -262,9 +332,14 @@ hipError_t launch_pack(const uint16_t* from, int64_t stride, int64_t rows, int c
 }
 
 hipError_t launch_loss_lse(const LossRows& r, hipStream_t stream, int64_t max_grid) {
-  // few rows: a workgroup to each
-  if (r.tokens <= 64) return launch(lse_kernel<1>, r.tokens, 1024, stream, max_grid, r);
-  return launch(lse_kernel<16>, (r.tokens + 15) / 16, 1024, stream, max_grid, r);
+  // one workgroup where it is enough, a workgroup to each of few rows, then 16 rows to one
+  if (r.tokens <= 1) return launch(lse_kernel<1>, 1, 1024, stream, max_grid, r);
+  if (r.tokens <= 16) return launch(lse_kernel<16>, 1, 1024, stream, max_grid, r);
+  const hipError_t e =
+      r.tokens <= 256 ? launch(lse_kernel<1>, r.tokens, 1024, stream, max_grid, r)
+                      : launch(lse_kernel<16>, (r.tokens + 15) / 16, 1024, stream, max_grid, r);
+  if (e != hipSuccess) return e;
+  return launch(sum_kernel, 1, 1024, stream, max_grid, r);
 }
 
 hipError_t launch_loss_softmax(const LossRows& r, const LossPiece& piece, hipStream_t stream,
@@ -276,14 +351,11 @@ hipError_t launch_loss_softmax(const LossRows& r, const LossPiece& piece, hipStr
                 max_grid, r, piece);
 }
 
-hipError_t launch_loss_sum(const LossRows& r, hipStream_t stream) {
-  return launch(sum_kernel, 1, 1024, stream, 1, r);
-}
-
 hipError_t launch_loss_input(const LossRows& r, const float* partial, int splits,
                              hipStream_t stream, int64_t max_grid) {
-  return launch(r.bf16 ? input_kernel<ScaledBf16> : input_kernel<ScaledFp16>, r.tokens, 256,
-                stream, max_grid, r, partial, splits);
+  return launch(r.bf16 ? input_kernel<ScaledBf16> : input_kernel<ScaledFp16>,
+                r.tokens * ((static_cast<int64_t>(r.width) + 1023) / 1024), 256, stream, max_grid,
+                r, partial, splits);
 }
 
 }  // namespace la

@@ -32,6 +32,7 @@ struct Plan {
   int64_t chunks;
   int64_t columns, pieces;    // of a piece; 0 without gradients
   int64_t splits;
+  bool large_input;
   // places in the workspace
   int64_t count, index, target, xc, wc, sums, target_logit, lse, losses, piece, partial;
   int64_t bytes;
@@ -87,7 +88,13 @@ void lay_out(const la_cross_entropy_desc& d, int64_t pieces, Plan* p) {
   p->chunks = (d.vocab + (int64_t(1) << shift) - 1) >> shift;
   p->columns = p->gradients ? round_up((d.vocab + pieces - 1) / pieces, la::kPieceUnit) : 0;
   p->pieces = p->gradients ? (d.vocab + p->columns - 1) / p->columns : 0;
-  p->splits = d.dx != nullptr ? la::loss_splits(d.tokens, d.hidden, p->columns) : 0;
+  p->splits = 0;
+  p->large_input = false;
+  if (d.dx != nullptr) {
+    const la::LossSplits splits = la::loss_splits(d.tokens, d.hidden, p->columns);
+    p->splits = splits.parts;
+    p->large_input = splits.large;
+  }
   la::Taker take;
   p->count = take(4);
   p->index = take(4 * d.tokens);
@@ -192,6 +199,7 @@ la_status cross_entropy(const la_cross_entropy_desc* d, void* ws, int64_t ws_byt
   a.ldw = d->vocab > 1 ? d->weight_row_stride : d->hidden;
   a.partial = place<float>(ws, p.partial);
   a.splits = static_cast<int32_t>(p.splits);
+  a.large_input = p.large_input;
   a.dw = static_cast<uint16_t*>(d->dweight);
   a.dw_stride = d->vocab > 1 ? d->dweight_row_stride : 0;
   a.dw_vectors = aligned(d->dweight, 16) && a.dw_stride % 8 == 0;
@@ -218,7 +226,6 @@ la_status cross_entropy(const la_cross_entropy_desc* d, void* ws, int64_t ws_byt
   if (!p.gradients) {
     if ((e = product(LossProduct::kSums, 0, d->vocab)) != hipSuccess) return launch_failed(e);
     if ((e = la::launch_loss_lse(r, stream, max_grid)) != hipSuccess) return launch_failed(e);
-    if ((e = la::launch_loss_sum(r, stream)) != hipSuccess) return launch_failed(e);
     return ok();
   }
   if (p.pieces > 1 &&
@@ -228,7 +235,6 @@ la_status cross_entropy(const la_cross_entropy_desc* d, void* ws, int64_t ws_byt
   if ((e = la::launch_loss_lse(r, stream, max_grid)) != hipSuccess) return launch_failed(e);
   e = la::launch_loss_softmax(r, a.piece, stream, max_grid);
   if (e != hipSuccess) return launch_failed(e);
-  if ((e = la::launch_loss_sum(r, stream)) != hipSuccess) return launch_failed(e);
   for (int64_t k = 0; k < p.pieces; ++k) {
     const int64_t first = k * p.columns;
     if (k > 0 && (e = product(LossProduct::kAgain, first, p.columns)) != hipSuccess)

@@ -101,7 +101,7 @@ struct LossTile {
   static constexpr bool halves = BUFFERS == 5;
   static constexpr int elements = halves ? 5 * rows * kLossDepth : BUFFERS * stage;
   static constexpr int p_copies = rows / (8 * waves), q_copies = cols / (8 * waves);
-  static constexpr int in_flight = (BUFFERS - 2) * (p_copies + q_copies);
+  static constexpr int in_flight = BUFFERS > 2 ? (BUFFERS - 2) * (p_copies + q_copies) : 0;
   // the epilogue's part of LDS: blocks of 32 rows that a wave exchanges at once
   static constexpr int lds = elements * 2;
   static constexpr int at_once =
@@ -217,24 +217,38 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void loss_product_kernel(LossProdu
         qo[c] = min(row, N - 1 - col0) * ldq * 2 + piece * 16;
       }
     }
+    // Where the stages' first rows lie: copies go stage by stage, and past the end
+    // the last stage is copied again, into places that nobody reads.
+    struct {
+      const uint16_t* at;
+      int left;  // stages behind this one
+    } ap = {p_first, stages - 1}, aq = {q_first, stages - 1};
     const int64_t p_step = PT ? static_cast<int64_t>(kLossDepth) * ldp : kLossDepth;
     const int64_t q_step = QT ? static_cast<int64_t>(kLossDepth) * ldq : kLossDepth;
-    // copies [from, to) of an operand's part of stage k
-    auto copy_p = [&](int k, uint16_t* to, int from, int end) {
+    auto advance_p = [&] {
+      ap.at += ap.left > 0 ? p_step : 0;
+      --ap.left;
+    };
+    auto advance_q = [&] {
+      aq.at += aq.left > 0 ? q_step : 0;
+      aq.left -= aq.left > 0 ? 1 : 0;
+    };
+    // copies [from, to) of an operand's part of the stage ahead
+    auto copy_p = [&](uint16_t* to, int from, int end) {
       const __amdgpu_buffer_rsrc_t rp = __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<uint16_t*>(p_first + k * p_step), 0, kRsrcRange, kRsrcWord3);
+          const_cast<uint16_t*>(ap.at), 0, kRsrcRange, kRsrcWord3);
 #pragma unroll
       for (int c = from; c < end; ++c)
         copy_to_lds(rp, to + (c * G::waves + wave) * 512, po[c], 0);
     };
-    auto copy_q = [&](int k, uint16_t* to, int from, int end) {
+    auto copy_q = [&](uint16_t* to, int from, int end) {
       const __amdgpu_buffer_rsrc_t rq = __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<uint16_t*>(q_first + k * q_step), 0, kRsrcRange, kRsrcWord3);
+          const_cast<uint16_t*>(aq.at), 0, kRsrcRange, kRsrcWord3);
       // the last row of w that there is, from the stage's first
       int last = kRsrcRange;
       if constexpr (INPUT) {
-        const int64_t rows = r.vocab - 1 - a.piece.first - k0 - static_cast<int64_t>(k) * kLossDepth;
-        if (rows < kLossDepth) last = static_cast<int>(rows) * ldq * 2;
+        const int rows = r.vocab - 1 - a.piece.first - k0 - (stages - 1 - aq.left) * kLossDepth;
+        if (rows < kLossDepth) last = rows * ldq * 2;
       }
 #pragma unroll
       for (int c = from; c < end; ++c)
@@ -298,56 +312,80 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void loss_product_kernel(LossProdu
       // P_0 and so on: part i lies at i % 5. Behind the meeting after stage k's
       // last reads its places take Q of stage k + 2, at once, and P of stage k + 3,
       // which has a whole stage more to arrive: the meeting waits for older copies
-      // only. The loop has no branch that would part the products: past the end the
-      // last stage is copied again, into places that nobody reads.
+      // only. The loop has no branch that would part the products.
       if (stages > 0) {
-        auto stage = [&](int k) { return k < stages ? k : stages - 1; };
         constexpr int half = G::rows * kLossDepth;
-        copy_p(0, lds, 0, G::p_copies);
-        copy_q(0, lds + half, 0, G::q_copies);
-        copy_p(stage(1), lds + 2 * half, 0, G::p_copies);
-        copy_q(stage(1), lds + 3 * half, 0, G::q_copies);
+        copy_p(lds, 0, G::p_copies);
+        copy_q(lds + half, 0, G::q_copies);
+        advance_p();
+        advance_q();
+        copy_p(lds + 2 * half, 0, G::p_copies);
+        copy_q(lds + 3 * half, 0, G::q_copies);
+        advance_p();
         wait_and_meet<G::p_copies + G::q_copies>();
         read(f[0], lds, lds + half, 0);
         using Qcopies = std::integral_constant<int, G::q_copies>;
         using Phalf = std::integral_constant<int, G::p_copies / 2>;
         int at = 0;  // place of P_k
+        auto place = [&](int i) { return lds + (at + i < 5 ? at + i : at + i - 5) * half; };
+        uint16_t *p = place(0), *q = place(1), *later = place(4);
         for (int k = 0; k < stages; ++k) {
-          auto place = [&](int i) { return lds + (at + i < 5 ? at + i : at + i - 5) * half; };
-          uint16_t *p = place(0), *q = place(1), *later = place(4);
+          // scalar work lies where products cover it, not at the stage's ends
           read(f[1], p, q, 1);
-          copy_p(stage(k + 2), later, 0, G::p_copies / 2);
+          copy_p(later, 0, G::p_copies / 2);
+          advance_q();
           multiply(f[0]);
           interleave(Phalf());
           read(f[0], p, q, 2);
-          copy_p(stage(k + 2), later, G::p_copies / 2, G::p_copies);
+          copy_p(later, G::p_copies / 2, G::p_copies);
+          advance_p();
           multiply(f[1]);
           interleave(Phalf());
           read(f[1], p, q, 3);
+          uint16_t* const done = p;
+          at = at + 2 < 5 ? at + 2 : at - 3;
+          p = place(0);
+          q = place(1);
+          later = place(4);
           multiply(f[0]);
           interleave(None());
           wait_and_meet<G::p_copies>();
-          read(f[0], place(2), place(3), 0);
-          copy_q(stage(k + 2), p, 0, G::q_copies);
+          read(f[0], p, q, 0);
+          copy_q(done, 0, G::q_copies);
           multiply(f[1]);
           interleave(Qcopies());
-          at = at + 2 < 5 ? at + 2 : at - 3;
         }
       }
       wait_and_meet<0>();
     } else {
-      auto copy = [&](int k, int buffer) {
+      auto copy = [&](int buffer) {
         uint16_t* to = lds + buffer * G::stage;
-        copy_p(k, to, 0, G::p_copies);
-        copy_q(k, to + G::rows * kLossDepth, 0, G::q_copies);
+        copy_p(to, 0, G::p_copies);
+        copy_q(to + G::rows * kLossDepth, 0, G::q_copies);
+        advance_p();
+        advance_q();
       };
       auto part = [&](Fragments& to, int buffer, int step) {
         const uint16_t* from = lds + buffer * G::stage;
         read(to, from, from + G::rows * kLossDepth, step);
       };
+      if constexpr (BUFFERS == 1) {  // a stage or two: several workgroups a compute unit instead
+        for (int k = 0; k < stages; ++k) {
+          copy(0);
+          wait_and_meet<0>();
+          part(f[0], 0, 0);
+#pragma unroll
+          for (int step = 1; step < kLossDepth / 16; ++step) {
+            part(f[step & 1], 0, step);
+            multiply(f[(step - 1) & 1]);
+          }
+          multiply(f[1]);
+          wait_and_meet<0>();
+        }
+      } else {
 #pragma unroll
       for (int k = 0; k < BUFFERS - 1; ++k)
-        if (k < stages) copy(k, k);
+        if (k < stages) copy(k);
       if (stages >= BUFFERS - 1) wait_and_meet<G::in_flight>();
       else wait_and_meet<0>();
       if (stages > 0) part(f[0], 0, 0);
@@ -356,7 +394,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void loss_product_kernel(LossProdu
         const int next = buffer + 1 == BUFFERS ? 0 : buffer + 1;
         const int last = buffer == 0 ? BUFFERS - 1 : buffer - 1;
         const bool more = k + BUFFERS - 1 < stages;
-        if (more) copy(k + BUFFERS - 1, last);
+        if (more) copy(last);
 #pragma unroll
         for (int step = 1; step < kLossDepth / 16; ++step) {
           part(f[step & 1], buffer, step);
@@ -368,6 +406,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void loss_product_kernel(LossProdu
         if (k + 1 < stages) part(f[0], next, 0);
         multiply(f[1]);
         buffer = next;
+      }
       }
     }
     // Every wave is past its last read of LDS, and no copy is under way.
@@ -559,19 +598,31 @@ hipError_t launch_tile(const LossProductArgs& a, hipStream_t stream, int64_t max
 
 // Whether a product of m x n, taken `times` over, goes in 256 x 256 tiles: one
 // takes 5/3 of the time of one of 128 x 128, on 256 compute units.
-bool large_tiles(int64_t m, int64_t n, int64_t times) {
-  auto rounds = [&](int64_t side) {
-    return (((m + side - 1) / side) * ((n + side - 1) / side) * times + 255) / 256;
-  };
-  return 5 * rounds(256) < 3 * rounds(128);
+int64_t rounds(int64_t m, int64_t n, int64_t side, int64_t times) {
+  return (((m + side - 1) / side) * ((n + side - 1) / side) * times + 255) / 256;
 }
+bool large_tiles(int64_t m, int64_t n) {
+  return 5 * rounds(m, n, 256, 1) < 3 * rounds(m, n, 128, 1);
+}
+
+// Up to this many tokens the weight's traffic decides: tiles of 32 or 64 rows
+// by 128 columns, two workgroups a compute unit.
+constexpr int kFewTokens = 64, kFewestTokens = 32;
 
 template <typename T, LossProduct WHAT>
 hipError_t launch_one(const LossProductArgs& a, hipStream_t stream, int64_t max_grid) {
-  constexpr bool INPUT = WHAT == LossProduct::kInput, WEIGHT = WHAT == LossProduct::kWeight;
-  const bool large = INPUT    ? large_tiles(a.r.tokens, a.r.hidden, a.splits)
-                     : WEIGHT ? large_tiles(a.piece.cols, a.r.hidden, 1)
-                              : a.r.chunk_shift == 7;
+  if constexpr (WHAT == LossProduct::kWeight) {
+    if (a.r.tokens <= 2 * kLossDepth)
+      return launch_tile<T, WHAT, 2, 2, 2, 2, 1>(a, stream, max_grid);
+  } else {
+    if (a.r.tokens <= kFewestTokens)
+      return launch_tile<T, WHAT, 1, 2, 1, 2, 4>(a, stream, max_grid);
+    if (a.r.tokens <= kFewTokens)
+      return launch_tile<T, WHAT, 1, 2, 2, 2, 3>(a, stream, max_grid);
+  }
+  const bool large = WHAT == LossProduct::kInput    ? a.large_input != 0
+                     : WHAT == LossProduct::kWeight ? large_tiles(a.piece.cols, a.r.hidden)
+                                                    : a.r.chunk_shift == 7;
   return large ? launch_tile<T, WHAT, 4, 4, 2, 2, 5>(a, stream, max_grid)
                : launch_tile<T, WHAT, 2, 2, 2, 2, 4>(a, stream, max_grid);
 }
@@ -591,23 +642,31 @@ hipError_t launch_type(const LossProductArgs& a, LossProduct what, hipStream_t s
 }  // namespace
 
 int loss_chunk_shift(int64_t tokens, int64_t vocab) {
-  return large_tiles(tokens, vocab, 1) ? 7 : 6;
+  return tokens > kFewTokens && large_tiles(tokens, vocab) ? 7 : 6;
 }
 
-int loss_splits(int64_t tokens, int64_t hidden, int64_t columns) {
-  // as many parts as fill the last round of tiles best, of at least 2048 columns
-  const int64_t tiles = std::max<int64_t>(1, (tokens + 255) / 256) * ((hidden + 255) / 256);
-  int64_t best = 1;
-  double best_fill = 0.0;
-  for (int64_t s = 1; s <= 32 && (s == 1 || columns / s >= 2048); ++s) {
-    const int64_t work = tiles * s, rounds = (work + 255) / 256;
-    const double fill = static_cast<double>(work) / static_cast<double>(rounds * 256);
-    if (fill > best_fill + 0.02) {
-      best_fill = fill;
-      best = s;
-    }
+// Parts that fill the last round of tiles, of at least 1024 columns; each one
+// more costs its binary32 results written and read, 8 bytes to 2 flops a column
+// at some 250 flops a byte.
+LossSplits loss_splits(int64_t tokens, int64_t hidden, int64_t columns) {
+  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(64, columns / 1024));
+  if (tokens <= kFewTokens) {
+    const int64_t tiles = (hidden + 127) / 128;
+    return {static_cast<int>(std::min(most, std::max<int64_t>(1, 512 / tiles))), false};
   }
-  return static_cast<int>(best);
+  LossSplits best = {1, false};
+  double least = 0.0;
+  for (int large = 0; large < 2; ++large)
+    for (int64_t k = 1; k <= most; ++k) {
+      const double time = static_cast<double>(rounds(tokens, hidden, large ? 256 : 128, k)) *
+                          (large ? 5.0 : 3.0) / static_cast<double>(k) *
+                          (1.0 + 1000.0 * static_cast<double>(k) / static_cast<double>(columns));
+      if (least == 0.0 || time < 0.99 * least) {
+        least = time;
+        best = {static_cast<int>(k), large != 0};
+      }
+    }
+  return best;
 }
 
 hipError_t launch_loss_product(const LossProductArgs& a, LossProduct what, hipStream_t stream,
