@@ -99,7 +99,7 @@ struct LossProductArgs {
 };
 
 // log2 of a chunk's columns in the tile that a call of this size takes.
-int loss_chunk_shift(int64_t tokens, int64_t vocab);
+int loss_chunk_shift(int64_t tokens, int64_t hidden, int64_t vocab);
 
 hipError_t launch_loss_gather(const LossRows& r, hipStream_t stream, int64_t max_grid);
 hipError_t launch_pack(const uint16_t* from, int64_t stride, int64_t rows, int cols, uint16_t* to,

@@ -127,13 +127,31 @@ __global__ __launch_bounds__(256) void index_gather_kernel(LossRows r) {
   }
 }
 
-// A copy of rows whose length or alignment the products cannot read: zeros up
-// to width.
+// A copy of rows whose length or alignment the products cannot read, zeros
+// behind each; four pieces a thread, so that its loads overlap.
+constexpr int kPackPieces = 4;
+
 __global__ __launch_bounds__(256) void pack_kernel(const uint16_t* from, int64_t stride,
-                                                   int64_t rows, int cols, uint16_t* to, int width) {
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x)
-    for (int at = threadIdx.x * 8; at < width; at += 2048)
-      store_vector<Bf16>(to + row * width, at, width, load_vector<Bf16>(from + row * stride, at, cols));
+                                                   int64_t rows, int cols, uint16_t* to,
+                                                   int width) {
+  const int pieces = width / 8;
+  const int64_t total = rows * pieces, span = 256 * kPackPieces;
+  for (int64_t first = blockIdx.x * span; first < total; first += gridDim.x * span) {
+    Vector<Bf16> v[kPackPieces];
+#pragma unroll
+    for (int i = 0; i < kPackPieces; ++i) {
+      const int64_t k = first + i * 256 + threadIdx.x;
+      if (k >= total) continue;
+      const int64_t row =
+          k <= 0xffffffffll ? static_cast<uint32_t>(k) / static_cast<uint32_t>(pieces) : k / pieces;
+      v[i] = load_vector<Bf16>(from + row * stride, static_cast<int>(k - row * pieces) * 8, cols);
+    }
+#pragma unroll
+    for (int i = 0; i < kPackPieces; ++i) {
+      const int64_t k = first + i * 256 + threadIdx.x;
+      if (k < total) __builtin_memcpy(to + k * 8, &v[i], 16);
+    }
+  }
 }
 
 // The types of g, and their scale.
@@ -328,7 +346,8 @@ hipError_t launch_loss_gather(const LossRows& r, hipStream_t stream, int64_t max
 
 hipError_t launch_pack(const uint16_t* from, int64_t stride, int64_t rows, int cols, uint16_t* to,
                        int width, hipStream_t stream, int64_t max_grid) {
-  return launch(pack_kernel, rows, 256, stream, max_grid, from, stride, rows, cols, to, width);
+  const int64_t span = 256 * kPackPieces;
+  return launch(pack_kernel, (rows * (width / 8) + span - 1) / span, 256, stream, max_grid, from, stride, rows, cols, to, width);
 }
 
 hipError_t launch_loss_lse(const LossRows& r, hipStream_t stream, int64_t max_grid) {

@@ -84,7 +84,7 @@ void lay_out(const la_cross_entropy_desc& d, int64_t pieces, Plan* p) {
   // aligned pieces, and a padded copy otherwise
   const int64_t ldw = d.vocab > 1 ? d.weight_row_stride : d.hidden;
   p->pack = p->width != d.hidden || ldw % 8 != 0 || ldw > LA_MAX_SIDE || !aligned(d.weight, 16);
-  const int shift = la::loss_chunk_shift(d.tokens, d.vocab);
+  const int shift = la::loss_chunk_shift(d.tokens, d.hidden, d.vocab);
   p->chunks = (d.vocab + (int64_t(1) << shift) - 1) >> shift;
   p->columns = p->gradients ? round_up((d.vocab + pieces - 1) / pieces, la::kPieceUnit) : 0;
   p->pieces = p->gradients ? (d.vocab + p->columns - 1) / p->columns : 0;
@@ -187,7 +187,7 @@ la_status cross_entropy(const la_cross_entropy_desc* d, void* ws, int64_t ws_byt
   r.width = static_cast<int32_t>(p.width);
   r.sums = place<float2>(ws, p.sums);
   r.chunks = static_cast<int32_t>(p.chunks);
-  r.chunk_shift = la::loss_chunk_shift(d->tokens, d->vocab);
+  r.chunk_shift = la::loss_chunk_shift(d->tokens, d->hidden, d->vocab);
   r.target_logit = place<float>(ws, p.target_logit);
   r.lse = place<float>(ws, p.lse);
   r.losses = d->losses;

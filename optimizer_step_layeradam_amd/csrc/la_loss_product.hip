@@ -154,7 +154,7 @@ __device__ __forceinline__ s16x8 fragment(const uint16_t* from, int first, int s
 }
 
 template <typename T, LossProduct WHAT, int MT, int NT, int WM, int WN, int BUFFERS>
-__global__ __launch_bounds__(64 * WM * WN, 1) void loss_product_kernel(LossProductArgs a) {
+__global__ __launch_bounds__(64 * WM * WN, BUFFERS == 1 ? 4 : BUFFERS == 2 ? 2 : 1) void loss_product_kernel(LossProductArgs a) {
   using G = LossTile<MT, NT, WM, WN, BUFFERS>;
   constexpr bool INPUT = WHAT == LossProduct::kInput, WEIGHT = WHAT == LossProduct::kWeight;
   constexpr bool PT = WEIGHT, QT = INPUT || WEIGHT;
@@ -252,7 +252,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void loss_product_kernel(LossProdu
       }
 #pragma unroll
       for (int c = from; c < end; ++c)
-        copy_to_lds(rq, to + (c * G::waves + wave) * 512,
+        copy_to_lds<MT == 1 ? kNonTemporal : 0>(rq, to + (c * G::waves + wave) * 512,
                     QT ? (INPUT ? min(qo[c], last) : qo[c]) + qc[QT ? c : 0] : qo[c], 0);
     };
     struct Fragments {
@@ -475,7 +475,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void loss_product_kernel(LossProdu
             if (row[u] >= M || col >= N) continue;
             uint16_t* to = a.dw + (a.piece.first + row[u]) * a.dw_stride + col;
             if (a.dw_vectors && col + 8 <= N) {
-              *reinterpret_cast<s16x8*>(to) = o;
+              __builtin_nontemporal_store(o, reinterpret_cast<s16x8*>(to));
             } else {
 #pragma unroll
               for (int e = 0; e < 8; ++e)
@@ -596,35 +596,48 @@ hipError_t launch_tile(const LossProductArgs& a, hipStream_t stream, int64_t max
       dim3(static_cast<unsigned>(grid)), dim3(G::threads), params, 0, stream);
 }
 
-// Whether a product of m x n, taken `times` over, goes in 256 x 256 tiles: one
-// takes 5/3 of the time of one of 128 x 128, on 256 compute units.
-int64_t rounds(int64_t m, int64_t n, int64_t side, int64_t times) {
-  return (((m + side - 1) / side) * ((n + side - 1) / side) * times + 255) / 256;
+// What `tiles` tiles of `stages` stages take, in us. Measured with 32768 words
+// (us, 256 x 256 tiles | 128 x 128): 4096 tokens' logits over hidden 512 212 |
+// 176, 1024 310 | 303, 4096 904 | 1082; 256 tokens' over 4096 101 | 95; the
+// weight's gradient at 4096 columns from 256 tokens 123 | 100, 1024 309 | 306,
+// 4096 845 | 1037, at 128 columns from 4096 tokens 88 | 95. The small tile has one
+// buffer alone, and four workgroups a compute unit that take turns (with two or
+// four buffers and fewer workgroups every one of these took as long or longer).
+double time_of(bool large, int64_t tiles, int64_t stages) {
+  const double s = static_cast<double>(stages);
+  const int64_t each = (tiles + 255) / 256;  // of a compute unit
+  if (large) return static_cast<double>(each) * (14.0 + 1.55 * s);
+  const int64_t rest = each % 4;
+  return static_cast<double>(each / 4) * (5.4 + 2.04 * s) +
+         (rest > 0 ? 2.5 + s * (1.2 + 0.21 * static_cast<double>(rest)) : 0.0);
 }
-bool large_tiles(int64_t m, int64_t n) {
-  return 5 * rounds(m, n, 256, 1) < 3 * rounds(m, n, 128, 1);
+
+bool large_tiles(int64_t m, int64_t n, int64_t depth) {
+  auto tiles = [&](int64_t side) { return ((m + side - 1) / side) * ((n + side - 1) / side); };
+  const int64_t stages = (depth + kLossDepth - 1) / kLossDepth;
+  return time_of(true, tiles(256), stages) < time_of(false, tiles(128), stages);
 }
 
 // Up to this many tokens the weight's traffic decides: tiles of 32 or 64 rows
-// by 128 columns, two workgroups a compute unit.
+// by 128 columns, two workgroups a compute unit, whose copies of the weight pass by
+// the caches (24 tokens x 4096 x 128000, 1.05 GB: logits 198 us, and 262 us through
+// them).
 constexpr int kFewTokens = 64, kFewestTokens = 32;
 
 template <typename T, LossProduct WHAT>
 hipError_t launch_one(const LossProductArgs& a, hipStream_t stream, int64_t max_grid) {
-  if constexpr (WHAT == LossProduct::kWeight) {
-    if (a.r.tokens <= 2 * kLossDepth)
-      return launch_tile<T, WHAT, 2, 2, 2, 2, 1>(a, stream, max_grid);
-  } else {
+  if constexpr (WHAT != LossProduct::kWeight) {
     if (a.r.tokens <= kFewestTokens)
       return launch_tile<T, WHAT, 1, 2, 1, 2, 4>(a, stream, max_grid);
     if (a.r.tokens <= kFewTokens)
       return launch_tile<T, WHAT, 1, 2, 2, 2, 3>(a, stream, max_grid);
   }
-  const bool large = WHAT == LossProduct::kInput    ? a.large_input != 0
-                     : WHAT == LossProduct::kWeight ? large_tiles(a.piece.cols, a.r.hidden)
-                                                    : a.r.chunk_shift == 7;
+  const bool large = WHAT == LossProduct::kInput ? a.large_input != 0
+                     : WHAT == LossProduct::kWeight
+                         ? large_tiles(a.piece.cols, a.r.hidden, a.r.tokens)
+                         : a.r.chunk_shift == 7;
   return large ? launch_tile<T, WHAT, 4, 4, 2, 2, 5>(a, stream, max_grid)
-               : launch_tile<T, WHAT, 2, 2, 2, 2, 4>(a, stream, max_grid);
+               : launch_tile<T, WHAT, 2, 2, 2, 2, 1>(a, stream, max_grid);
 }
 
 template <typename T>
@@ -641,14 +654,12 @@ hipError_t launch_type(const LossProductArgs& a, LossProduct what, hipStream_t s
 
 }  // namespace
 
-int loss_chunk_shift(int64_t tokens, int64_t vocab) {
-  return tokens > kFewTokens && large_tiles(tokens, vocab) ? 7 : 6;
+int loss_chunk_shift(int64_t tokens, int64_t hidden, int64_t vocab) {
+  return tokens > kFewTokens && large_tiles(tokens, vocab, hidden) ? 7 : 6;
 }
 
-// Parts that fill the last round of tiles, of at least 1024 columns; each one
-// more costs its binary32 results written and read, 8 bytes to 2 flops a column
-// at some 250 flops a byte.
 LossSplits loss_splits(int64_t tokens, int64_t hidden, int64_t columns) {
+  // parts of at least 1024 columns
   const int64_t most = std::max<int64_t>(1, std::min<int64_t>(64, columns / 1024));
   if (tokens <= kFewTokens) {
     const int64_t tiles = (hidden + 127) / 128;
@@ -658,9 +669,11 @@ LossSplits loss_splits(int64_t tokens, int64_t hidden, int64_t columns) {
   double least = 0.0;
   for (int large = 0; large < 2; ++large)
     for (int64_t k = 1; k <= most; ++k) {
-      const double time = static_cast<double>(rounds(tokens, hidden, large ? 256 : 128, k)) *
-                          (large ? 5.0 : 3.0) / static_cast<double>(k) *
-                          (1.0 + 1000.0 * static_cast<double>(k) / static_cast<double>(columns));
+      const int64_t side = large ? 256 : 128;
+      const int64_t tiles = ((tokens + side - 1) / side) * ((hidden + side - 1) / side) * k;
+      // a part's binary32 results are written and read, at 5 TB/s
+      const double time = time_of(large, tiles, (columns / k + kLossDepth - 1) / kLossDepth) +
+                          static_cast<double>(k * tokens * hidden) * 8.0 / 5e6;
       if (least == 0.0 || time < 0.99 * least) {
         least = time;
         best = {static_cast<int>(k), large != 0};

@@ -15,10 +15,14 @@ constexpr int kRsrcWord3 = 0x00020000;
 
 // 16 bytes per lane from memory to 1 KiB of LDS at `to` (lane order), without
 // a register between; done when the wave's vmcnt says so.
+// CACHE: 0, or kNonTemporal for what is read once.
+constexpr int kNonTemporal = 2;
+
+template <int CACHE = 0>
 __device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t from, void* to, int offset,
                                             int uniform_offset) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(
-      from, (__attribute__((address_space(3))) void*)to, 16, offset, uniform_offset, 0, 0);
+      from, (__attribute__((address_space(3))) void*)to, 16, offset, uniform_offset, 0, CACHE);
 }
 
 // All but the last PENDING of this wave's copies have landed and its reads of
