@@ -2,8 +2,8 @@
 
     python -m optimizer_step_layeradam_amd.build
 
-Compiles csrc/*.hip and csrc/*.cpp with hipcc for gfx950 into
-optimizer_step_layeradam_amd/liblayeradam.so. Always recompiles.
+Compiles csrc/*.hip and csrc/*.cpp with hipcc for gfx950, side by side, and
+links them into optimizer_step_layeradam_amd/liblayeradam.so. Always recompiles.
 """
 from __future__ import annotations
 
@@ -11,6 +11,8 @@ import glob
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -44,11 +46,22 @@ def sources():
 
 
 def build(verbose: bool = False, out: str = LIB_PATH, extra=()) -> str:
-    cmd = [hipcc(), *HIPCC_FLAGS, *extra, "-I", os.path.join(ROOT, "include"),
-           "-I", os.path.join(HERE, "csrc"), "-o", out + ".tmp", *sources()]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+
+    flags = [*HIPCC_FLAGS, *extra]
+    with tempfile.TemporaryDirectory() as d:
+        def compiled(source):
+            obj = os.path.join(d, os.path.basename(source) + ".o")
+            run([hipcc(), *[f for f in flags if f != "-shared"], "-c", "-I",
+                 os.path.join(ROOT, "include"), "-I", os.path.join(HERE, "csrc"), "-o", obj, source])
+            return obj
+
+        with ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+            objects = list(pool.map(compiled, sources()))
+        run([hipcc(), *flags, "-o", out + ".tmp", *objects])
     os.replace(out + ".tmp", out)
     return out
 

@@ -13,7 +13,7 @@
 // nothing of it (a NaN, say) can reach a sum. The vocabulary is taken in
 // pieces, and one piece of a T x V matrix is held at a time:
 //
-//   logits of the first piece -> e = exp(z - max of some columns), with the
+//   logits of the first piece -> e = exp(z - max of some columns) with the
 //       maxima and the sums beside them            product, kKeep
 //   logits of the other pieces -> their maxima and sums alone        kSums
 //   lse and losses from those; e -> g in place                       softmax
@@ -42,7 +42,13 @@ constexpr int kPieceUnit = 256;
 constexpr int kLossDepth = 64;
 
 // Scale of e, and of g in binary16.
-constexpr float kLossScale = 16384.0f;
+constexpr float kLossExponent = 14.0f, kLossScale = 16384.0f;
+
+// Exponentials are powers of two: of z log2 e, which one multiply-add forms to
+// the last bit or so of z. log2 e itself is 1.3e-8 off in binary32, a fifth of
+// what rounding z costs.
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr double kLn2 = 0.693147180559945309;
 
 // What the passes over tokens need.
 struct LossRows {
@@ -61,11 +67,11 @@ struct LossRows {
   int32_t* target;          // their targets, -1 where out of range
   uint16_t* xc;             // gathered, rows x width, zeros behind hidden
   int32_t width;            // hidden, up to whole depths
-  float2* sums;             // chunks x tokens: maximum and sum of exp(z - maximum)
+  float2* sums;             // chunks x tokens: maximum m of z log2 e, sum of e = 2^(z log2 e - m + 14)
   int32_t chunks;           // of vocab columns
   int32_t chunk_shift;      // log2 of a chunk's columns
   float* target_logit;
-  float* lse;
+  float* lse;               // times log2 e
   // outputs
   float* losses;            // per token, or null
   float* compact_losses;    // workspace
@@ -95,7 +101,6 @@ struct LossProductArgs {
   int32_t add;              // kInput: to what is there
   uint16_t* dw;             // kWeight
   int64_t dw_stride;
-  int32_t dw_vectors;       // kWeight: every 8 elements of a row are 16-byte aligned
 };
 
 // log2 of a chunk's columns in the tile that a call of this size takes.

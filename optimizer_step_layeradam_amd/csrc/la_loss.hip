@@ -15,8 +15,6 @@
 namespace la {
 namespace {
 
-constexpr float kLog2e = 1.44269504088896341f;
-
 __device__ __forceinline__ int64_t target_of(const LossRows& r, int t) {
   return r.wide_targets ? static_cast<const int64_t*>(r.targets)[t]
                         : static_cast<const int32_t*>(r.targets)[t];
@@ -195,8 +193,8 @@ __global__ __launch_bounds__(1024) void lse_kernel(LossRows r) {
       const float top = __builtin_fmaxf(most, x.x);
       // nothing so far, or nothing here: exp(-inf - top) is 0, unless top is too
       const float point = top == -__builtin_inff() ? 0.0f : top;
-      sum = sum * __builtin_amdgcn_exp2f((most - point) * kLog2e) +
-            x.y * __builtin_amdgcn_exp2f((x.x - point) * kLog2e);
+      sum = sum * __builtin_amdgcn_exp2f(most - point) +
+            x.y * __builtin_amdgcn_exp2f(x.x - point);
       most = top;
     };
     const float2* sums = r.sums + row;
@@ -221,9 +219,13 @@ __global__ __launch_bounds__(1024) void lse_kernel(LossRows r) {
     if (share == 0 && first + lane < n) {
       // a target outside the vocabulary makes all of its token's results NaN
       const bool outside = r.target[row] < 0;
-      const float log_sum = __builtin_logf(sum), nan = __builtin_nanf("");
-      const float loss = outside ? nan : (most - r.target_logit[row]) + log_sum;
-      r.lse[row] = outside ? nan : most + log_sum;
+      const float nan = __builtin_nanf("");
+      // in binary64, since these are large beside a small loss
+      const double log_sum = log(static_cast<double>(sum)) - kLossExponent * kLn2;
+      const double lse = static_cast<double>(most) * kLn2 + log_sum;
+      const float loss =
+          outside ? nan : static_cast<float>(lse - static_cast<double>(r.target_logit[row]));
+      r.lse[row] = outside ? nan : static_cast<float>(lse / kLn2);
       r.compact_losses[row] = own[lane] = loss;
       if (r.losses != nullptr) r.losses[r.index[row]] = loss;
     }
@@ -249,43 +251,66 @@ __global__ __launch_bounds__(1024) void sum_kernel(LossRows r) {
     *r.loss = static_cast<float>(r.mean && n > 1 ? s / static_cast<double>(n) : s);
 }
 
-// e of the held piece becomes g, in place: 16 rows of 2048 columns a workgroup.
+// e of the held piece becomes g, in place: 16 rows of 2048 columns a workgroup,
+// whose factors are formed once, in LDS. Eight rows of a thread are asked for before
+// the first is needed.
 constexpr int kSoftmaxRows = 16, kSoftmaxCols = 2048;
 
 template <typename T>
 __global__ __launch_bounds__(256) void softmax_kernel(LossRows r, LossPiece piece) {
   constexpr float scale = T::encode_scale;
+  constexpr int BATCH = 8;
+  __shared__ float factors[kSoftmaxCols / 64][kSoftmaxRows];
+  __shared__ int targets[kSoftmaxRows];
+  __shared__ uint16_t at_target[kSoftmaxRows];
   const int n = *r.count;
   const int padded = (n + kLossDepth - 1) / kLossDepth * kLossDepth;
   const int width = (piece.cols + kLossDepth - 1) / kLossDepth * kLossDepth;
   const int across = (width + kSoftmaxCols - 1) / kSoftmaxCols;
-  const int64_t total = static_cast<int64_t>((padded + kSoftmaxRows - 1) / kSoftmaxRows) * across;
+  const int64_t total = static_cast<int64_t>(padded / kSoftmaxRows) * across;
   for (int64_t k = blockIdx.x; k < total; k += gridDim.x) {
     const int first = static_cast<int>(k / across) * kSoftmaxRows;
-    const int at = static_cast<int>(k % across) * kSoftmaxCols + threadIdx.x * 8;
+    const int col0 = static_cast<int>(k % across) * kSoftmaxCols;
+    const int at = col0 + threadIdx.x * 8;
+    __syncthreads();  // the last round's factors have been read
+    for (int i = threadIdx.x; i < (kSoftmaxCols >> r.chunk_shift) * kSoftmaxRows; i += 256) {
+      const int row = first + i % kSoftmaxRows, chunk = (col0 >> r.chunk_shift) + i / kSoftmaxRows;
+      if (row < n && chunk < r.chunks)
+        factors[i / kSoftmaxRows][i % kSoftmaxRows] =
+            __builtin_amdgcn_exp2f(r.sums[static_cast<int64_t>(chunk) * r.tokens + row].x -
+                                   r.lse[row]) *
+            (scale / kLossScale);
+    }
+    if (threadIdx.x < kSoftmaxRows) {
+      const int row = min(first + static_cast<int>(threadIdx.x), n - 1);
+      targets[threadIdx.x] = r.target[row] - piece.first;
+      // not 1 - p, whose difference loses what a well predicted token has
+      at_target[threadIdx.x] = T::encode(scale * expm1f(-r.compact_losses[row]));
+    }
+    __syncthreads();
     if (at >= width) continue;
-    const float2* sums = r.sums + static_cast<int64_t>(at >> r.chunk_shift) * r.tokens;
     uint16_t* g = piece.g + static_cast<int64_t>(first) * piece.ld + at;
-#pragma unroll 8
-    for (int i = 0; i < kSoftmaxRows; ++i) {
-      const int row = first + i;  // padded is a multiple of kSoftmaxRows
-      Vector<Bf16> o = {};        // rows behind the last one are read as zeros
-      if (row < n) {
-        Vector<Fp16> e;
-        __builtin_memcpy(&e, g + static_cast<int64_t>(i) * piece.ld, 16);
-        const float f = __builtin_amdgcn_exp2f((sums[row].x - r.lse[row]) * kLog2e) *
-                        (scale / kLossScale);
-        const int own = r.target[row] - piece.first - at;
+    const float* f = factors[(at - col0) >> r.chunk_shift];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o.e[j] = T::encode(Fp16::decode(e.e[j]) * f);
+    for (int i = 0; i < kSoftmaxRows; i += BATCH) {
+      Vector<Fp16> e[BATCH];
+#pragma unroll
+      for (int u = 0; u < BATCH; ++u)  // padded is a multiple of kSoftmaxRows
+        __builtin_memcpy(&e[u], g + static_cast<int64_t>(i + u) * piece.ld, 16);
+#pragma unroll
+      for (int u = 0; u < BATCH; ++u) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = Fp16::decode(e[u].e[j]) * f[i + u];
+        Vector<Bf16> o = __builtin_bit_cast(Vector<Bf16>, encode_vector<T>(v));
+        const int own = targets[i + u] - at;
         if (own >= 0 && own < 8) {
-          // not 1 - p, whose difference loses what a well predicted token has
-          const uint16_t t = T::encode(scale * expm1f(-r.compact_losses[row]));
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o.e[j] = own == j ? t : o.e[j];
+          for (int j = 0; j < 8; ++j) o.e[j] = own == j ? at_target[i + u] : o.e[j];
         }
+        if (first + i + u >= n) o = {};  // rows behind the last one are read as zeros
+        __builtin_memcpy(g + static_cast<int64_t>(i + u) * piece.ld, &o, 16);
       }
-      __builtin_memcpy(g + static_cast<int64_t>(i) * piece.ld, &o, 16);
     }
   }
 }

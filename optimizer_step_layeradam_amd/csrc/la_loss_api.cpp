@@ -202,7 +202,6 @@ la_status cross_entropy(const la_cross_entropy_desc* d, void* ws, int64_t ws_byt
   a.large_input = p.large_input;
   a.dw = static_cast<uint16_t*>(d->dweight);
   a.dw_stride = d->vocab > 1 ? d->dweight_row_stride : 0;
-  a.dw_vectors = aligned(d->dweight, 16) && a.dw_stride % 8 == 0;
 
   hipError_t e = la::launch_loss_gather(r, stream, max_grid);
   if (e != hipSuccess) return launch_failed(e);

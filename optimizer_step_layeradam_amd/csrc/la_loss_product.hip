@@ -21,10 +21,9 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef s16x8 s16x8_anywhere __attribute__((aligned(2)));
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-
-constexpr float kLog2e = 1.44269504088896341f;
 
 template <typename T>
 __device__ __forceinline__ f32x16 mfma(s16x8 p, s16x8 q, f32x16 c) {
@@ -57,6 +56,14 @@ __device__ __forceinline__ s16x8 rounded(const float (&v)[8]) {
 template <int CONTROL>
 __device__ __forceinline__ float moved(float x) {
   return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CONTROL, 0xF, 0xF, true));
+}
+
+// The largest of three, a NaN being none: one instruction, where the built-in
+// function first makes every NaN among its operands a quiet one.
+__device__ __forceinline__ float larger(float x, float y, float z) {
+  float m;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(m) : "v"(x), "v"(y), "v"(z));
+  return m;
 }
 
 template <int LANES, int SIDE, typename F>
@@ -264,17 +271,20 @@ __global__ __launch_bounds__(64 * WM * WN, BUFFERS == 1 ? 4 : BUFFERS == 2 ? 2 :
 #pragma unroll
       for (int j = 0; j < NT; ++j) f.q[j] = fragment<QT, G::cols>(q, wn + 32 * j, step, lane);
     };
-    // The targets and lse of the wave's rows, a lane to a row.
+    // What the wave's rows have, a lane to a row.
     struct {
       int target[MT > 2 ? 2 : 1];
-      float lse[MT > 2 ? 2 : 1];
+      float lse[MT > 2 ? 2 : 1], loss[MT > 2 ? 2 : 1];
     } mine = {};
     if constexpr (LOGITS) {
 #pragma unroll
       for (int i = 0; i < (MT > 2 ? 2 : 1); ++i) {
         const int row = min(row0 + wm + 64 * i + lane, M - 1);
         mine.target[i] = r.target[row];
-        if constexpr (WHAT == LossProduct::kAgain) mine.lse[i] = r.lse[row];
+        if constexpr (WHAT == LossProduct::kAgain) {
+          mine.lse[i] = r.lse[row];
+          mine.loss[i] = r.compact_losses[row];
+        }
       }
     }
     f32x16 acc[MT][NT] = {};
@@ -474,8 +484,8 @@ __global__ __launch_bounds__(64 * WM * WN, BUFFERS == 1 ? 4 : BUFFERS == 2 ? 2 :
             const s16x8 o = rounded<T>(v[u]);
             if (row[u] >= M || col >= N) continue;
             uint16_t* to = a.dw + (a.piece.first + row[u]) * a.dw_stride + col;
-            if (a.dw_vectors && col + 8 <= N) {
-              __builtin_nontemporal_store(o, reinterpret_cast<s16x8*>(to));
+            if (col + 8 <= N) {  // at any element; nothing here reads it again
+              __builtin_nontemporal_store(o, reinterpret_cast<s16x8_anywhere*>(to));
             } else {
 #pragma unroll
               for (int e = 0; e < 8; ++e)
@@ -484,7 +494,7 @@ __global__ __launch_bounds__(64 * WM * WN, BUFFERS == 1 ? 4 : BUFFERS == 2 ? 2 :
           }
         } else {
           int own[SIDE];      // the target's place among the lane's columns
-          float lse[SIDE];
+          float lse[SIDE], loss[SIDE];
 #pragma unroll
           for (int u = 0; u < SIDE; ++u) {
             // lanes hold what belongs to the wave's rows
@@ -497,9 +507,12 @@ __global__ __launch_bounds__(64 * WM * WN, BUFFERS == 1 ? 4 : BUFFERS == 2 ? 2 :
             own[u] -= a.piece.first + col;
             if constexpr (WHAT == LossProduct::kAgain) {
               lse[u] = __shfl(mine.lse[0], at & 63, 64);
+              loss[u] = __shfl(mine.loss[0], at & 63, 64);
               if constexpr (MT == 4) {
                 const float other = __shfl(mine.lse[1], at & 63, 64);
+                const float another = __shfl(mine.loss[1], at & 63, 64);
                 lse[u] = at < 64 ? lse[u] : other;
+                loss[u] = at < 64 ? loss[u] : another;
               }
             }
             if (edge) {  // columns behind the piece count as exp(-inf)
@@ -513,15 +526,10 @@ __global__ __launch_bounds__(64 * WM * WN, BUFFERS == 1 ? 4 : BUFFERS == 2 ? 2 :
             for (int u = 0; u < SIDE; ++u) {
               constexpr float scale = std::is_same<T, Bf16>::value ? 1.0f : kLossScale;
               float at_target = 0.0f;
-              if (own[u] >= 0 && own[u] < 8) {
-                float z = v[u][0];
-#pragma unroll
-                for (int e = 1; e < 8; ++e) z = own[u] == e ? v[u][e] : z;
-                at_target = scale * expm1f(z - lse[u]);
-              }
+              if (own[u] >= 0 && own[u] < 8) at_target = scale * expm1f(-loss[u]);
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                v[u][e] = scale * __builtin_amdgcn_exp2f((v[u][e] - lse[u]) * kLog2e);
+                v[u][e] = scale * __builtin_amdgcn_exp2f(__builtin_fmaf(v[u][e], kLog2e, -lse[u]));
                 v[u][e] = own[u] == e ? at_target : v[u][e];
               }
               if (row[u] < M && col < a.piece.ld)
@@ -538,19 +546,23 @@ __global__ __launch_bounds__(64 * WM * WN, BUFFERS == 1 ? 4 : BUFFERS == 2 ? 2 :
                 for (int e = 1; e < 8; ++e) z = own[u] == e ? v[u][e] : z;
                 r.target_logit[row[u]] = z;
               }
-              most[u] = v[u][0];
-#pragma unroll
-              for (int e = 1; e < 8; ++e) most[u] = __builtin_fmaxf(most[u], v[u][e]);
+              most[u] = larger(larger(v[u][0], v[u][1], v[u][2]),
+                               larger(v[u][3], v[u][4], v[u][5]),
+                               larger(v[u][6], v[u][7], v[u][7]));
             }
-            over_lanes<LANES, SIDE>(most, [](float x, float y) { return __builtin_fmaxf(x, y); });
+            over_lanes<LANES, SIDE>(most, [](float x, float y) { return larger(x, y, y); });
 #pragma unroll
             for (int u = 0; u < SIDE; ++u) {
-              // nothing in these columns: their exponentials are 0 from any point
-              const float from_here = most[u] == -__builtin_inff() ? 0.0f : most[u];
+              // From here on in powers of two, 14 above the maximum. Nothing in these
+              // columns: their exponentials are 0 from any point.
+              const float point = most[u] * kLog2e;
+              const bool none = point == -__builtin_inff();
+              const float from_here = (none ? 0.0f : point) - kLossExponent;
+              most[u] = none ? point : from_here + kLossExponent;  // exactly what was taken off
               sum[u] = 0.0f;
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                v[u][e] = __builtin_amdgcn_exp2f((v[u][e] - from_here) * kLog2e);
+                v[u][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(v[u][e], kLog2e, -from_here));
                 sum[u] += v[u][e];
               }
             }
@@ -561,8 +573,6 @@ __global__ __launch_bounds__(64 * WM * WN, BUFFERS == 1 ? 4 : BUFFERS == 2 ? 2 :
                 r.sums[static_cast<int64_t>(chunk) * r.tokens + row[u]] =
                     make_float2(most[u], sum[u]);
               if constexpr (WHAT == LossProduct::kKeep) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[u][e] *= kLossScale;
                 if (row[u] < M && col < a.piece.ld)
                   *reinterpret_cast<s16x8*>(a.piece.g + static_cast<int64_t>(row[u]) * a.piece.ld +
                                             col) = rounded<Fp16>(v[u]);

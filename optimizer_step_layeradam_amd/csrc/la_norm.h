@@ -24,9 +24,9 @@ struct NormArgs {
   float* partial;                            // backward: parts x (1 or 2) x cols
   float* coefficients;                       // backward of long rows: two per row
   void *dweight, *dbias;                     // null: not wanted
-  int64_t rows, inner;
-  int64_t parts;                             // backward: partial sums of the parameters' gradients
-  int64_t rows_per_part;
+  int32_t rows, inner;
+  int32_t parts;                             // backward: partial sums of the parameters' gradients
+  int32_t rows_per_part;
   int32_t cols;
   int32_t layer;                             // 1: layer norm, 0: RMS norm
   int32_t type, weight_type, grad_type;      // la_element_type
@@ -38,9 +38,14 @@ constexpr int kNormRegisterBytes = 32768;
 
 // The backward pass' parts: how many sums over rows are formed side by side,
 // and of how many rows each.
-void norm_parts(int64_t rows, int64_t cols, int type, int64_t* parts, int64_t* rows_per_part);
+void norm_parts(int64_t rows, int64_t cols, int type, int32_t* parts, int32_t* rows_per_part);
 
 hipError_t launch_norm_forward(const NormArgs& a, hipStream_t stream, int64_t max_grid);
+// The backward pass over rows that fit registers, by element type.
+hipError_t norm_backward_bf16(const NormArgs& a, hipStream_t stream, int64_t max_grid);
+hipError_t norm_backward_fp16(const NormArgs& a, hipStream_t stream, int64_t max_grid);
+hipError_t norm_backward_fp32(const NormArgs& a, hipStream_t stream, int64_t max_grid);
+
 hipError_t launch_norm_backward(const NormArgs& a, hipStream_t stream, int64_t max_grid);
 
 }  // namespace la

@@ -20,7 +20,7 @@ using la::range;
 using la::type_bytes;
 
 constexpr int64_t kMostStride = int64_t(1) << 40;  // keeps every offset far from 64 bits
-constexpr int64_t kMostRows = int64_t(1) << 31;
+constexpr int64_t kMostRows = (int64_t(1) << 30);  // row counts and steps past them fit 32 bits
 
 bool is_type(int t) { return t == LA_TYPE_BF16 || t == LA_TYPE_FP16 || t == LA_TYPE_FP32; }
 
@@ -33,10 +33,9 @@ la_status check_norm(const la_norm_desc* n) {
   if (!is_type(n->weight_type))
     return fail(LA_ERR_UNSUPPORTED, "weight_type = %d, need a la_element_type", n->weight_type);
   if (n->outer < 0 || n->inner < 0 || n->cols < 0 || n->outer > kMostRows ||
-      n->inner > kMostRows || n->cols > LA_MAX_SIDE ||
-      static_cast<double>(n->outer) * static_cast<double>(n->inner) *
-              static_cast<double>(n->cols) > 0x1p44)
-    return fail(LA_ERR_INVALID_ARGUMENT, "%lld x %lld rows of %lld elements, need 0..%d elements",
+      n->inner > kMostRows || n->outer * n->inner > kMostRows || n->cols > LA_MAX_SIDE ||
+      static_cast<double>(n->outer * n->inner) * static_cast<double>(n->cols) > 0x1p44)
+    return fail(LA_ERR_INVALID_ARGUMENT, "%lld x %lld rows of %lld elements: at most 2^30 rows of %d, 2^44 elements",
                 static_cast<long long>(n->outer), static_cast<long long>(n->inner),
                 static_cast<long long>(n->cols), LA_MAX_SIDE);
   if (!(std::isfinite(n->eps) && n->eps >= 0.0))
@@ -98,7 +97,7 @@ NormArgs arguments(const la_norm_desc& n) {
   NormArgs a = {};
   a.weight = n.weight;
   a.bias = n.bias;
-  a.rows = n.outer * n.inner;
+  a.rows = static_cast<int32_t>(n.outer * n.inner);
   a.cols = static_cast<int32_t>(n.cols);
   a.layer = n.kind == LA_NORM_LAYER;
   a.type = n.type;
@@ -110,7 +109,7 @@ NormArgs arguments(const la_norm_desc& n) {
 
 // One stride where it serves every tensor: no division per row.
 void merge(NormArgs& a, const la_norm_desc& n, bool merged) {
-  a.inner = n.inner;
+  a.inner = static_cast<int32_t>(n.inner);
   if (n.inner > 1 && !merged) return;
   a.inner = 1;
   if (n.inner > 1)
@@ -150,7 +149,7 @@ la_status forward(const la_norm_desc* n, const la_norm_forward_io* io, void* str
 }
 
 // Places of the backward pass' workspace; returns its bytes.
-int64_t plan_backward(const la_norm_desc& n, int64_t* parts, int64_t* rows_per_part,
+int64_t plan_backward(const la_norm_desc& n, int32_t* parts, int32_t* rows_per_part,
                       int64_t* partial, int64_t* coefficients) {
   *parts = 0;
   *rows_per_part = 1;
@@ -158,7 +157,7 @@ int64_t plan_backward(const la_norm_desc& n, int64_t* parts, int64_t* rows_per_p
   if (n.cols == 0 || rows == 0) return 0;
   la::norm_parts(rows, n.cols, n.type, parts, rows_per_part);
   la::Taker take;
-  *partial = take(2 * 4 * *parts * n.cols);
+  *partial = take(2 * 4 * int64_t(*parts) * n.cols);
   *coefficients = take(n.cols * type_bytes(n.type) > la::kNormRegisterBytes ? 8 * rows : 0);
   return take.at;
 }
@@ -218,7 +217,8 @@ LA_API int64_t la_norm_backward_workspace_bytes(const la_norm_desc* norm) {
   return la::guarded(
       [&]() -> int64_t {
         if (check_norm(norm) != LA_OK) return -1;
-        int64_t parts, rows_per_part, partial, coefficients;
+        int32_t parts, rows_per_part;
+        int64_t partial, coefficients;
         const int64_t bytes =
             plan_backward(*norm, &parts, &rows_per_part, &partial, &coefficients);
         ok();
