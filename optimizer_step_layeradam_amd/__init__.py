@@ -1145,16 +1145,22 @@ def norm_backward_raw(desc: NormDesc, io: NormBackwardIO, workspace: int = 0,
                                    workspace_bytes, stream or None), lib)
 
 
+_types = {}
+
+
 def _element_types():
-    import torch
-    return {torch.bfloat16: TYPE_BF16, torch.float16: TYPE_FP16, torch.float32: TYPE_FP32}
+    if not _types:
+        import torch
+        _types.update({torch.bfloat16: TYPE_BF16, torch.float16: TYPE_FP16,
+                       torch.float32: TYPE_FP32})
+    return _types
 
 
 def _element_type(t, what: str) -> int:
-    types = _element_types()
-    if t.dtype not in types:
-        raise TypeError(f"{what} must be one of {[str(k) for k in types]}, got {t.dtype}")
-    return types[t.dtype]
+    kind = _element_types().get(t.dtype)
+    if kind is None:
+        raise TypeError(f"{what} must be one of {[str(k) for k in _types]}, got {t.dtype}")
+    return kind
 
 
 def _one_stride(shape, strides):
@@ -1167,71 +1173,112 @@ def _one_stride(shape, strides):
     return axes[-1][1] if axes else 0
 
 
+def _current_device(x) -> int:
+    """The device that x is on if it is the current one, else -2, which no
+    tensor is on: _address() then goes by device_address() and its refusals."""
+    import torch
+    device = x.get_device()
+    return device if device >= 0 and device == torch.cuda.current_device() else -2
+
+
+def _address(t, device: int) -> int:
+    """device_address(), in short for a tensor on the current device; 0 where
+    there is no tensor, or nothing in it."""
+    if t is None or not t.numel():
+        return 0
+    return t.data_ptr() if t.get_device() == device else device_address(t)
+
+
+def _stream_address(stream, device: int) -> int:
+    """Address of the stream, or of the current one: where torch has it at
+    hand without a Stream object, 2.5 us sooner."""
+    import torch
+    if stream is not None:
+        return stream.cuda_stream
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is not None and device >= 0:
+        return raw(device)
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _new_workspace(needed: int, stream, device):
+    import torch
+    if needed < 0:
+        raise LayerAdamError(1, last_error())
+    return _new(stream, max(1, needed), torch.uint8, device)
+
+
+def _workspace_address(workspace, device: int) -> int:
+    import torch
+    if workspace.dtype != torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous():
+        raise TypeError("the workspace must be a contiguous uint8 CUDA tensor")
+    return _address(workspace, device)
+
+
+def _new(stream, shape, dtype, device):
+    """A new tensor that belongs to the call's stream."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 class _RowLayout:
     """How a call's tensors of one shape divide into rows with two strides:
     (outer, inner) counts, and each tensor's strides."""
 
-    def __init__(self, x, what: str = "x"):
+    def __init__(self, x):
         if x.dim() < 1:
-            raise ValueError(f"{what} needs at least one dimension")
+            raise ValueError("x needs at least one dimension")
         self.shape, self.dtype = x.shape, x.dtype
+        self.device = _current_device(x)
         self.cols = x.shape[-1]
-        lead = x.shape[:-1]
-        self.rows = 1
-        for n in lead:
-            self.rows *= n
-        self.inner = lead[-1] if len(lead) > 1 else 1
-        self.outer = self.rows // self.inner if self.inner else 0
+        self.inner = x.shape[-2] if x.dim() > 2 else 1
+        self.outer = 1
+        for n in x.shape[:-2] if x.dim() > 2 else x.shape[:-1]:
+            self.outer *= n
+        self.rows = self.outer * self.inner
 
     def __call__(self, t, what: str) -> Rows:
+        if t is None:
+            return Rows()
         if t.shape != self.shape or t.dtype != self.dtype:
             raise ValueError(f"{what} is {tuple(t.shape)} {t.dtype}, expected "
                              f"{tuple(self.shape)} {self.dtype}")
-        if self.rows == 0 or self.cols == 0:
-            return Rows(0, 0, 0)
-        if self.cols > 1 and t.stride(-1) != 1:
+        strides = t.stride()
+        if self.cols > 1 and strides[-1] != 1 and self.rows:
             raise ValueError(f"{what} must be contiguous along its last axis")
-        if len(self.shape) < 3:
-            return Rows(device_address(t), t.stride(0) if len(self.shape) == 2 else 0, 0)
-        outer = _one_stride(self.shape[:-2], t.stride()[:-2])
+        if len(strides) < 3:
+            return Rows(_address(t, self.device), strides[0] if len(strides) == 2 else 0, 0)
+        outer = _one_stride(self.shape[:-2], strides[:-2])
         if outer is None:
             raise ValueError(f"{what}: the axes before the last two must be one stride apart, got "
-                             f"strides {t.stride()} of shape {tuple(t.shape)}")
-        return Rows(device_address(t), outer, t.stride(-2))
+                             f"strides {strides} of shape {tuple(t.shape)}")
+        return Rows(_address(t, self.device), outer, strides[-2])
 
+    def parameter(self, t, what: str, dtype=None) -> int:
+        """Address of a contiguous vector of cols elements; 0 for None."""
+        if t is None:
+            return 0
+        if t.shape != (self.cols,) or not t.is_contiguous():
+            raise ValueError(f"{what} must be a contiguous vector of {self.cols} elements, got "
+                             f"{tuple(t.shape)}")
+        if dtype is not None and t.dtype != dtype:
+            raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+        return _address(t, self.device)
 
-def _parameter(t, cols: int, what: str, dtype=None) -> int:
-    """Address of a contiguous vector of cols elements; 0 for None."""
-    if t is None:
-        return 0
-    if t.dim() != 1 or t.shape[0] != cols or not (t.is_contiguous() or cols <= 1):
-        raise ValueError(f"{what} must be a contiguous vector of {cols} elements, got "
-                         f"{tuple(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    return device_address(t) if cols else 0
+    def check_statistics(self, stats, layer: bool) -> None:
+        import torch
+        wanted = (2 if layer else 1, self.rows)
+        if stats.dtype != torch.float32 or stats.shape != wanted or not stats.is_contiguous():
+            raise ValueError(f"stats must be a contiguous float32 tensor of shape {wanted}, got "
+                             f"{tuple(stats.shape)} {stats.dtype}")
 
-
-def _check_statistics(stats, rows: int, layer: bool) -> None:
-    import torch
-    wanted = (2 if layer else 1, rows)
-    if stats.dtype != torch.float32 or tuple(stats.shape) != wanted or not stats.is_contiguous():
-        raise ValueError(f"stats must be a contiguous float32 tensor of shape {wanted}, got "
-                         f"{tuple(stats.shape)} {stats.dtype}")
-
-
-def _statistics(stats, rows: int, layer: bool):
-    """(mean, rstd) addresses of a statistics tensor."""
-    if rows == 0:
-        return 0, 0
-    p = device_address(stats)
-    return (p, p + 4 * rows) if layer else (0, p)
-
-
-def _on(stream):
-    """The context in which a call takes new tensors: they belong to its stream."""
-    import torch
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    def statistics(self, stats, layer: bool):
+        """(mean, rstd) addresses of a statistics tensor."""
+        p = _address(stats, self.device)
+        return (p, p + 4 * self.rows) if layer and p else (0, p)
 
 
 def _norm(kind, x, weight, bias, eps, residual, out, sum_out, stats, stream):
@@ -1239,32 +1286,26 @@ def _norm(kind, x, weight, bias, eps, residual, out, sum_out, stats, stream):
     layout = _RowLayout(x)
     layer = kind == NORM_LAYER
     type_ = _element_type(x, "x")
-    weight_type = type_ if weight is None else _element_type(weight, "weight")
-    if weight is None and bias is not None:
-        weight_type = _element_type(bias, "bias")
+    parameter = weight if weight is not None else bias
+    weight_type = type_ if parameter is None else _element_type(parameter, "the parameters")
     if sum_out is not None and residual is None:
         raise ValueError("sum_out is the sum of x and a residual: give the residual too")
-    if stats is not None:
-        _check_statistics(stats, layout.rows, layer)
-    with _on(stream):
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        if sum_out is None and residual is not None:
-            sum_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        if stats is None:
-            stats = torch.empty((2 if layer else 1, layout.rows), dtype=torch.float32,
-                                device=x.device)
-    none = Rows(0, 0, 0)
-    desc = make_norm(kind, layout.outer, layout.inner, layout.cols, type_, weight_type,
-                     _parameter(weight, layout.cols, "weight"),
-                     _parameter(bias, layout.cols, "bias",
-                                None if weight is None else weight.dtype), eps)
-    mean, rstd = _statistics(stats, layout.rows, layer)
-    io = NormForwardIO(layout(x, "x"), none if residual is None else layout(residual, "residual"),
-                       layout(out, "out"), none if residual is None else layout(sum_out, "sum_out"),
-                       mean or None, rstd or None)
-    s = stream if stream is not None else torch.cuda.current_stream()
-    norm_forward_raw(desc, io, s.cuda_stream)
+    if stats is None:
+        stats = _new(stream, (2 if layer else 1, layout.rows), torch.float32, x.device)
+    else:
+        layout.check_statistics(stats, layer)
+    if out is None:
+        out = _new(stream, x.shape, x.dtype, x.device)
+    if sum_out is None and residual is not None:
+        sum_out = _new(stream, x.shape, x.dtype, x.device)
+    desc = NormDesc(layout.outer, layout.inner, layout.cols, kind, type_, weight_type,
+                    layout.parameter(weight, "weight"),
+                    layout.parameter(bias, "bias", None if weight is None else weight.dtype),
+                    eps)
+    mean, rstd = layout.statistics(stats, layer)
+    norm_forward_raw(desc, NormForwardIO(layout(x, "x"), layout(residual, "residual"),
+                                         layout(out, "out"), layout(sum_out, "sum_out"), mean,
+                                         rstd), _stream_address(stream, layout.device))
     return (out, stats) if residual is None else (out, stats, sum_out)
 
 
@@ -1298,39 +1339,34 @@ def rms_norm(x, weight=None, *, eps: float = 1e-6, residual=None, out=None, sum_
 
 def _norm_backward(kind, dy, x, weight, stats, residual_grad, dx, dweight, dbias, weight_grad,
                    bias_grad, workspace, stream):
-    import torch
     layout = _RowLayout(x)
+    layer = kind == NORM_LAYER
     type_ = _element_type(x, "x")
     weight_type = type_ if weight is None else _element_type(weight, "weight")
-    _check_statistics(stats, layout.rows, kind == NORM_LAYER)
-    with _on(stream):
-        if dx is None:
-            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        grad_dtype = x.dtype if weight is None else weight.dtype
-        if dweight is not None:
-            grad_dtype = dweight.dtype
-        elif dbias is not None:
-            grad_dtype = dbias.dtype
-        if dweight is None and weight_grad:
-            dweight = torch.empty(layout.cols, dtype=grad_dtype, device=x.device)
-        if dbias is None and bias_grad:
-            dbias = torch.empty(layout.cols, dtype=grad_dtype, device=x.device)
-    grads = [t for t in (dweight, dbias) if t is not None]
-    grad_type = _element_type_of(grads, "dweight and dbias", _element_types()) if grads else type_
-    desc = make_norm(kind, layout.outer, layout.inner, layout.cols, type_, weight_type,
-                     _parameter(weight, layout.cols, "weight"))
-    mean, rstd = _statistics(stats, layout.rows, kind == NORM_LAYER)
-    none = Rows(0, 0, 0)
-    io = NormBackwardIO(layout(dy, "dy"), layout(x, "x"),
-                        none if residual_grad is None else layout(residual_grad, "residual_grad"),
-                        layout(dx, "dx"), mean or None, rstd or None,
-                        _parameter(dweight, layout.cols, "dweight") or None,
-                        _parameter(dbias, layout.cols, "dbias") or None, grad_type)
-    s = stream if stream is not None else torch.cuda.current_stream()
+    layout.check_statistics(stats, layer)
+    if dx is None:
+        dx = _new(stream, x.shape, x.dtype, x.device)
+    given = dweight if dweight is not None else dbias if dbias is not None else weight
+    grad_dtype = x.dtype if given is None else given.dtype
+    if dweight is None and weight_grad:
+        dweight = _new(stream, layout.cols, grad_dtype, x.device)
+    if dbias is None and bias_grad:
+        dbias = _new(stream, layout.cols, grad_dtype, x.device)
+    if dweight is not None and dbias is not None and dweight.dtype != dbias.dtype:
+        raise TypeError(f"dweight and dbias must have one type, got {dweight.dtype} and "
+                        f"{dbias.dtype}")
+    some = dweight if dweight is not None else dbias
+    grad_type = type_ if some is None else _element_type(some, "dweight and dbias")
+    desc = NormDesc(layout.outer, layout.inner, layout.cols, kind, type_, weight_type,
+                    layout.parameter(weight, "weight"), None, 0.0)
+    mean, rstd = layout.statistics(stats, layer)
+    io = NormBackwardIO(layout(dy, "dy"), layout(x, "x"), layout(residual_grad, "residual_grad"),
+                        layout(dx, "dx"), mean, rstd, layout.parameter(dweight, "dweight"),
+                        layout.parameter(dbias, "dbias"), grad_type)
     if workspace is None:
-        needed = norm_backward_workspace_bytes_raw(desc)
-        workspace = _allocate_workspace(needed, s)
-    norm_backward_raw(desc, io, _workspace_ptr(workspace), workspace.numel(), s.cuda_stream)
+        workspace = _new_workspace(norm_backward_workspace_bytes_raw(desc), stream, x.device)
+    norm_backward_raw(desc, io, _workspace_address(workspace, layout.device), workspace.numel(),
+                      _stream_address(stream, layout.device))
     return dx, dweight, dbias
 
 
@@ -1414,11 +1450,6 @@ def _check_matrix(t, shape, dtype, what: str) -> None:
         raise ValueError(f"{what} must be contiguous along its last axis")
 
 
-def _address(t) -> int:
-    """Address of a tensor; 0 where there is none, or nothing in it."""
-    return device_address(t) if t is not None and t.numel() else 0
-
-
 def _cross_entropy(x, weight, targets, ignore_index, reduction, grad_scale, loss, losses, dx,
                    dweight, input_grad, weight_grad, workspace, stream):
     import torch
@@ -1427,17 +1458,18 @@ def _cross_entropy(x, weight, targets, ignore_index, reduction, grad_scale, loss
     if x.dim() < 1 or weight.dim() != 2:
         raise ValueError("x needs at least one dimension, the weight two")
     hidden, vocab = x.shape[-1], weight.shape[0]
-    types = {torch.bfloat16: TYPE_BF16, torch.float16: TYPE_FP16}
-    type_ = _element_type_of([x, weight], "x and the weight", types)
-    indices = {torch.int64: INDEX_INT64, torch.int32: INDEX_INT32}
-    if targets.dtype not in indices:
+    type_ = _element_type(x, "x")
+    if type_ == TYPE_FP32 or weight.dtype != x.dtype:
+        raise TypeError(f"x and the weight must be both bfloat16 or both float16, got {x.dtype} "
+                        f"and {weight.dtype}")
+    if targets.dtype not in (torch.int64, torch.int32):
         raise TypeError(f"targets must be int64 or int32, got {targets.dtype}")
-    if targets.shape != x.shape[:-1]:
-        raise ValueError(f"targets are {tuple(targets.shape)}, expected {tuple(x.shape[:-1])}")
+    lead = x.shape[:-1]
+    if targets.shape != lead:
+        raise ValueError(f"targets are {tuple(targets.shape)}, expected {tuple(lead)}")
     if not targets.is_contiguous():
         raise ValueError("targets must be contiguous")
     tokens = targets.numel()
-    lead = tuple(targets.shape)
     if x.dim() != 2:
         x = _token_rows(x, "x")
     _check_matrix(x, (tokens, hidden), x.dtype, "x")
@@ -1446,33 +1478,33 @@ def _cross_entropy(x, weight, targets, ignore_index, reduction, grad_scale, loss
         if t is not None and (t.dtype != torch.float32 or t.numel() != n or
                               not t.is_contiguous()):
             raise ValueError(f"{what} must be a contiguous float32 tensor of {n} elements")
-    with _on(stream):
-        if loss is None:
-            loss = torch.empty((), dtype=torch.float32, device=x.device)
-        if dx is None and input_grad:
-            dx = torch.empty((*lead, hidden), dtype=x.dtype, device=x.device)
-        if dweight is None and weight_grad:
-            dweight = torch.empty((vocab, hidden), dtype=x.dtype, device=x.device)
+    if loss is None:
+        loss = _new(stream, (), torch.float32, x.device)
+    if dx is None and input_grad:
+        dx = _new(stream, (*lead, hidden), x.dtype, x.device)
+    if dweight is None and weight_grad:
+        dweight = _new(stream, (vocab, hidden), x.dtype, x.device)
     rows = dx
     if dx is not None:
-        if tuple(dx.shape) != (*lead, hidden):
+        if dx.shape != (*lead, hidden):
             raise ValueError(f"dx is {tuple(dx.shape)}, expected {(*lead, hidden)}")
         rows = dx if dx.dim() == 2 else _token_rows(dx, "dx")
         _check_matrix(rows, (tokens, hidden), x.dtype, "dx")
     if dweight is not None:
         _check_matrix(dweight, (vocab, hidden), x.dtype, "dweight")
+    device = _current_device(x)
     desc = CrossEntropyDesc(
-        _address(x), _address(weight), _address(targets), tokens, hidden, vocab, x.stride(0),
-        weight.stride(0), type_, indices[targets.dtype], int(ignore_index), REDUCTIONS[reduction],
-        float(grad_scale), _address(loss), _address(losses), _address(rows), _address(dweight),
-        0 if rows is None else rows.stride(0), 0 if dweight is None else dweight.stride(0))
-    s = stream if stream is not None else torch.cuda.current_stream()
+        _address(x, device), _address(weight, device), _address(targets, device), tokens, hidden,
+        vocab, x.stride(0), weight.stride(0), type_,
+        INDEX_INT64 if targets.dtype == torch.int64 else INDEX_INT32, ignore_index,
+        REDUCTIONS[reduction], grad_scale, _address(loss, device), _address(losses, device),
+        _address(rows, device), _address(dweight, device), 0 if rows is None else rows.stride(0),
+        0 if dweight is None else dweight.stride(0))
     if workspace is None:
-        needed = linear_cross_entropy_workspace_bytes_raw(desc)
-        if needed < 0:
-            raise LayerAdamError(1, last_error())
-        workspace = _allocate_workspace(needed, s)
-    linear_cross_entropy_raw(desc, _workspace_ptr(workspace), workspace.numel(), s.cuda_stream)
+        workspace = _new_workspace(linear_cross_entropy_workspace_bytes_raw(desc), stream,
+                                   x.device)
+    linear_cross_entropy_raw(desc, _workspace_address(workspace, device), workspace.numel(),
+                             _stream_address(stream, device))
     return loss, dx, dweight
 
 

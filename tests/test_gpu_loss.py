@@ -14,7 +14,8 @@ NAN = float("nan")
 
 
 def run(x, w, y, mean=True, scale=1.0, **kw):
-    losses = torch.full((y.numel(),), 9.0, device="cuda")
+    with torch.cuda.stream(kw.get("stream")):  # None: the current one
+        losses = torch.full((y.numel(),), 9.0, device="cuda")
     loss, dx, dw = la.linear_cross_entropy_gradients(
         x, w, y, reduction="mean" if mean else "sum", grad_scale=scale, losses=losses, **kw)
     return loss, losses, dx, dw
@@ -300,7 +301,7 @@ def test_from_the_norm_to_the_step(dtype):
         assert float((got.double() - e).norm() / e.norm()) < 4 * half
     # a rounded `out` moves each logit by at most half times the sum of its products' sizes
     moved = half * float((od.detach().abs() @ wd.detach().abs().T).max())
-    assert abs(float(loss) - float(want_loss)) < 2 * moved
+    assert abs(float(loss) - float(want_loss.detach())) < 2 * moved
 
     state = [(t.float(), torch.zeros(t.shape, device="cuda"), torch.zeros(t.shape, device="cuda"),
               t.clone()) for t in (gamma, w)]
