@@ -89,41 +89,52 @@ struct LossPiece {
 
 enum class LossProduct { kKeep, kSums, kAgain, kInput, kWeight };
 
+// Tiles of the products: 32 x 128, 64 x 128, 128 x 128 and 256 x 256.
+enum class LossTile { kSmallest, kSmall, kMedium, kLarge };
+
+// A product's tiles, and the parts that its sum is cut into.
+struct LossShape {
+  LossTile tile;
+  int32_t parts;
+};
+
+struct LossShapes {
+  LossShape logits, input, weight;
+  int32_t chunk_shift;      // log2 of the columns of one of `sums`, by the logits' tile
+};
+
+// For pieces of `columns` (0: no gradients).
+LossShapes loss_shapes(int64_t tokens, int64_t hidden, int64_t vocab, int64_t columns);
+
 struct LossProductArgs {
   LossRows r;
   LossPiece piece;
+  LossShape shape;          // of this product
   const uint16_t* w;        // weight, rows ldw elements apart, zeros behind hidden up to width
   int64_t ldw;
-  float* partial;           // kInput: splits x tokens x width
-  int32_t splits;           // kInput: parts of the sum over the piece
-  int32_t large_input;      // kInput: in 256 x 256 tiles
-  int32_t depth;            // kInput: columns of one part, a multiple of 64
+  float* partial;           // results in binary32, parts x rows x width: always of kInput, unless
+                            // `direct`; of kWeight where its sum has parts
+  int32_t depth;            // elements of one part, a multiple of 64
   int32_t add;              // kInput: to what is there
+  int32_t direct;           // kInput: the results are dx
   uint16_t* dw;             // kWeight
   int64_t dw_stride;
 };
 
-// log2 of a chunk's columns in the tile that a call of this size takes.
-int loss_chunk_shift(int64_t tokens, int64_t hidden, int64_t vocab);
-
 hipError_t launch_loss_gather(const LossRows& r, hipStream_t stream, int64_t max_grid);
 hipError_t launch_pack(const uint16_t* from, int64_t stride, int64_t rows, int cols, uint16_t* to,
                        int width, hipStream_t stream, int64_t max_grid);
-// lse and losses from the chunks, and the loss from those.
-hipError_t launch_loss_lse(const LossRows& r, hipStream_t stream, int64_t max_grid);
-// e becomes g in the first piece.
+// lse and losses from the chunks; with `sum`, the loss from those.
+hipError_t launch_loss_lse(const LossRows& r, bool sum, hipStream_t stream, int64_t max_grid);
+// e becomes g in the first piece; the loss.
 hipError_t launch_loss_softmax(const LossRows& r, const LossPiece& piece, hipStream_t stream,
                                int64_t max_grid);
-hipError_t launch_loss_input(const LossRows& r, const float* partial, int splits,
+// dx, or dw of a piece, from the parts.
+hipError_t launch_loss_input(const LossRows& r, const float* partial, int parts,
                              hipStream_t stream, int64_t max_grid);
+hipError_t launch_loss_weight(const LossProductArgs& a, hipStream_t stream, int64_t max_grid);
 
 hipError_t launch_loss_product(const LossProductArgs& a, LossProduct what, hipStream_t stream,
                                int64_t max_grid);
-// Parts of the sum of kInput, and its tiles.
-struct LossSplits {
-  int parts;
-  bool large;
-};
-LossSplits loss_splits(int64_t tokens, int64_t hidden, int64_t columns);
 
 }  // namespace la

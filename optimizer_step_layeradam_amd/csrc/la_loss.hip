@@ -180,7 +180,7 @@ __device__ __forceinline__ S block_sum(S x) {
 // joined to lse. A workgroup takes ROWS rows at a time, 1024 / ROWS threads
 // to each, whose reads are whole lines where ROWS is 16.
 template <int ROWS>
-__global__ __launch_bounds__(1024) void lse_kernel(LossRows r) {
+__global__ __launch_bounds__(1024) void lse_kernel(LossRows r, int sum) {
   constexpr int SHARES = 1024 / ROWS;
   __shared__ float2 parts[SHARES][ROWS];
   __shared__ float own[ROWS];
@@ -188,13 +188,13 @@ __global__ __launch_bounds__(1024) void lse_kernel(LossRows r) {
   const int share = threadIdx.x / ROWS, lane = threadIdx.x % ROWS;
   for (int first = blockIdx.x * ROWS; first < n; first += gridDim.x * ROWS) {
     const int row = min(first + lane, n - 1);
-    float most = -__builtin_inff(), sum = 0.0f;
-    auto join = [](float& most, float& sum, float2 x) {
+    float most = -__builtin_inff(), total = 0.0f;
+    auto join = [](float& most, float& total, float2 x) {
       const float top = __builtin_fmaxf(most, x.x);
       // nothing so far, or nothing here: exp(-inf - top) is 0, unless top is too
       const float point = top == -__builtin_inff() ? 0.0f : top;
-      sum = sum * __builtin_amdgcn_exp2f(most - point) +
-            x.y * __builtin_amdgcn_exp2f(x.x - point);
+      total = total * __builtin_amdgcn_exp2f(most - point) +
+              x.y * __builtin_amdgcn_exp2f(x.x - point);
       most = top;
     };
     const float2* sums = r.sums + row;
@@ -204,15 +204,15 @@ __global__ __launch_bounds__(1024) void lse_kernel(LossRows r) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] = sums[static_cast<int64_t>(k + i * SHARES) * r.tokens];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) join(most, sum, x[i]);
+      for (int i = 0; i < 4; ++i) join(most, total, x[i]);
     }
-    for (; k < r.chunks; k += SHARES) join(most, sum, sums[static_cast<int64_t>(k) * r.tokens]);
-    parts[share][lane] = make_float2(most, sum);
+    for (; k < r.chunks; k += SHARES) join(most, total, sums[static_cast<int64_t>(k) * r.tokens]);
+    parts[share][lane] = make_float2(most, total);
     __syncthreads();
     for (int step = SHARES / 2; step > 0; step >>= 1) {
       if (share < step) {
-        join(most, sum, parts[share + step][lane]);
-        parts[share][lane] = make_float2(most, sum);
+        join(most, total, parts[share + step][lane]);
+        parts[share][lane] = make_float2(most, total);
       }
       __syncthreads();
     }
@@ -221,7 +221,7 @@ __global__ __launch_bounds__(1024) void lse_kernel(LossRows r) {
       const bool outside = r.target[row] < 0;
       const float nan = __builtin_nanf("");
       // in binary64, since these are large beside a small loss
-      const double log_sum = log(static_cast<double>(sum)) - kLossExponent * kLn2;
+      const double log_sum = log(static_cast<double>(total)) - kLossExponent * kLn2;
       const double lse = static_cast<double>(most) * kLn2 + log_sum;
       const float loss =
           outside ? nan : static_cast<float>(lse - static_cast<double>(r.target_logit[row]));
@@ -232,28 +232,30 @@ __global__ __launch_bounds__(1024) void lse_kernel(LossRows r) {
     __syncthreads();
   }
   // The one workgroup of a call of few tokens adds their losses up itself.
-  if (r.tokens <= ROWS && threadIdx.x == 0) {
+  if (sum && threadIdx.x == 0) {
     double s = 0.0;
     for (int i = 0; i < n; ++i) s += static_cast<double>(own[i]);
     *r.loss = static_cast<float>(r.mean && n > 1 ? s / static_cast<double>(n) : s);
   }
 }
 
-// The loss of all tokens, summed in binary64 in a fixed order. (Not by the last
-// workgroup of lse_kernel: the fence that it would take writes back what L2
-// holds of e, 150 us where e is 2.4 GB.)
-__global__ __launch_bounds__(1024) void sum_kernel(LossRows r) {
-  const int n = *r.count;
+template <int THREADS>
+__device__ __forceinline__ void sum_losses(const LossRows& r, int n) {
   double s = 0.0;
-  for (int i = threadIdx.x; i < n; i += 1024) s += static_cast<double>(r.compact_losses[i]);
-  s = block_sum<1024>(s);
+  for (int i = threadIdx.x; i < n; i += THREADS) s += static_cast<double>(r.compact_losses[i]);
+  s = block_sum<THREADS>(s);
   if (threadIdx.x == 0)
     *r.loss = static_cast<float>(r.mean && n > 1 ? s / static_cast<double>(n) : s);
 }
 
+// The loss of all tokens without gradients. (Not by the last workgroup of
+// lse_kernel: the fence that it would take writes back what L2 holds.)
+__global__ __launch_bounds__(1024) void sum_kernel(LossRows r) { sum_losses<1024>(r, *r.count); }
+
 // e of the held piece becomes g, in place: 16 rows of 2048 columns a workgroup,
 // whose factors are formed once, in LDS. Eight rows of a thread are asked for before
-// the first is needed.
+// the first is needed. The first workgroup adds the losses up too, in binary64 and
+// in a fixed order.
 constexpr int kSoftmaxRows = 16, kSoftmaxCols = 2048;
 
 template <typename T>
@@ -268,6 +270,7 @@ __global__ __launch_bounds__(256) void softmax_kernel(LossRows r, LossPiece piec
   const int width = (piece.cols + kLossDepth - 1) / kLossDepth * kLossDepth;
   const int across = (width + kSoftmaxCols - 1) / kSoftmaxCols;
   const int64_t total = static_cast<int64_t>(padded / kSoftmaxRows) * across;
+  if (blockIdx.x == 0) sum_losses<256>(r, n);
   for (int64_t k = blockIdx.x; k < total; k += gridDim.x) {
     const int first = static_cast<int>(k / across) * kSoftmaxRows;
     const int col0 = static_cast<int>(k % across) * kSoftmaxCols;
@@ -315,36 +318,37 @@ __global__ __launch_bounds__(256) void softmax_kernel(LossRows r, LossPiece piec
   }
 }
 
-// dx of the gathered tokens from the parts of their sums, in order: 1024
-// columns of a row a workgroup.
-template <typename T>
-__global__ __launch_bounds__(256) void input_kernel(LossRows r, const float* partial, int splits) {
-  const int n = *r.count, across = (r.width + 1023) / 1024;
+// A product's results from the parts of its sum, in order, times c: 1024 columns
+// of a row a workgroup. INPUT: row i is that of the token it was gathered from.
+template <typename T, bool INPUT>
+__global__ __launch_bounds__(256) void parts_kernel(LossRows r, const float* partial, int parts,
+                                                    int rows, uint16_t* to, int64_t to_stride) {
+  const int n = *r.count, across = (r.width + 1023) / 1024, kept = INPUT ? n : rows;
   const float c = (r.mean && n > 1 ? r.scale / static_cast<float>(n) : r.scale) / T::encode_scale;
-  const int64_t stride = static_cast<int64_t>(r.tokens) * r.width;
-  for (int64_t k = blockIdx.x; k < static_cast<int64_t>(n) * across; k += gridDim.x) {
+  const int64_t stride = static_cast<int64_t>(rows) * r.width;
+  for (int64_t k = blockIdx.x; k < static_cast<int64_t>(kept) * across; k += gridDim.x) {
     const int row = static_cast<int>(k / across);
     const int at = static_cast<int>(k - static_cast<int64_t>(row) * across) * 1024 + threadIdx.x * 4;
     if (at >= r.hidden) continue;
     const float* from = partial + static_cast<int64_t>(row) * r.width + at;
     float4 s = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
-    for (int i = 0; i < splits; ++i) {  // width is a multiple of 4
+    for (int i = 0; i < parts; ++i) {  // width is a multiple of 4
       const float4 v = *reinterpret_cast<const float4*>(from + i * stride);
       s.x += v.x;
       s.y += v.y;
       s.z += v.z;
       s.w += v.w;
     }
-    uint16_t* to = r.dx + r.index[row] * r.dx_stride + at;
+    uint16_t* out = to + (INPUT ? r.index[row] : row) * to_stride + at;
     const uint16_t o[4] = {T::encode(s.x * c), T::encode(s.y * c), T::encode(s.z * c),
                            T::encode(s.w * c)};
     if (at + 4 <= r.hidden) {
-      __builtin_memcpy(to, o, 8);
+      __builtin_memcpy(out, o, 8);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (at + i < r.hidden) to[i] = o[i];
+        if (at + i < r.hidden) out[i] = o[i];
     }
   }
 }
@@ -375,31 +379,40 @@ hipError_t launch_pack(const uint16_t* from, int64_t stride, int64_t rows, int c
   return launch(pack_kernel, (rows * (width / 8) + span - 1) / span, 256, stream, max_grid, from, stride, rows, cols, to, width);
 }
 
-hipError_t launch_loss_lse(const LossRows& r, hipStream_t stream, int64_t max_grid) {
+hipError_t launch_loss_lse(const LossRows& r, bool sum, hipStream_t stream, int64_t max_grid) {
   // one workgroup where it is enough, a workgroup to each of few rows, then 16 rows to one
-  if (r.tokens <= 1) return launch(lse_kernel<1>, 1, 1024, stream, max_grid, r);
-  if (r.tokens <= 16) return launch(lse_kernel<16>, 1, 1024, stream, max_grid, r);
+  const int now = sum;
+  if (r.tokens <= 1) return launch(lse_kernel<1>, 1, 1024, stream, max_grid, r, now);
+  if (r.tokens <= 16) return launch(lse_kernel<16>, 1, 1024, stream, max_grid, r, now);
   const hipError_t e =
-      r.tokens <= 256 ? launch(lse_kernel<1>, r.tokens, 1024, stream, max_grid, r)
-                      : launch(lse_kernel<16>, (r.tokens + 15) / 16, 1024, stream, max_grid, r);
-  if (e != hipSuccess) return e;
+      r.tokens <= 256 ? launch(lse_kernel<1>, r.tokens, 1024, stream, max_grid, r, 0)
+                      : launch(lse_kernel<16>, (r.tokens + 15) / 16, 1024, stream, max_grid, r, 0);
+  if (e != hipSuccess || !sum) return e;
   return launch(sum_kernel, 1, 1024, stream, max_grid, r);
 }
 
 hipError_t launch_loss_softmax(const LossRows& r, const LossPiece& piece, hipStream_t stream,
                                int64_t max_grid) {
   const int64_t rows = (static_cast<int64_t>(r.tokens) + kLossDepth - 1) / kLossDepth * kLossDepth;
-  const int64_t grid = rows / kSoftmaxRows *
+  const int64_t grid = std::max<int64_t>(1, rows / kSoftmaxRows) *
                        ((static_cast<int64_t>(piece.cols) + kSoftmaxCols - 1) / kSoftmaxCols);
   return launch(r.bf16 ? softmax_kernel<ScaledBf16> : softmax_kernel<ScaledFp16>, grid, 256, stream,
                 max_grid, r, piece);
 }
 
-hipError_t launch_loss_input(const LossRows& r, const float* partial, int splits,
+hipError_t launch_loss_input(const LossRows& r, const float* partial, int parts,
                              hipStream_t stream, int64_t max_grid) {
-  return launch(r.bf16 ? input_kernel<ScaledBf16> : input_kernel<ScaledFp16>,
+  return launch(r.bf16 ? parts_kernel<ScaledBf16, true> : parts_kernel<ScaledFp16, true>,
                 r.tokens * ((static_cast<int64_t>(r.width) + 1023) / 1024), 256, stream, max_grid,
-                r, partial, splits);
+                r, partial, parts, r.tokens, r.dx, r.dx_stride);
+}
+
+hipError_t launch_loss_weight(const LossProductArgs& a, hipStream_t stream, int64_t max_grid) {
+  const LossRows& r = a.r;
+  return launch(r.bf16 ? parts_kernel<ScaledBf16, false> : parts_kernel<ScaledFp16, false>,
+                a.piece.cols * ((static_cast<int64_t>(r.width) + 1023) / 1024), 256, stream,
+                max_grid, r, a.partial, a.shape.parts, a.piece.cols,
+                a.dw + a.piece.first * a.dw_stride, a.dw_stride);
 }
 
 }  // namespace la

@@ -31,10 +31,11 @@ struct Plan {
   int64_t rows, width;        // padded to whole depths
   int64_t chunks;
   int64_t columns, pieces;    // of a piece; 0 without gradients
-  int64_t splits;
-  bool large_input;
+  la::LossShapes shapes;
+  bool direct;                // dx comes straight from its product
   // places in the workspace
-  int64_t count, index, target, xc, wc, sums, target_logit, lse, losses, piece, partial;
+  int64_t count, index, target, xc, wc, sums, target_logit, lse, losses, piece, input_parts,
+      weight_parts;
   int64_t bytes;
 };
 
@@ -84,17 +85,15 @@ void lay_out(const la_cross_entropy_desc& d, int64_t pieces, Plan* p) {
   // aligned pieces, and a padded copy otherwise
   const int64_t ldw = d.vocab > 1 ? d.weight_row_stride : d.hidden;
   p->pack = p->width != d.hidden || ldw % 8 != 0 || ldw > LA_MAX_SIDE || !aligned(d.weight, 16);
-  const int shift = la::loss_chunk_shift(d.tokens, d.hidden, d.vocab);
-  p->chunks = (d.vocab + (int64_t(1) << shift) - 1) >> shift;
   p->columns = p->gradients ? round_up((d.vocab + pieces - 1) / pieces, la::kPieceUnit) : 0;
   p->pieces = p->gradients ? (d.vocab + p->columns - 1) / p->columns : 0;
-  p->splits = 0;
-  p->large_input = false;
-  if (d.dx != nullptr) {
-    const la::LossSplits splits = la::loss_splits(d.tokens, d.hidden, p->columns);
-    p->splits = splits.parts;
-    p->large_input = splits.large;
-  }
+  p->shapes = la::loss_shapes(d.tokens, d.hidden, d.vocab, std::min(p->columns, d.vocab));
+  const int shift = p->shapes.chunk_shift;
+  p->chunks = (d.vocab + (int64_t(1) << shift) - 1) >> shift;
+  p->direct = p->pieces == 1 && p->shapes.input.parts == 1;
+  const int64_t input_parts = d.dx != nullptr && !p->direct ? p->shapes.input.parts : 0;
+  const int64_t weight_parts =
+      d.dweight != nullptr && p->shapes.weight.parts > 1 ? p->shapes.weight.parts : 0;
   la::Taker take;
   p->count = take(4);
   p->index = take(4 * d.tokens);
@@ -106,7 +105,8 @@ void lay_out(const la_cross_entropy_desc& d, int64_t pieces, Plan* p) {
   p->lse = take(4 * d.tokens);
   p->losses = take(4 * d.tokens);
   p->piece = take(2 * p->rows * p->columns);
-  p->partial = take(4 * p->splits * d.tokens * p->width);
+  p->input_parts = take(4 * input_parts * d.tokens * p->width);
+  p->weight_parts = take(4 * weight_parts * std::min(p->columns, d.vocab) * p->width);
   p->bytes = take.at;
 }
 
@@ -187,7 +187,7 @@ la_status cross_entropy(const la_cross_entropy_desc* d, void* ws, int64_t ws_byt
   r.width = static_cast<int32_t>(p.width);
   r.sums = place<float2>(ws, p.sums);
   r.chunks = static_cast<int32_t>(p.chunks);
-  r.chunk_shift = la::loss_chunk_shift(d->tokens, d->hidden, d->vocab);
+  r.chunk_shift = p.shapes.chunk_shift;
   r.target_logit = place<float>(ws, p.target_logit);
   r.lse = place<float>(ws, p.lse);
   r.losses = d->losses;
@@ -197,9 +197,7 @@ la_status cross_entropy(const la_cross_entropy_desc* d, void* ws, int64_t ws_byt
   r.dx_stride = d->tokens > 1 ? d->dx_row_stride : 0;
   a.w = static_cast<const uint16_t*>(d->weight);
   a.ldw = d->vocab > 1 ? d->weight_row_stride : d->hidden;
-  a.partial = place<float>(ws, p.partial);
-  a.splits = static_cast<int32_t>(p.splits);
-  a.large_input = p.large_input;
+  a.direct = p.direct;
   a.dw = static_cast<uint16_t*>(d->dweight);
   a.dw_stride = d->vocab > 1 ? d->dweight_row_stride : 0;
 
@@ -217,21 +215,24 @@ la_status cross_entropy(const la_cross_entropy_desc* d, void* ws, int64_t ws_byt
     a.piece.ld = static_cast<int32_t>(p.columns);
     a.piece.first = static_cast<int32_t>(first);
     a.piece.cols = static_cast<int32_t>(std::min(columns, d->vocab - first));
-    if (what == LossProduct::kInput)
-      a.depth = static_cast<int32_t>(
-          round_up((a.piece.cols + p.splits - 1) / p.splits, la::kLossDepth));
+    const bool input = what == LossProduct::kInput, weight = what == LossProduct::kWeight;
+    a.shape = input ? p.shapes.input : weight ? p.shapes.weight : p.shapes.logits;
+    a.partial = place<float>(ws, input ? p.input_parts : p.weight_parts);
+    const int64_t sum = input ? a.piece.cols : d->tokens;
+    a.depth = static_cast<int32_t>(
+        round_up(std::max<int64_t>(1, (sum + a.shape.parts - 1) / a.shape.parts), la::kLossDepth));
     return la::launch_loss_product(a, what, stream, max_grid);
   };
   if (!p.gradients) {
     if ((e = product(LossProduct::kSums, 0, d->vocab)) != hipSuccess) return launch_failed(e);
-    if ((e = la::launch_loss_lse(r, stream, max_grid)) != hipSuccess) return launch_failed(e);
-    return ok();
+    e = la::launch_loss_lse(r, true, stream, max_grid);
+    return e == hipSuccess ? ok() : launch_failed(e);
   }
   if (p.pieces > 1 &&
       (e = product(LossProduct::kSums, p.columns, d->vocab)) != hipSuccess)
     return launch_failed(e);
   if ((e = product(LossProduct::kKeep, 0, p.columns)) != hipSuccess) return launch_failed(e);
-  if ((e = la::launch_loss_lse(r, stream, max_grid)) != hipSuccess) return launch_failed(e);
+  if ((e = la::launch_loss_lse(r, false, stream, max_grid)) != hipSuccess) return launch_failed(e);
   e = la::launch_loss_softmax(r, a.piece, stream, max_grid);
   if (e != hipSuccess) return launch_failed(e);
   for (int64_t k = 0; k < p.pieces; ++k) {
@@ -241,12 +242,16 @@ la_status cross_entropy(const la_cross_entropy_desc* d, void* ws, int64_t ws_byt
     a.add = k > 0;
     if (d->dx != nullptr && (e = product(LossProduct::kInput, first, p.columns)) != hipSuccess)
       return launch_failed(e);
-    if (d->dweight != nullptr &&
-        (e = product(LossProduct::kWeight, first, p.columns)) != hipSuccess)
-      return launch_failed(e);
+    if (d->dweight != nullptr) {
+      if ((e = product(LossProduct::kWeight, first, p.columns)) != hipSuccess)
+        return launch_failed(e);
+      if (a.shape.parts > 1 && (e = la::launch_loss_weight(a, stream, max_grid)) != hipSuccess)
+        return launch_failed(e);
+    }
   }
-  if (d->dx != nullptr) {
-    e = la::launch_loss_input(r, a.partial, a.splits, stream, max_grid);
+  if (d->dx != nullptr && !p.direct) {
+    e = la::launch_loss_input(r, place<float>(ws, p.input_parts), p.shapes.input.parts, stream,
+                              max_grid);
     if (e != hipSuccess) return launch_failed(e);
   }
   return ok();

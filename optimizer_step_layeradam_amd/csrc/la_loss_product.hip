@@ -99,7 +99,7 @@ __device__ __forceinline__ void over_lanes(float (&x)[SIDE], F join) {
 // rows on, take different banks. No second copy of w, g or x is ever made.
 
 template <int MT, int NT, int WM, int WN, int BUFFERS>
-struct LossTile {
+struct Tile {
   static constexpr int waves = WM * WN;
   static constexpr int threads = 64 * waves;
   static constexpr int rows = 32 * MT * WM, cols = 32 * NT * WN;
@@ -162,7 +162,7 @@ __device__ __forceinline__ s16x8 fragment(const uint16_t* from, int first, int s
 
 template <typename T, LossProduct WHAT, int MT, int NT, int WM, int WN, int BUFFERS>
 __global__ __launch_bounds__(64 * WM * WN, BUFFERS == 1 ? 4 : BUFFERS == 2 ? 2 : 1) void loss_product_kernel(LossProductArgs a) {
-  using G = LossTile<MT, NT, WM, WN, BUFFERS>;
+  using G = Tile<MT, NT, WM, WN, BUFFERS>;
   constexpr bool INPUT = WHAT == LossProduct::kInput, WEIGHT = WHAT == LossProduct::kWeight;
   constexpr bool PT = WEIGHT, QT = INPUT || WEIGHT;
   constexpr bool LOGITS = !INPUT && !WEIGHT;
@@ -184,16 +184,16 @@ __global__ __launch_bounds__(64 * WM * WN, BUFFERS == 1 ? 4 : BUFFERS == 2 ? 2 :
   const int ldq = WEIGHT ? r.width : static_cast<int>(a.ldw);
   const int tiles_m = (M + G::rows - 1) / G::rows, tiles_n = (N + G::cols - 1) / G::cols;
   const int64_t tiles = static_cast<int64_t>(tiles_m) * tiles_n;
-  const int64_t total = tiles * (INPUT ? a.splits : 1);
+  const int64_t total = tiles * (LOGITS ? 1 : a.shape.parts);
 
   for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
     const int64_t local = xcd_order(w, total);
-    const int split = INPUT ? static_cast<int>(local / tiles) : 0;
+    const int part_of = LOGITS ? 0 : static_cast<int>(local / tiles);
     int ti, tj;
-    rectangle(static_cast<int>(local - split * tiles), tiles_m, tiles_n, ti, tj);
+    rectangle(static_cast<int>(local - part_of * tiles), tiles_m, tiles_n, ti, tj);
     const int row0 = ti * G::rows, col0 = tj * G::cols;
-    const int k0 = INPUT ? split * a.depth : 0;
-    const int depth = LOGITS ? r.width : WEIGHT ? padded : min(a.depth, whole - k0);
+    const int k0 = LOGITS ? 0 : part_of * a.depth;
+    const int depth = LOGITS ? r.width : min(a.depth, (WEIGHT ? padded : whole) - k0);
     const int stages = depth > 0 ? depth / kLossDepth : 0;
 
     // Copies of an operand that is contiguous along the sum: rows past its
@@ -431,9 +431,9 @@ __global__ __launch_bounds__(64 * WM * WN, BUFFERS == 1 ? 4 : BUFFERS == 2 ? 2 :
     static_assert(PASSES % SIDE == 0, "whole passes");
     float* sums = reinterpret_cast<float*>(lds) + wave * (32 * G::at_once * WIDTH);
     const int k8 = (lane % LANES) * 8, col = col0 + wn + k8;
-    const float c_out = WEIGHT ? (r.mean && n > 1 ? r.scale / static_cast<float>(n) : r.scale) /
-                                     (std::is_same<T, Bf16>::value ? 1.0f : kLossScale)
-                               : 0.0f;
+    const float c_out = !LOGITS ? (r.mean && n > 1 ? r.scale / static_cast<float>(n) : r.scale) /
+                                      (std::is_same<T, Bf16>::value ? 1.0f : kLossScale)
+                                : 0.0f;
     const bool edge = col0 + G::cols > N;
     const int chunk = LOGITS ? (a.piece.first + col0 + wn) >> r.chunk_shift : 0;
 #pragma unroll
@@ -461,35 +461,35 @@ __global__ __launch_bounds__(64 * WM * WN, BUFFERS == 1 ? 4 : BUFFERS == 2 ? 2 :
           *reinterpret_cast<f32x4*>(v[u]) = *reinterpret_cast<const f32x4*>(from);
           *reinterpret_cast<f32x4*>(v[u] + 4) = *reinterpret_cast<const f32x4*>(from + 4);
         }
-        if constexpr (INPUT) {
+        if constexpr (!LOGITS) {
+          const bool partial = INPUT ? !a.direct : a.shape.parts > 1;
+          const int64_t rows = INPUT ? r.tokens : M;
 #pragma unroll
           for (int u = 0; u < SIDE; ++u) {
             if (row[u] >= M || col >= r.width) continue;
-            float* to =
-                a.partial + (static_cast<int64_t>(split) * r.tokens + row[u]) * r.width + col;
-            f32x4 lo = *reinterpret_cast<const f32x4*>(v[u]);
-            f32x4 hi = *reinterpret_cast<const f32x4*>(v[u] + 4);
-            if (a.add) {
-              lo += *reinterpret_cast<const f32x4*>(to);
-              hi += *reinterpret_cast<const f32x4*>(to + 4);
+            if (partial) {
+              float* to = a.partial + (part_of * rows + row[u]) * r.width + col;
+              f32x4 lo = *reinterpret_cast<const f32x4*>(v[u]);
+              f32x4 hi = *reinterpret_cast<const f32x4*>(v[u] + 4);
+              if (INPUT && a.add) {
+                lo += *reinterpret_cast<const f32x4*>(to);
+                hi += *reinterpret_cast<const f32x4*>(to + 4);
+              }
+              *reinterpret_cast<f32x4*>(to) = lo;
+              *reinterpret_cast<f32x4*>(to + 4) = hi;
+              continue;
             }
-            *reinterpret_cast<f32x4*>(to) = lo;
-            *reinterpret_cast<f32x4*>(to + 4) = hi;
-          }
-        } else if constexpr (WEIGHT) {
-#pragma unroll
-          for (int u = 0; u < SIDE; ++u) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[u][e] *= c_out;
             const s16x8 o = rounded<T>(v[u]);
-            if (row[u] >= M || col >= N) continue;
-            uint16_t* to = a.dw + (a.piece.first + row[u]) * a.dw_stride + col;
+            uint16_t* to = INPUT ? r.dx + r.index[row[u]] * r.dx_stride
+                                 : a.dw + (a.piece.first + row[u]) * a.dw_stride;
             if (col + 8 <= N) {  // at any element; nothing here reads it again
-              __builtin_nontemporal_store(o, reinterpret_cast<s16x8_anywhere*>(to));
+              __builtin_nontemporal_store(o, reinterpret_cast<s16x8_anywhere*>(to + col));
             } else {
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                if (col + e < N) to[e] = o[e];
+                if (col + e < N) to[col + e] = o[e];
             }
           }
         } else {
@@ -591,13 +591,13 @@ __global__ __launch_bounds__(64 * WM * WN, BUFFERS == 1 ? 4 : BUFFERS == 2 ? 2 :
 
 template <typename T, LossProduct WHAT, int MT, int NT, int WM, int WN, int BUFFERS>
 hipError_t launch_tile(const LossProductArgs& a, hipStream_t stream, int64_t max_grid) {
-  using G = LossTile<MT, NT, WM, WN, BUFFERS>;
+  using G = Tile<MT, NT, WM, WN, BUFFERS>;
   constexpr bool INPUT = WHAT == LossProduct::kInput, WEIGHT = WHAT == LossProduct::kWeight;
   // as many as there would be if every token counted
   const int64_t m = WEIGHT ? a.piece.cols : a.r.tokens;
   const int64_t n = INPUT || WEIGHT ? a.r.hidden : a.piece.cols;
   const int64_t total = ((m + G::rows - 1) / G::rows) * ((n + G::cols - 1) / G::cols) *
-                        (INPUT ? a.splits : 1);
+                        (INPUT || WEIGHT ? a.shape.parts : 1);
   const int64_t grid = std::max<int64_t>(1, std::min({total, kMaxWorkgroups, max_grid}));
   LossProductArgs copy = a;
   void* params[] = {&copy};
@@ -606,48 +606,16 @@ hipError_t launch_tile(const LossProductArgs& a, hipStream_t stream, int64_t max
       dim3(static_cast<unsigned>(grid)), dim3(G::threads), params, 0, stream);
 }
 
-// What `tiles` tiles of `stages` stages take, in us. Measured with 32768 words
-// (us, 256 x 256 tiles | 128 x 128): 4096 tokens' logits over hidden 512 212 |
-// 176, 1024 310 | 303, 4096 904 | 1082; 256 tokens' over 4096 101 | 95; the
-// weight's gradient at 4096 columns from 256 tokens 123 | 100, 1024 309 | 306,
-// 4096 845 | 1037, at 128 columns from 4096 tokens 88 | 95. The small tile has one
-// buffer alone, and four workgroups a compute unit that take turns (with two or
-// four buffers and fewer workgroups every one of these took as long or longer).
-double time_of(bool large, int64_t tiles, int64_t stages) {
-  const double s = static_cast<double>(stages);
-  const int64_t each = (tiles + 255) / 256;  // of a compute unit
-  if (large) return static_cast<double>(each) * (14.0 + 1.55 * s);
-  const int64_t rest = each % 4;
-  return static_cast<double>(each / 4) * (5.4 + 2.04 * s) +
-         (rest > 0 ? 2.5 + s * (1.2 + 0.21 * static_cast<double>(rest)) : 0.0);
-}
-
-bool large_tiles(int64_t m, int64_t n, int64_t depth) {
-  auto tiles = [&](int64_t side) { return ((m + side - 1) / side) * ((n + side - 1) / side); };
-  const int64_t stages = (depth + kLossDepth - 1) / kLossDepth;
-  return time_of(true, tiles(256), stages) < time_of(false, tiles(128), stages);
-}
-
-// Up to this many tokens the weight's traffic decides: tiles of 32 or 64 rows
-// by 128 columns, two workgroups a compute unit, whose copies of the weight pass by
-// the caches (24 tokens x 4096 x 128000, 1.05 GB: logits 198 us, and 262 us through
-// them).
-constexpr int kFewTokens = 64, kFewestTokens = 32;
-
 template <typename T, LossProduct WHAT>
 hipError_t launch_one(const LossProductArgs& a, hipStream_t stream, int64_t max_grid) {
-  if constexpr (WHAT != LossProduct::kWeight) {
-    if (a.r.tokens <= kFewestTokens)
+  if constexpr (WHAT != LossProduct::kWeight) {  // turned rows of g are 128 columns at least
+    if (a.shape.tile == LossTile::kSmallest)
       return launch_tile<T, WHAT, 1, 2, 1, 2, 4>(a, stream, max_grid);
-    if (a.r.tokens <= kFewTokens)
+    if (a.shape.tile == LossTile::kSmall)
       return launch_tile<T, WHAT, 1, 2, 2, 2, 3>(a, stream, max_grid);
   }
-  const bool large = WHAT == LossProduct::kInput ? a.large_input != 0
-                     : WHAT == LossProduct::kWeight
-                         ? large_tiles(a.piece.cols, a.r.hidden, a.r.tokens)
-                         : a.r.chunk_shift == 7;
-  return large ? launch_tile<T, WHAT, 4, 4, 2, 2, 5>(a, stream, max_grid)
-               : launch_tile<T, WHAT, 2, 2, 2, 2, 1>(a, stream, max_grid);
+  return a.shape.tile == LossTile::kLarge ? launch_tile<T, WHAT, 4, 4, 2, 2, 5>(a, stream, max_grid)
+                                          : launch_tile<T, WHAT, 2, 2, 2, 2, 1>(a, stream, max_grid);
 }
 
 template <typename T>
@@ -664,32 +632,89 @@ hipError_t launch_type(const LossProductArgs& a, LossProduct what, hipStream_t s
 
 }  // namespace
 
-int loss_chunk_shift(int64_t tokens, int64_t hidden, int64_t vocab) {
-  return tokens > kFewTokens && large_tiles(tokens, vocab, hidden) ? 7 : 6;
+namespace {
+
+int64_t tiles_of(LossTile tile, int64_t m, int64_t n) {
+  const int64_t rows = tile == LossTile::kLarge ? 256 : tile == LossTile::kMedium ? 128 : 64;
+  const int64_t cols = tile == LossTile::kLarge ? 256 : 128;
+  return ((m + rows - 1) / rows) * ((n + cols - 1) / cols);
 }
 
-LossSplits loss_splits(int64_t tokens, int64_t hidden, int64_t columns) {
-  // parts of at least 1024 columns
-  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(64, columns / 1024));
-  if (tokens <= kFewTokens) {
-    const int64_t tiles = (hidden + 127) / 128;
-    return {static_cast<int>(std::min(most, std::max<int64_t>(1, 512 / tiles))), false};
+// What `tiles` tiles of `stages` stages take, in us, from these measurements (us,
+// 256 x 256 | 128 x 128 | 64 x 128):
+//   logits of 4096 tokens, 32768 words, hidden 512    212 |  176 |
+//                                       hidden 4096   904 | 1082 |
+//             256                       hidden 4096   101 |   95 |
+//             512 tokens, 8000 words, hidden 4096         |   65 |  62
+//            2048                     hidden  512         |   26 |  40
+//            2048 tokens, 1000 words, hidden 4096         |   62 |  39
+//             512                     hidden 1024         |   19 |  11
+//   the weight's gradient, 4096 columns of 32768 words, from
+//             256 tokens                              123 |  100 |
+//            4096                                     845 | 1037 |
+// The medium tile has one buffer, and four workgroups a compute unit that take
+// turns (with two or four buffers and fewer workgroups all of these took as long
+// or longer), the small one three and two workgroups: it is the one for few tiles,
+// which nothing else hides the copies of.
+double time_of(LossTile tile, int64_t tiles, int64_t stages) {
+  const double s = static_cast<double>(stages);
+  const int64_t each = (tiles + 255) / 256;  // of a compute unit
+  if (tile == LossTile::kLarge) return static_cast<double>(each) * (14.0 + 1.55 * s);
+  if (tile == LossTile::kMedium) {
+    const int64_t rest = each % 4;
+    return static_cast<double>(each / 4) * (5.4 + 2.04 * s) +
+           (rest > 0 ? 2.5 + s * (1.2 + 0.21 * static_cast<double>(rest)) : 0.0);
   }
-  LossSplits best = {1, false};
-  double least = 0.0;
-  for (int large = 0; large < 2; ++large)
+  return static_cast<double>(each / 2) * (2.5 + 0.95 * s) +
+         static_cast<double>(each % 2) * (2.5 + 0.4 * s);
+}
+
+// The tile and parts that take least for an m x n product over `depth`. `least`:
+// elements of a part at least; 0: one part.
+LossShape shape_of(int64_t m, int64_t n, int64_t depth, int64_t least, bool small) {
+  LossShape best = {LossTile::kMedium, 1};
+  double time = 0.0;
+  const int64_t most = least > 0 ? std::max<int64_t>(1, std::min<int64_t>(64, depth / least)) : 1;
+  for (LossTile tile : {LossTile::kSmall, LossTile::kMedium, LossTile::kLarge}) {
+    if (tile == LossTile::kSmall && !small) continue;
     for (int64_t k = 1; k <= most; ++k) {
-      const int64_t side = large ? 256 : 128;
-      const int64_t tiles = ((tokens + side - 1) / side) * ((hidden + side - 1) / side) * k;
-      // a part's binary32 results are written and read, at 5 TB/s
-      const double time = time_of(large, tiles, (columns / k + kLossDepth - 1) / kLossDepth) +
-                          static_cast<double>(k * tokens * hidden) * 8.0 / 5e6;
-      if (least == 0.0 || time < 0.99 * least) {
-        least = time;
-        best = {static_cast<int>(k), large != 0};
+      const int64_t stages = (depth + kLossDepth * k - 1) / (kLossDepth * k);
+      double t = time_of(tile, tiles_of(tile, m, n) * k, stages);
+      // parts' binary32 results are written and read, at 5 TB/s, by a launch more
+      if (k > 1) t += 4.0 + static_cast<double>(k * m * n) * 8.0 / 5e6;
+      if (time == 0.0 || t < 0.99 * time) {
+        time = t;
+        best = {tile, static_cast<int32_t>(k)};
       }
     }
+  }
   return best;
+}
+
+}  // namespace
+
+// Up to this many tokens the weight's traffic decides: tiles of 32 or 64 rows by
+// 128 columns, whose copies of the weight pass by the caches (24 tokens x 4096 x
+// 128000, 1.05 GB: logits 198 us, and 262 us through them).
+constexpr int64_t kFewTokens = 64, kFewestTokens = 32;
+
+LossShapes loss_shapes(int64_t tokens, int64_t hidden, int64_t vocab, int64_t columns) {
+  LossShapes s = {};
+  tokens = std::max<int64_t>(1, tokens);
+  if (tokens <= kFewTokens) {
+    const LossTile tile = tokens <= kFewestTokens ? LossTile::kSmallest : LossTile::kSmall;
+    const int64_t tiles = (hidden + 127) / 128;
+    // parts for two workgroups a compute unit, of at least 512 columns
+    const int64_t parts = std::max<int64_t>(1, std::min({columns / 512, 512 / tiles, int64_t(64)}));
+    s.logits = {tile, 1};
+    s.input = {tile, static_cast<int32_t>(parts)};
+  } else {
+    s.logits = shape_of(tokens, vocab, hidden, 0, true);
+    s.input = shape_of(tokens, hidden, columns, 512, true);
+  }
+  s.weight = shape_of(columns, hidden, tokens, 512, false);
+  s.chunk_shift = s.logits.tile == LossTile::kLarge ? 7 : 6;
+  return s;
 }
 
 hipError_t launch_loss_product(const LossProductArgs& a, LossProduct what, hipStream_t stream,
