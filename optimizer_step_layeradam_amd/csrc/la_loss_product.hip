@@ -274,17 +274,16 @@ __global__ __launch_bounds__(64 * WM * WN, BUFFERS == 1 ? 4 : BUFFERS == 2 ? 2 :
     // What the wave's rows have, a lane to a row.
     struct {
       int target[MT > 2 ? 2 : 1];
-      float lse[MT > 2 ? 2 : 1], loss[MT > 2 ? 2 : 1];
+      float lse[MT > 2 ? 2 : 1];
     } mine = {};
-    if constexpr (LOGITS) {
+    // (kAgain in one buffer, where registers are short, reads them when it needs them.)
+    constexpr bool MINE = LOGITS && !(WHAT == LossProduct::kAgain && BUFFERS == 1);
+    if constexpr (MINE) {
 #pragma unroll
       for (int i = 0; i < (MT > 2 ? 2 : 1); ++i) {
         const int row = min(row0 + wm + 64 * i + lane, M - 1);
         mine.target[i] = r.target[row];
-        if constexpr (WHAT == LossProduct::kAgain) {
-          mine.lse[i] = r.lse[row];
-          mine.loss[i] = r.compact_losses[row];
-        }
+        if constexpr (WHAT == LossProduct::kAgain) mine.lse[i] = r.lse[row];
       }
     }
     f32x16 acc[MT][NT] = {};
@@ -426,8 +425,10 @@ __global__ __launch_bounds__(64 * WM * WN, BUFFERS == 1 ? 4 : BUFFERS == 2 ? 2 :
     // their own.
     constexpr int WIDTH = 32 * NT, LANES = WIDTH / 8, TOGETHER = 64 / LANES;
     // rows of a lane that are worked on side by side: alone, a row is a chain of
-    // exchanges that the wave would wait for
-    constexpr int SIDE = 4, PASSES = 32 * G::at_once / TOGETHER;
+    // exchanges that the wave would wait for (fewer where four workgroups share the
+    // registers)
+    constexpr int SIDE = !LOGITS || BUFFERS > 1 ? 4 : 2;
+    constexpr int PASSES = 32 * G::at_once / TOGETHER;
     static_assert(PASSES % SIDE == 0, "whole passes");
     float* sums = reinterpret_cast<float*>(lds) + wave * (32 * G::at_once * WIDTH);
     const int k8 = (lane % LANES) * 8, col = col0 + wn + k8;
@@ -494,25 +495,29 @@ __global__ __launch_bounds__(64 * WM * WN, BUFFERS == 1 ? 4 : BUFFERS == 2 ? 2 :
           }
         } else {
           int own[SIDE];      // the target's place among the lane's columns
-          float lse[SIDE], loss[SIDE];
+          float lse[SIDE];
 #pragma unroll
           for (int u = 0; u < SIDE; ++u) {
-            // lanes hold what belongs to the wave's rows
             const int at = row[u] - row0 - wm;
-            own[u] = __shfl(mine.target[0], at & 63, 64);
-            if constexpr (MT == 4) {
-              const int other = __shfl(mine.target[1], at & 63, 64);
-              own[u] = at < 64 ? own[u] : other;
+            if constexpr (MINE) {
+              own[u] = __shfl(mine.target[0], at & 63, 64);
+              if constexpr (MT == 4) {
+                const int other = __shfl(mine.target[1], at & 63, 64);
+                own[u] = at < 64 ? own[u] : other;
+              }
+            } else {
+              own[u] = r.target[min(row[u], M - 1)];
             }
             own[u] -= a.piece.first + col;
             if constexpr (WHAT == LossProduct::kAgain) {
-              lse[u] = __shfl(mine.lse[0], at & 63, 64);
-              loss[u] = __shfl(mine.loss[0], at & 63, 64);
-              if constexpr (MT == 4) {
-                const float other = __shfl(mine.lse[1], at & 63, 64);
-                const float another = __shfl(mine.loss[1], at & 63, 64);
-                lse[u] = at < 64 ? lse[u] : other;
-                loss[u] = at < 64 ? loss[u] : another;
+              if constexpr (MINE) {
+                lse[u] = __shfl(mine.lse[0], at & 63, 64);
+                if constexpr (MT == 4) {
+                  const float other = __shfl(mine.lse[1], at & 63, 64);
+                  lse[u] = at < 64 ? lse[u] : other;
+                }
+              } else {
+                lse[u] = r.lse[min(row[u], M - 1)];
               }
             }
             if (edge) {  // columns behind the piece count as exp(-inf)
@@ -526,7 +531,8 @@ __global__ __launch_bounds__(64 * WM * WN, BUFFERS == 1 ? 4 : BUFFERS == 2 ? 2 :
             for (int u = 0; u < SIDE; ++u) {
               constexpr float scale = std::is_same<T, Bf16>::value ? 1.0f : kLossScale;
               float at_target = 0.0f;
-              if (own[u] >= 0 && own[u] < 8) at_target = scale * expm1f(-loss[u]);
+              if (own[u] >= 0 && own[u] < 8 && row[u] < M)
+                at_target = scale * expm1f(-r.compact_losses[row[u]]);
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 v[u][e] = scale * __builtin_amdgcn_exp2f(__builtin_fmaf(v[u][e], kLog2e, -lse[u]));
