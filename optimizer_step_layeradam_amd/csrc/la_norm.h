@@ -33,15 +33,17 @@ struct NormArgs {
   float eps, inverse_cols;
 };
 
-// Rows up to this many bytes are held in a workgroup's registers.
+// Rows up to this many bytes are held in registers beside what their columns
+// need, up to this many elements alone in those of 1024 lanes.
 constexpr int kNormRegisterBytes = 32768;
+constexpr int kNormWideCols = 32768;
 
 // The backward pass' parts: how many sums over rows are formed side by side,
 // and of how many rows each.
 void norm_parts(int64_t rows, int64_t cols, int type, int32_t* parts, int32_t* rows_per_part);
 
 hipError_t launch_norm_forward(const NormArgs& a, hipStream_t stream, int64_t max_grid);
-// The backward pass over rows that fit registers, by element type.
+// The backward pass over rows of up to kNormWideCols elements, by their type.
 hipError_t norm_backward_bf16(const NormArgs& a, hipStream_t stream, int64_t max_grid);
 hipError_t norm_backward_fp16(const NormArgs& a, hipStream_t stream, int64_t max_grid);
 hipError_t norm_backward_fp32(const NormArgs& a, hipStream_t stream, int64_t max_grid);

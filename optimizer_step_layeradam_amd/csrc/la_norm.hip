@@ -109,6 +109,91 @@ __global__ __launch_bounds__(threads_of<G>()) void forward_kernel(NormArgs a) {
   }
 }
 
+// Rows that fill the registers of 1024 lanes: these hold the row alone, as it
+// comes from memory, and the parameters are read where they are needed (from L2).
+// What overlaps a row's sums with other rows' loads is a second workgroup.
+template <typename T, int P, Ends ENDS>
+__global__ __launch_bounds__(1024, P <= 4 ? 8 : 4) void forward_wide_kernel(NormArgs a) {
+  constexpr int N = Vector<T>::n, G = 1024;
+  __shared__ float part[2][1][G / 64];
+  RowSum<G, 1> row_sum{part};
+  const int lane = threadIdx.x;
+  for (int row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const typename T::bits* x = row_of<T, true>(a.x, row, a.inner);
+    u32x4_bits v[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) v[p] = load_raw<T, ENDS>(x, (p * G + lane) * N, a.cols);
+    if (a.residual.p != nullptr) {
+      const typename T::bits* r = row_of<T, true>(a.residual, row, a.inner);
+      typename T::bits* sum = row_of<T, true>(a.sum, row, a.inner);
+      u32x4_bits u[P];
+#pragma unroll
+      for (int p = 0; p < P; ++p) u[p] = load_raw<T, ENDS>(r, (p * G + lane) * N, a.cols);
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const int at = formed_again((p * G + lane) * N);
+        const Vector<T> xv = settled<T, ENDS>(v[p], at, a.cols), rv = settled<T, ENDS>(u[p], at, a.cols);
+        float o[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] = T::decode(xv.e[i]) + T::decode(rv.e[i]);
+        const Vector<T> s = encode_vector<T>(o);
+        store_vector<T>(sum, at, a.cols, s);
+        v[p] = __builtin_bit_cast(u32x4_bits, s);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    } else {
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+        v[p] = __builtin_bit_cast(
+            u32x4_bits, settled<T, ENDS>(v[p], formed_again((p * G + lane) * N), a.cols));
+    }
+    float mean = 0.0f, t[1] = {0.0f};
+    if (a.layer) {
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const Vector<T> s = __builtin_bit_cast(Vector<T>, v[p]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) t[0] += T::decode(s.e[i]);  // zeros past the row
+      }
+      row_sum(t);
+      mean = t[0] * a.inverse_cols;
+    }
+    t[0] = 0.0f;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int at = formed_again((p * G + lane) * N);
+      asm("" : "+v"(v[p]));  // decoded again each time: kept, it would be twice the registers
+      const Vector<T> s = __builtin_bit_cast(Vector<T>, v[p]);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float d = at + i < a.cols ? T::decode(s.e[i]) - mean : 0.0f;
+        t[0] = __builtin_fmaf(d, d, t[0]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    row_sum(t);
+    const float rstd = 1.0f / __builtin_sqrtf(t[0] * a.inverse_cols + a.eps);
+    if (lane == 0) {
+      if (a.layer && a.mean != nullptr) a.mean[row] = mean;
+      if (a.rstd != nullptr) a.rstd[row] = rstd;
+    }
+    typename T::bits* y = row_of<T, true>(a.y, row, a.inner);
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int at = formed_again((p * G + lane) * N);
+      float w[N], b[N], o[N];
+      load_parameter<ENDS>(w, a.weight, a.weight_type, at, a.cols, 1.0f);
+      load_parameter<ENDS>(b, a.bias, a.weight_type, at, a.cols, 0.0f);
+      asm("" : "+v"(v[p]));
+      const Vector<T> s = __builtin_bit_cast(Vector<T>, v[p]);
+#pragma unroll
+      for (int i = 0; i < N; ++i) o[i] = __builtin_fmaf((T::decode(s.e[i]) - mean) * rstd, w[i], b[i]);
+      store_vector<T>(y, at, a.cols, encode_vector<T>(o));
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+}
+
 // Rows too long for registers: a workgroup reads its row once more for each
 // sum and for the result (from L2 while it holds them).
 constexpr int kLongThreads = 1024;
@@ -248,7 +333,8 @@ __global__ __launch_bounds__(256) void backward_long_kernel(NormArgs a) {
   }
 }
 
-// The parts of a column added up: 32 columns and 32 chains a workgroup.
+// The parts of a column added up: 32 columns and 32 chains a workgroup, whose
+// sums 32 lanes then exchange.
 __global__ __launch_bounds__(1024) void reduce_kernel(NormArgs a) {
   __shared__ float lds[32][33];
   const int c = threadIdx.x & 31, chain = threadIdx.x >> 5;
@@ -257,18 +343,18 @@ __global__ __launch_bounds__(1024) void reduce_kernel(NormArgs a) {
     const bool bias = k >= blocks;
     void* to = bias ? a.dbias : a.dweight;
     if (to == nullptr) continue;
-    const int col = (k - (bias ? blocks : 0)) * 32 + c;
+    const int first = (k - (bias ? blocks : 0)) * 32, col = first + c;
     const float* from = a.partial + static_cast<int64_t>(bias ? a.parts : 0) * a.cols + col;
     float s = 0.0f;
     if (col < a.cols)
-      #pragma unroll 8
+#pragma unroll 8
       for (int p = chain; p < a.parts; p += 32) s += from[static_cast<int64_t>(p) * a.cols];
     lds[chain][c] = s;
     __syncthreads();
-    if (chain == 0 && col < a.cols) {
-      for (int i = 1; i < 32; ++i) s += lds[i][c];
-      store_parameter(to, a.grad_type, col, s);
-    }
+    s = lds[c][chain];  // lane c of column `chain`
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor(s, d, 64);
+    if (c == 0 && first + chain < a.cols) store_parameter(to, a.grad_type, first + chain, s);
     __syncthreads();
   }
 }
@@ -278,9 +364,15 @@ __global__ __launch_bounds__(1024) void reduce_kernel(NormArgs a) {
 template <typename T>
 hipError_t forward(const NormArgs& a, hipStream_t stream, int64_t max_grid) {
   const int64_t bytes = static_cast<int64_t>(a.cols) * T::bytes;
-  if (bytes > kNormRegisterBytes)
+  if (a.cols > kNormWideCols)
     return launch(reinterpret_cast<const void*>(&forward_long_kernel<T>), a.rows, kLongThreads, a,
                   stream, max_grid);
+  if (bytes > kNormRegisterBytes)
+    return with_wide_shape<T>(bytes, [&](auto p, auto ends) {
+      return launch(reinterpret_cast<const void*>(
+                        &forward_wide_kernel<T, decltype(p)::value, decltype(ends)::value>),
+                    a.rows, 1024, a, stream, max_grid);
+    });
   return with_shape(bytes, [&](auto g, auto p, auto ends) {
     constexpr int G = decltype(g)::value, P = decltype(p)::value, threads = threads_of<G>();
     return launch(reinterpret_cast<const void*>(&forward_kernel<T, G, P, decltype(ends)::value>),
@@ -292,10 +384,8 @@ hipError_t forward(const NormArgs& a, hipStream_t stream, int64_t max_grid) {
 template <typename T>
 hipError_t backward(const NormArgs& a, hipStream_t stream, int64_t max_grid,
                     decltype(norm_backward_fp32)* rows) {
-  const int64_t bytes = static_cast<int64_t>(a.cols) * T::bytes;
-  hipError_t e;
-  if (bytes > kNormRegisterBytes) {
-    e = launch(reinterpret_cast<const void*>(&backward_sums_kernel<T>), a.rows, kLongThreads, a,
+  if (a.cols > kNormWideCols) {
+    const hipError_t e = launch(reinterpret_cast<const void*>(&backward_sums_kernel<T>), a.rows, kLongThreads, a,
                stream, max_grid);
     if (e != hipSuccess) return e;
     const int64_t span = 256 * Vector<T>::n;
@@ -312,19 +402,24 @@ void norm_parts(int64_t rows, int64_t cols, int type, int32_t* parts, int32_t* r
   // As many workgroups as the backward kernel's registers let a compute unit
   // hold, so that each row's loads are under way beside other rows' work, and all
   // of them at once: with a few left over for a second round everything waits for
-  // these. At two vectors a lane three would fit, but 32768 rows of 4096 are 64 to each of
-  // 512 workgroups and 42 or 43 to 768: 171 us and 189. together: rows that a workgroup takes at once.
-  int64_t together = 1, each_unit = 2;
-  if (bytes <= kNormRegisterBytes)
+  // these. At two vectors a lane three would fit, but 32768 rows of 4096 are 64 to
+  // each of 512 workgroups and 42 or 43 to 768: 171 us and 189. Each takes four
+  // rows at least, for the sake of the sum over the parts, but where a row fills a
+  // compute unit: 50 rows of 32768 took 67 us by four and take 25 one by one.
+  int64_t together = 1, each_unit = 2, least = 4;  // together: rows taken at once
+  if (cols > kNormWideCols) {
+  } else if (bytes > kNormRegisterBytes) {
+    each_unit = least = 1;
+  } else {
     with_shape(bytes, [&](auto g, auto p, auto) {
       constexpr int G = decltype(g)::value, P = decltype(p)::value;
       together = threads_of<G>() / G;
       each_unit = G > 256 ? 1 : P == 1 ? 4 : 2;
       return 0;
     });
+  }
   const int64_t most = 256 * each_unit;
-  // and at least four rows to one, for the sake of the sum over the parts
-  const int64_t share = std::max<int64_t>(4, (rows + most - 1) / most);
+  const int64_t share = std::max(least, (rows + most - 1) / most);
   const int64_t each = (share + together - 1) / together * together;
   *rows_per_part = static_cast<int32_t>(each);
   *parts = static_cast<int32_t>((rows + each - 1) / each);

@@ -19,7 +19,9 @@ using la::Range;
 using la::range;
 using la::type_bytes;
 
-constexpr int64_t kMostStride = int64_t(1) << 40;  // keeps every offset far from 64 bits
+// Elements between rows, and of a whole tensor: keep every offset far from 64 bits.
+constexpr int64_t kMostStride = int64_t(1) << 40;
+constexpr double kMostExtent = 0x1p56;
 constexpr int64_t kMostRows = (int64_t(1) << 30);  // row counts and steps past them fit 32 bits
 
 bool is_type(int t) { return t == LA_TYPE_BF16 || t == LA_TYPE_FP16 || t == LA_TYPE_FP32; }
@@ -62,7 +64,10 @@ struct Buffers {
       return;
     }
     const int64_t outer = n.outer > 1 ? t.outer_stride : 0, inner = n.inner > 1 ? t.inner_stride : 0;
-    const bool fits = outer >= 0 && inner >= 0 && outer <= kMostStride && inner <= kMostStride;
+    const bool fits = outer >= 0 && inner >= 0 && outer <= kMostStride && inner <= kMostStride &&
+                      static_cast<double>(n.outer) * static_cast<double>(outer) +
+                              static_cast<double>(n.inner) * static_cast<double>(inner) <=
+                          kMostExtent;
     // rows that are written may not touch: one of the two strides passes over the other's rows
     const bool stacked = (n.inner < 2 || inner >= n.cols) &&
                          (n.outer < 2 || outer >= (n.inner - 1) * inner + n.cols);
@@ -158,7 +163,7 @@ int64_t plan_backward(const la_norm_desc& n, int32_t* parts, int32_t* rows_per_p
   la::norm_parts(rows, n.cols, n.type, parts, rows_per_part);
   la::Taker take;
   *partial = take(2 * 4 * int64_t(*parts) * n.cols);
-  *coefficients = take(n.cols * type_bytes(n.type) > la::kNormRegisterBytes ? 8 * rows : 0);
+  *coefficients = take(n.cols > la::kNormWideCols ? 8 * rows : 0);
   return take.at;
 }
 

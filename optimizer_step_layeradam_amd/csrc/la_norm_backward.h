@@ -19,6 +19,18 @@ struct BackwardRow {
   float rstd, mean;
 };
 
+// Columns [at, at + 4) of a part.
+template <typename V>
+__device__ __forceinline__ void leave_four(float* to, int at, int cols, const V& sums) {
+  if (at + 4 <= cols) {
+    __builtin_memcpy(to + at, &sums, 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (at + i < cols) to[at + i] = sums[i];
+  }
+}
+
 template <typename T, int G, int P, bool BIAS, bool ADDED, Ends ENDS>
 __global__ __launch_bounds__(threads_of<G>()) void backward_kernel(NormArgs a) {
   constexpr int N = Vector<T>::n, threads = threads_of<G>(), groups = threads / G;
@@ -136,8 +148,10 @@ __global__ __launch_bounds__(threads_of<G>()) void backward_kernel(NormArgs a) {
 #pragma unroll
         for (int p = 0; p < P; ++p)
 #pragma unroll
-          for (int i = 0; i < N; ++i)
-            if ((p * G + lane) * N + i < a.cols) to[(p * G + lane) * N + i] = sums[p][i];
+          for (int i = 0; i < N; i += 4) {
+            const float four[4] = {sums[p][i], sums[p][i + 1], sums[p][i + 2], sums[p][i + 3]};
+            leave_four(to, (p * G + lane) * N + i, a.cols, four);
+          }
       }
     };
     if (a.dweight != nullptr) leave(dw, a.partial + static_cast<int64_t>(wg) * a.cols);
@@ -145,18 +159,137 @@ __global__ __launch_bounds__(threads_of<G>()) void backward_kernel(NormArgs a) {
   }
 }
 
+// Rows that fill the registers of 1024 lanes: x and dy as they come from memory
+// and the sums of dy are there, those of dy h in LDS (read and written
+// once a row, by the lane whose columns they are), and w is read twice (from L2).
+template <typename T, int P, bool BIAS, bool ADDED, Ends ENDS>
+__global__ __launch_bounds__(1024) void backward_wide_kernel(NormArgs a) {
+  constexpr int N = Vector<T>::n, G = 1024;
+  typedef float f32x4 __attribute__((ext_vector_type(4)));
+  __shared__ float part[2][2][G / 64];
+  __shared__ f32x4 dw[P * N / 4][G];
+  RowSum<G, 2> row_sum{part};
+  const int lane = threadIdx.x;
+  for (int wg = blockIdx.x; wg < a.parts; wg += gridDim.x) {
+    float db[BIAS ? P : 1][N] = {};
+#pragma unroll
+    for (int i = 0; i < P * N / 4; ++i) dw[i][lane] = f32x4{};
+    const int begin = wg * a.rows_per_part;
+    const int end = begin + min(a.rows_per_part, a.rows - begin);
+    for (int row = begin; row < end; ++row) {
+      const typename T::bits* x = row_of<T, true>(a.x, row, a.inner);
+      const typename T::bits* dy = row_of<T, true>(a.dy, row, a.inner);
+      u32x4_bits xr[P], dr[P];
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const int at = formed_again((p * G + lane) * N);
+        xr[p] = load_raw<T, ENDS>(x, at, a.cols);
+        dr[p] = load_raw<T, ENDS>(dy, at, a.cols);
+      }
+      const float rstd = a.rstd[row], mean = a.layer ? a.mean[row] : 0.0f;
+      float t[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const int at = formed_again((p * G + lane) * N);
+        float w[N];
+        load_parameter<ENDS>(w, a.weight, a.weight_type, at, a.cols, 1.0f);
+        // past the row dy is 0, and with it every term of a sum
+        const Vector<T> xv = settled<T, ENDS>(xr[p], at, a.cols);
+        const Vector<T> dv = settled<T, ENDS>(dr[p], at, a.cols);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float h = (T::decode(xv.e[i]) - mean) * rstd, g = T::decode(dv.e[i]) * w[i];
+          t[0] += g;
+          t[1] = __builtin_fmaf(g, h, t[1]);
+        }
+        __builtin_amdgcn_sched_barrier(0);  // a vector at a time: registers decide
+      }
+      row_sum(t);
+      const float mean_g = a.layer ? t[0] * a.inverse_cols : 0.0f, mean_gh = t[1] * a.inverse_cols;
+      typename T::bits* dx = row_of<T, true>(a.dx, row, a.inner);
+      const typename T::bits* ds = ADDED ? row_of<T, true>(a.dsum, row, a.inner) : nullptr;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const int at = formed_again((p * G + lane) * N);
+        u32x4_bits sr = {};
+        if constexpr (ADDED) sr = load_raw<T, ENDS>(ds, at, a.cols);
+        float w[N];
+        load_parameter<ENDS>(w, a.weight, a.weight_type, at, a.cols, 1.0f);
+        asm("" : "+v"(xr[p]), "+v"(dr[p]));
+        const Vector<T> xv = settled<T, ENDS>(xr[p], at, a.cols);
+        const Vector<T> dv = settled<T, ENDS>(dr[p], at, a.cols);
+        float o[N];
+#pragma unroll
+        for (int j = 0; j < N / 4; ++j) {
+          f32x4 s = dw[p * N / 4 + j][lane];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = 4 * j + e;
+            const float h = (T::decode(xv.e[i]) - mean) * rstd, d = T::decode(dv.e[i]);
+            o[i] = rstd * __builtin_fmaf(-h, mean_gh, d * w[i] - mean_g);
+            s[e] = __builtin_fmaf(d, h, s[e]);
+            if constexpr (BIAS) db[p][i] += d;
+          }
+          dw[p * N / 4 + j][lane] = s;
+        }
+        if constexpr (ADDED) {
+          const Vector<T> sv = settled<T, ENDS>(sr, at, a.cols);
+#pragma unroll
+          for (int i = 0; i < N; ++i) o[i] += T::decode(sv.e[i]);
+        }
+        if (a.dx.p != nullptr) store_vector<T>(dx, at, a.cols, encode_vector<T>(o));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    float* const to = a.partial + static_cast<int64_t>(wg) * a.cols;
+    float* const to_bias = a.partial + static_cast<int64_t>(a.parts + wg) * a.cols;
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      const int at = formed_again((p * G + lane) * N);
+#pragma unroll
+      for (int i = 0; i < N; i += 4) {
+        if (a.dweight != nullptr) leave_four(to, at + i, a.cols, dw[(p * N + i) / 4][lane]);
+        if constexpr (BIAS) {
+          const f32x4 four = {db[p][i], db[p][i + 1], db[p][i + 2], db[p][i + 3]};
+          leave_four(to_bias, at + i, a.cols, four);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+}
+
 template <typename T>
 hipError_t backward_rows(const NormArgs& a, hipStream_t stream, int64_t max_grid) {
-  return with_shape(static_cast<int64_t>(a.cols) * T::bytes, [&](auto g, auto p, auto ends) {
-    constexpr int G = decltype(g)::value, P = decltype(p)::value;
-    constexpr Ends ENDS = decltype(ends)::value;
-    const bool bias = a.dbias != nullptr, added = a.dsum.p != nullptr;
-    const void* kernel =
-        bias ? added ? reinterpret_cast<const void*>(&backward_kernel<T, G, P, true, true, ENDS>)
-                     : reinterpret_cast<const void*>(&backward_kernel<T, G, P, true, false, ENDS>)
-        : added ? reinterpret_cast<const void*>(&backward_kernel<T, G, P, false, true, ENDS>)
-                : reinterpret_cast<const void*>(&backward_kernel<T, G, P, false, false, ENDS>);
-    return launch(kernel, a.parts, threads_of<G>(), a, stream, max_grid);
+  const int64_t bytes = static_cast<int64_t>(a.cols) * T::bytes;
+  const bool bias = a.dbias != nullptr, added = a.dsum.p != nullptr;
+  auto with = [&](auto kernel, int threads) {
+    using std::false_type;
+    using std::true_type;
+    return launch(bias ? added ? kernel(true_type(), true_type()) : kernel(true_type(), false_type())
+                  : added ? kernel(false_type(), true_type())
+                          : kernel(false_type(), false_type()),
+                  a.parts, threads, a, stream, max_grid);
+  };
+  if (bytes > kNormRegisterBytes)
+    return with_wide_shape<T>(bytes, [&](auto p, auto ends) {
+      return with(
+          [&](auto b, auto d) {
+            return reinterpret_cast<const void*>(
+                &backward_wide_kernel<T, decltype(p)::value, decltype(b)::value,
+                                      decltype(d)::value, decltype(ends)::value>);
+          },
+          1024);
+    });
+  return with_shape(bytes, [&](auto g, auto p, auto ends) {
+    constexpr int G = decltype(g)::value;
+    return with(
+        [&](auto b, auto d) {
+          return reinterpret_cast<const void*>(
+              &backward_kernel<T, G, decltype(p)::value, decltype(b)::value, decltype(d)::value,
+                               decltype(ends)::value>);
+        },
+        threads_of<G>());
   });
 }
 

@@ -71,6 +71,14 @@ __device__ __forceinline__ typename T::bits* row_of(const NormRows& t, int row, 
   return p + i * t.outer_stride + (row - i * inner) * t.inner_stride;
 }
 
+// `at`, of which the compiler knows nothing: what follows from it (masks, addresses,
+// a parameter's elements) is formed again where it is needed, and not kept in
+// registers from one row to the next.
+__device__ __forceinline__ int formed_again(int at) {
+  asm volatile("" : "+v"(at));
+  return at;
+}
+
 // Sums of N values over the G lanes that share a row; every one of them gets
 // the result. Within a wave by exchanges; over a workgroup of G lanes the waves'
 // sums meet in LDS, in two places in turn, so that one barrier a time is
@@ -140,6 +148,22 @@ auto with_shape(int64_t bytes, F f) {
   if (bytes <= 1024 * 16) return LA_SHAPE(256, 4);
   return LA_SHAPE(1024, 2);
 #undef LA_SHAPE
+}
+
+// The same for rows of more than kNormRegisterBytes, 1024 lanes to each.
+template <typename T, typename F>
+hipError_t with_wide_shape(int64_t bytes, F f) {
+  using std::integral_constant;
+  auto at = [&](auto p) {
+    return bytes % 16 == 0 ? f(p, integral_constant<Ends, Ends::kWhole>())
+                           : f(p, integral_constant<Ends, Ends::kInside>());
+  };
+  if (bytes <= 3 * 16384) return at(integral_constant<int, 3>());
+  if constexpr (T::bytes == 4) {
+    if (bytes > 6 * 16384) return at(integral_constant<int, 8>());
+    if (bytes > 4 * 16384) return at(integral_constant<int, 6>());
+  }
+  return at(integral_constant<int, 4>());
 }
 
 }  // namespace

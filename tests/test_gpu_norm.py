@@ -65,6 +65,23 @@ def test_against_formulas(rows, cols, dtype, wtype, layer):
     run(x, w, b, layer, 1e-5, dy=dy)
 
 
+# Rows that fill the registers of 1024 lanes, from their shortest to their longest, whole
+# vectors and not; more rows than workgroups, so that each adds rows up.
+@pytest.mark.parametrize("layer", [True, False])
+@pytest.mark.parametrize("added", [False, True])
+@pytest.mark.parametrize("dtype,wtype,rows,cols", [
+    (BF, BF, 3, 24576), (BF, F, 2, 24577), (BF, BF, 2, 32767), (H, H, 3, 32768), (H, F, 2, 16391),
+    (F, F, 2, 8196), (F, H, 3, 12290), (F, F, 2, 16384), (F, BF, 2, 16387), (F, F, 3, 24576),
+    (F, F, 2, 24579), (F, BF, 2, 32766), (F, F, 3, 32768), (BF, BF, 2, 32769), (F, F, 2, 32772),
+    (BF, BF, 517, 16392), (F, F, 300, 8193)])
+def test_wide_rows(dtype, wtype, rows, cols, added, layer):
+    x, r, dy, ds = (inputs(rows, cols, dtype, k).cuda() for k in range(4))
+    w, b = (t.cuda() for t in params(cols, wtype))
+    if not added:
+        r = ds = None
+    run(x, w, b if layer else None, layer, 1e-5, r, dy, ds)
+
+
 @pytest.mark.parametrize("dtype", [BF, H, F])
 @pytest.mark.parametrize("rows,cols", [(5, 100), (3, 2561), (4, 20000)])
 def test_residual(rows, cols, dtype):

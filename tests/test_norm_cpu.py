@@ -142,6 +142,17 @@ def test_refuses_workspaces():
         refuses(status, lambda: la.norm_backward_raw(norm(), backward_io(), ws, size))
 
 
+@host_only
+@pytest.mark.parametrize("outer,inner", [(1 << 30, 1), (1, 1 << 30), (1 << 20, 1 << 10)])
+def test_refuses_tensors_past_any_address(outer, inner):
+    # rows times stride would pass 64 bits, each alone is allowed
+    far = (1 << 40) - 1
+    n = norm(outer=outer, inner=inner, weight=0, bias=0, cols=8)
+    for kw in (dict(x=la.Rows(at(0), far, far)), dict(y=la.Rows(at(2), far, far))):
+        refuses(INVALID, lambda: la.norm_forward_raw(
+            n, forward_io(residual=NONE, sum=NONE, mean=0, rstd=0, **kw)))
+
+
 def test_null_descriptors():
     lib = la.load()
     assert lib.la_norm_forward(None, None, None) == INVALID
