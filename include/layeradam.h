@@ -502,9 +502,10 @@ typedef struct {
   int64_t outer_stride, inner_stride;
 } la_rows;
 
-/* A norm over outer * inner rows of cols (0..LA_MAX_SIDE) elements of `type`;
- * weight and bias have cols contiguous elements of weight_type, NULL standing
- * for ones and zeros. eps: finite and >= 0. */
+/* A norm over outer * inner rows (at most 2^30) of cols (0..LA_MAX_SIDE)
+ * elements of `type`, at most 2^44 in all, strides up to 2^40 and no tensor's
+ * extent past 2^56 elements; weight and bias have cols contiguous elements of
+ * weight_type, NULL standing for ones and zeros. eps: finite as FP32 and >= 0. */
 typedef struct {
   int64_t outer, inner, cols;
   int32_t kind;        /* a la_norm_kind                                     */
@@ -596,7 +597,7 @@ typedef enum { LA_REDUCE_MEAN = 0, LA_REDUCE_SUM = 1 } la_reduction;
 /* x: tokens (0..LA_MAX_SIDE) rows of hidden (1..) elements; weight: vocab (1..)
  * rows; both of `type`, LA_TYPE_BF16 or LA_TYPE_FP16, as dx and dweight. Rows
  * are contiguous, row strides in elements: at least hidden, those of x 0 or
- * more; all buffers are aligned to their element. targets: tokens indices of
+ * more, at most 2^40; all buffers are aligned to their element. targets: tokens indices of
  * target_type. A weight whose rows are not 16-byte aligned, or hidden not a
  * multiple of 64, costs a padded copy of it in the workspace and a pass over
  * it. loss: one FP32; losses: tokens of them, or NULL. dx, dweight: NULL where
@@ -609,7 +610,7 @@ typedef struct {
   int32_t target_type; /* a la_index_type                                    */
   int64_t ignore_index;
   int32_t reduction;   /* a la_reduction                                     */
-  double grad_scale;   /* finite                                             */
+  double grad_scale;   /* finite as FP32                                     */
   float *loss, *losses;
   void *dx, *dweight;
   int64_t dx_row_stride, dweight_row_stride;

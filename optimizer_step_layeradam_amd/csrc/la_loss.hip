@@ -68,7 +68,9 @@ __device__ __forceinline__ void gather_row(const LossRows& r, int row, int t) {
 }
 
 // Rows of x that count, one after the other, zeros behind the last up to a
-// whole depth.
+// whole depth. (A copy, where the products could read through the index: theirs would
+// be scattered rows in every tile. 8192 x 5120: 45 us of 30 ms, 3.7 TB/s; the index
+// before it 11 us.)
 __global__ __launch_bounds__(256) void gather_kernel(LossRows r) {
   const int n = *r.count;
   const int padded = (n + kLossDepth - 1) / kLossDepth * kLossDepth;
@@ -81,7 +83,8 @@ __global__ __launch_bounds__(256) void gather_kernel(LossRows r) {
 
 // Both in one launch where there are few tokens: every workgroup counts all
 // targets, those before its own token apart. Workgroups past the tokens fill
-// the last depth.
+// the last depth. (1 token 3.3 us, 1003 tokens 8.3: all targets are read by each
+// workgroup, from L2. The two launches take 7 and 15 us at 4096.)
 constexpr int kCountedTokens = 2048;
 
 __global__ __launch_bounds__(256) void index_gather_kernel(LossRows r) {
@@ -126,7 +129,8 @@ __global__ __launch_bounds__(256) void index_gather_kernel(LossRows r) {
 }
 
 // A copy of rows whose length or alignment the products cannot read, zeros
-// behind each; four pieces a thread, so that its loads overlap.
+// behind each; four pieces a thread, so that its loads overlap: memory bounds it
+// (50021 x 2049 FP16 67 us, 6.2 TB/s).
 constexpr int kPackPieces = 4;
 
 __global__ __launch_bounds__(256) void pack_kernel(const uint16_t* from, int64_t stride,
@@ -178,7 +182,8 @@ __device__ __forceinline__ S block_sum(S x) {
 
 // The chunks of a row (each its maximum and its sum of exponentials below it)
 // joined to lse. A workgroup takes ROWS rows at a time, 1024 / ROWS threads
-// to each, whose reads are whole lines where ROWS is 16.
+// to each, whose reads are whole lines where ROWS is 16. Latency bounds it: 77 MB of
+// chunks of 8192 tokens and 150000 columns take 21 us, those of one token 4.
 template <int ROWS>
 __global__ __launch_bounds__(1024) void lse_kernel(LossRows r, int sum) {
   constexpr int SHARES = 1024 / ROWS;
@@ -255,7 +260,10 @@ __global__ __launch_bounds__(1024) void sum_kernel(LossRows r) { sum_losses<1024
 // e of the held piece becomes g, in place: 16 rows of 2048 columns a workgroup,
 // whose factors are formed once, in LDS. Eight rows of a thread are asked for before
 // the first is needed. The first workgroup adds the losses up too, in binary64 and
-// in a fixed order.
+// in a fixed order. Memory bounds it, two bytes an element in and two out: 8192 x
+// 150000 0.94 ms, 5.2 TB/s (stores past the caches or more rows a thread: the same).
+// Without it dx and dw would form the exponential anew for each read of g, or
+// the logits be formed twice.
 constexpr int kSoftmaxRows = 16, kSoftmaxCols = 2048;
 
 template <typename T>
@@ -320,6 +328,7 @@ __global__ __launch_bounds__(256) void softmax_kernel(LossRows r, LossPiece piec
 
 // A product's results from the parts of its sum, in order, times c: 1024 columns
 // of a row a workgroup. INPUT: row i is that of the token it was gathered from.
+// Memory bounds it: 8192 x 5120 from one part 75 us, 3.4 TB/s.
 template <typename T, bool INPUT>
 __global__ __launch_bounds__(256) void parts_kernel(LossRows r, const float* partial, int parts,
                                                     int rows, uint16_t* to, int64_t to_stride) {

@@ -53,7 +53,7 @@ la_status check(const la_cross_entropy_desc* d) {
                 "%lld tokens, hidden %lld, vocab %lld: need 0, 1 and 1 to %d of each",
                 static_cast<long long>(d->tokens), static_cast<long long>(d->hidden),
                 static_cast<long long>(d->vocab), LA_MAX_SIDE);
-  if (!std::isfinite(d->grad_scale))
+  if (!std::isfinite(static_cast<float>(d->grad_scale)))
     return fail(LA_ERR_INVALID_ARGUMENT, "grad_scale = %g", d->grad_scale);
   auto stride = [&](int64_t s, int64_t rows, int64_t cols, const char* what) -> la_status {
     if (rows > 1 && (s < cols || s > kMostStride))

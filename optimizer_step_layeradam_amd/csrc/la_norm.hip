@@ -19,6 +19,11 @@ namespace {
 
 // ---- forward --------------------------------------------------------------------------
 
+// G lanes to a row, P vectors of 16 bytes to each, the fewest that hold it, and up to
+// 2048 workgroups that stride over the rows (1024 or 4096: the same). 8192 BF16
+// rows of 5120 with a residual 63 us (5.3 TB/s of 6.6 that a copy reaches), FP32 rows
+// of 2560 32 us (5.3), 163840 of 128 16 us (5.1). Without the next row's loads ahead
+// of this one's sums, and with branches at the row's end, these took half as long again.
 template <typename T, int G, int P, Ends ENDS>
 __global__ __launch_bounds__(threads_of<G>()) void forward_kernel(NormArgs a) {
   constexpr int N = Vector<T>::n, groups = threads_of<G>() / G;
@@ -111,7 +116,9 @@ __global__ __launch_bounds__(threads_of<G>()) void forward_kernel(NormArgs a) {
 
 // Rows that fill the registers of 1024 lanes: these hold the row alone, as it
 // comes from memory, and the parameters are read where they are needed (from L2).
-// What overlaps a row's sums with other rows' loads is a second workgroup.
+// What overlaps a row's sums with other rows' loads is a second workgroup. 4926
+// BF16 rows of 16448 109 us, 3.0 TB/s, where reading the row once a sum took 309; 4000
+// of 32768 122 us (4.3 TB/s) and 444.
 template <typename T, int P, Ends ENDS>
 __global__ __launch_bounds__(1024, P <= 4 ? 8 : 4) void forward_wide_kernel(NormArgs a) {
   constexpr int N = Vector<T>::n, G = 1024;
@@ -195,7 +202,8 @@ __global__ __launch_bounds__(1024, P <= 4 ? 8 : 4) void forward_wide_kernel(Norm
 }
 
 // Rows too long for registers: a workgroup reads its row once more for each
-// sum and for the result (from L2 while it holds them).
+// sum and for the result (from L2 while it holds them: a fifth to a third of what a
+// copy reaches; no hidden size is as long, and the loop serves every length).
 constexpr int kLongThreads = 1024;
 
 template <typename T>
@@ -334,7 +342,8 @@ __global__ __launch_bounds__(256) void backward_long_kernel(NormArgs a) {
 }
 
 // The parts of a column added up: 32 columns and 32 chains a workgroup, whose
-// sums 32 lanes then exchange.
+// sums 32 lanes then exchange. Latency bounds it: 4 to 5 us for 512 parts of 4096
+// columns (8 MB), as for two of 1027.
 __global__ __launch_bounds__(1024) void reduce_kernel(NormArgs a) {
   __shared__ float lds[32][33];
   const int c = threadIdx.x & 31, chain = threadIdx.x >> 5;

@@ -40,7 +40,7 @@ la_status check_norm(const la_norm_desc* n) {
     return fail(LA_ERR_INVALID_ARGUMENT, "%lld x %lld rows of %lld elements: at most 2^30 rows of %d, 2^44 elements",
                 static_cast<long long>(n->outer), static_cast<long long>(n->inner),
                 static_cast<long long>(n->cols), LA_MAX_SIDE);
-  if (!(std::isfinite(n->eps) && n->eps >= 0.0))
+  if (!(std::isfinite(static_cast<float>(n->eps)) && n->eps >= 0.0))
     return fail(LA_ERR_INVALID_ARGUMENT, "eps = %g", n->eps);
   return LA_OK;
 }

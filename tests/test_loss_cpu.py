@@ -69,6 +69,7 @@ def test_struct_has_the_size_of_the_header():
     (dict(tokens=la.MAX_SIDE + 1), INVALID), (dict(vocab=la.MAX_SIDE + 1), INVALID),
     (dict(hidden=la.MAX_SIDE + 1), INVALID),
     (dict(grad_scale=float("nan")), INVALID), (dict(grad_scale=float("inf")), INVALID),
+    (dict(grad_scale=1e39), INVALID), (dict(grad_scale=-1e300), INVALID),
     (dict(x_row_stride=-1), INVALID), (dict(x_row_stride=1 << 41), INVALID),
     (dict(weight_row_stride=H - 1), INVALID), (dict(dx_row_stride=0), INVALID),
     (dict(dweight_row_stride=H - 1), INVALID), (dict(dweight_row_stride=1 << 41), INVALID),

@@ -87,6 +87,7 @@ def test_structs_have_the_sizes_of_the_header():
     (dict(cols=la.MAX_SIDE + 1), INVALID), (dict(outer=1 << 32), INVALID),
     (dict(outer=1 << 30, inner=1 << 30), INVALID),
     (dict(eps=-1e-9), INVALID), (dict(eps=float("nan")), INVALID), (dict(eps=float("inf")), INVALID),
+    (dict(eps=1e39), INVALID),
     (dict(weight=at(10, 2)), MISALIGNED), (dict(bias=at(11, 1)), MISALIGNED),
     (dict(weight=at(2, 8)), ALIASING), (dict(bias=at(3, 8)), ALIASING),
 ])
