@@ -1201,11 +1201,11 @@ def _stream_address(stream, device: int) -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
-def _new_workspace(needed: int, stream, device):
+def _new_workspace(needed: int, stream, like):
     import torch
     if needed < 0:
         raise LayerAdamError(1, last_error())
-    return _new(stream, max(1, needed), torch.uint8, device)
+    return _new(stream, max(1, needed), like, torch.uint8)
 
 
 def _workspace_address(workspace, device: int) -> int:
@@ -1215,13 +1215,13 @@ def _workspace_address(workspace, device: int) -> int:
     return _address(workspace, device)
 
 
-def _new(stream, shape, dtype, device):
-    """A new tensor that belongs to the call's stream."""
+def _new(stream, shape, like, dtype=None):
+    """A new contiguous tensor on like's device that belongs to the call's stream."""
+    if stream is None:  # (1.9 us, torch.empty 2.4: of the smallest calls a twentieth)
+        return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
     import torch
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype or like.dtype)
 
 
 class _RowLayout:
@@ -1291,13 +1291,13 @@ def _norm(kind, x, weight, bias, eps, residual, out, sum_out, stats, stream):
     if sum_out is not None and residual is None:
         raise ValueError("sum_out is the sum of x and a residual: give the residual too")
     if stats is None:
-        stats = _new(stream, (2 if layer else 1, layout.rows), torch.float32, x.device)
+        stats = _new(stream, (2 if layer else 1, layout.rows), x, torch.float32)
     else:
         layout.check_statistics(stats, layer)
     if out is None:
-        out = _new(stream, x.shape, x.dtype, x.device)
+        out = _new(stream, x.shape, x)
     if sum_out is None and residual is not None:
-        sum_out = _new(stream, x.shape, x.dtype, x.device)
+        sum_out = _new(stream, x.shape, x)
     desc = NormDesc(layout.outer, layout.inner, layout.cols, kind, type_, weight_type,
                     layout.parameter(weight, "weight"),
                     layout.parameter(bias, "bias", None if weight is None else weight.dtype),
@@ -1345,13 +1345,13 @@ def _norm_backward(kind, dy, x, weight, stats, residual_grad, dx, dweight, dbias
     weight_type = type_ if weight is None else _element_type(weight, "weight")
     layout.check_statistics(stats, layer)
     if dx is None:
-        dx = _new(stream, x.shape, x.dtype, x.device)
+        dx = _new(stream, x.shape, x)
     given = dweight if dweight is not None else dbias if dbias is not None else weight
     grad_dtype = x.dtype if given is None else given.dtype
     if dweight is None and weight_grad:
-        dweight = _new(stream, layout.cols, grad_dtype, x.device)
+        dweight = _new(stream, layout.cols, x, grad_dtype)
     if dbias is None and bias_grad:
-        dbias = _new(stream, layout.cols, grad_dtype, x.device)
+        dbias = _new(stream, layout.cols, x, grad_dtype)
     if dweight is not None and dbias is not None and dweight.dtype != dbias.dtype:
         raise TypeError(f"dweight and dbias must have one type, got {dweight.dtype} and "
                         f"{dbias.dtype}")
@@ -1364,7 +1364,7 @@ def _norm_backward(kind, dy, x, weight, stats, residual_grad, dx, dweight, dbias
                         layout(dx, "dx"), mean, rstd, layout.parameter(dweight, "dweight"),
                         layout.parameter(dbias, "dbias"), grad_type)
     if workspace is None:
-        workspace = _new_workspace(norm_backward_workspace_bytes_raw(desc), stream, x.device)
+        workspace = _new_workspace(norm_backward_workspace_bytes_raw(desc), stream, x)
     norm_backward_raw(desc, io, _workspace_address(workspace, layout.device), workspace.numel(),
                       _stream_address(stream, layout.device))
     return dx, dweight, dbias
@@ -1479,11 +1479,11 @@ def _cross_entropy(x, weight, targets, ignore_index, reduction, grad_scale, loss
                               not t.is_contiguous()):
             raise ValueError(f"{what} must be a contiguous float32 tensor of {n} elements")
     if loss is None:
-        loss = _new(stream, (), torch.float32, x.device)
+        loss = _new(stream, (), x, torch.float32)
     if dx is None and input_grad:
-        dx = _new(stream, (*lead, hidden), x.dtype, x.device)
+        dx = _new(stream, (*lead, hidden), x)
     if dweight is None and weight_grad:
-        dweight = _new(stream, (vocab, hidden), x.dtype, x.device)
+        dweight = _new(stream, (vocab, hidden), x)
     rows = dx
     if dx is not None:
         if dx.shape != (*lead, hidden):
@@ -1501,8 +1501,7 @@ def _cross_entropy(x, weight, targets, ignore_index, reduction, grad_scale, loss
         _address(rows, device), _address(dweight, device), 0 if rows is None else rows.stride(0),
         0 if dweight is None else dweight.stride(0))
     if workspace is None:
-        workspace = _new_workspace(linear_cross_entropy_workspace_bytes_raw(desc), stream,
-                                   x.device)
+        workspace = _new_workspace(linear_cross_entropy_workspace_bytes_raw(desc), stream, x)
     linear_cross_entropy_raw(desc, _workspace_address(workspace, device), workspace.numel(),
                              _stream_address(stream, device))
     return loss, dx, dweight
