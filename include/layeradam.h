@@ -618,6 +618,7 @@ typedef struct {
 
 /* Workspace of one la_linear_cross_entropy with pieces of at most
  * piece_columns columns, rounded up to a multiple of 256; 0: as many as 4 GiB hold.
+ * That of some number of tokens serves every smaller number too, all else alike.
  * -1 if the descriptor is invalid. Of the pointers only whether dx and dweight
  * are NULL and the alignment of weight is looked at. Host only. */
 LA_API int64_t la_linear_cross_entropy_workspace_bytes(const la_cross_entropy_desc *loss,

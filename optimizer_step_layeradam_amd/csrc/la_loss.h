@@ -98,13 +98,30 @@ struct LossShape {
   int32_t parts;
 };
 
+// What a call's shapes depend on.
+struct LossSizes {
+  int64_t tokens, hidden, vocab;
+  int64_t columns, pieces;  // of a piece; 0: no gradients
+  bool input, weight;       // which of the two
+};
+
 struct LossShapes {
   LossShape logits, input, weight;
   int32_t chunk_shift;      // log2 of the columns of one of `sums`, by the logits' tile
+  double time;              // of the call's products, modelled, us
+  bool held_back;           // some product would take more parts than there is room for
 };
 
-// For pieces of `columns` (0: no gradients).
-LossShapes loss_shapes(int64_t tokens, int64_t hidden, int64_t vocab, int64_t columns);
+// `room`: bytes that binary32 results may take beside those that no call does
+// without (kLeastChunkShift, loss_least_parts).
+LossShapes loss_shapes(const LossSizes& s, int64_t room);
+
+// The shortest chunk of columns that a tile forms has 2^6: `sums` has places for these
+// whatever the tile, so that fewer tokens never need more of a workspace.
+constexpr int kLeastChunkShift = 6;
+
+// Parts of dx that lie in the workspace in any case: its sum over several pieces.
+constexpr int64_t loss_least_parts(const LossSizes& s) { return s.input && s.pieces > 1 ? 1 : 0; }
 
 struct LossProductArgs {
   LossRows r;

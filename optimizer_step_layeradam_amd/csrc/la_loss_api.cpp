@@ -26,11 +26,14 @@ constexpr int64_t kMostStride = int64_t(1) << 40;  // keeps every offset far fro
 // element 16384 tokens of a vocabulary of 131072 in one piece.
 constexpr int64_t kDefaultPieceBytes = int64_t(4) << 30;
 
+constexpr int64_t kUnlimited = int64_t(1) << 62;  // room for parts
+
 struct Plan {
   bool gradients, pack;
   int64_t rows, width;        // padded to whole depths
   int64_t chunks;
   int64_t columns, pieces;    // of a piece; 0 without gradients
+  la::LossSizes sizes;
   la::LossShapes shapes;
   bool direct;                // dx comes straight from its product
   // places in the workspace
@@ -77,7 +80,9 @@ la_status check(const la_cross_entropy_desc* d) {
   return LA_OK;
 }
 
-void lay_out(const la_cross_entropy_desc& d, int64_t pieces, Plan* p) {
+// The layout in `pieces` pieces (or fewer, of the same columns), without its shapes
+// and what depends on them.
+void divide(const la_cross_entropy_desc& d, int64_t pieces, Plan* p) {
   p->gradients = d.dx != nullptr || d.dweight != nullptr;
   p->rows = round_up(d.tokens, la::kLossDepth);
   p->width = round_up(d.hidden, la::kLossDepth);
@@ -87,20 +92,21 @@ void lay_out(const la_cross_entropy_desc& d, int64_t pieces, Plan* p) {
   p->pack = p->width != d.hidden || ldw % 8 != 0 || ldw > LA_MAX_SIDE || !aligned(d.weight, 16);
   p->columns = p->gradients ? round_up((d.vocab + pieces - 1) / pieces, la::kPieceUnit) : 0;
   p->pieces = p->gradients ? (d.vocab + p->columns - 1) / p->columns : 0;
-  p->shapes = la::loss_shapes(d.tokens, d.hidden, d.vocab, std::min(p->columns, d.vocab));
-  const int shift = p->shapes.chunk_shift;
-  p->chunks = (d.vocab + (int64_t(1) << shift) - 1) >> shift;
-  p->direct = p->pieces == 1 && p->shapes.input.parts == 1;
-  const int64_t input_parts = d.dx != nullptr && !p->direct ? p->shapes.input.parts : 0;
-  const int64_t weight_parts =
-      d.dweight != nullptr && p->shapes.weight.parts > 1 ? p->shapes.weight.parts : 0;
+  p->sizes = {d.tokens, d.hidden, d.vocab, p->columns, p->pieces, d.dx != nullptr,
+              d.dweight != nullptr};
+}
+
+// Places for so many parts of dx and dw. (A part's bytes are a multiple of the
+// workspace's alignment, and take nothing else with them.)
+void place_all(const la_cross_entropy_desc& d, int64_t input_parts, int64_t weight_parts, Plan* p) {
+  static_assert(4 * la::kLossDepth % LA_WORKSPACE_ALIGNMENT == 0, "");
   la::Taker take;
   p->count = take(4);
   p->index = take(4 * d.tokens);
   p->target = take(4 * d.tokens);
   p->xc = take(2 * p->rows * p->width);
   p->wc = take(p->pack ? 2 * d.vocab * p->width : 0);
-  p->sums = take(8 * d.tokens * p->chunks);
+  p->sums = take(8 * d.tokens * (round_up(d.vocab, 1 << la::kLeastChunkShift) >> la::kLeastChunkShift));
   p->target_logit = take(4 * d.tokens);
   p->lse = take(4 * d.tokens);
   p->losses = take(4 * d.tokens);
@@ -110,20 +116,69 @@ void lay_out(const la_cross_entropy_desc& d, int64_t pieces, Plan* p) {
   p->bytes = take.at;
 }
 
+// What a call in `pieces` pieces cannot do without.
+int64_t least_bytes(const la_cross_entropy_desc& d, int64_t pieces) {
+  Plan p;
+  divide(d, pieces, &p);
+  place_all(d, la::loss_least_parts(p.sizes), 0, &p);
+  return p.bytes;
+}
+
+// The layout whose parts take `room` bytes at most beside that.
+void lay_out(const la_cross_entropy_desc& d, int64_t pieces, int64_t room, Plan* p) {
+  divide(d, pieces, p);
+  p->shapes = la::loss_shapes(p->sizes, room);
+  const int shift = p->shapes.chunk_shift;
+  p->chunks = (d.vocab + (int64_t(1) << shift) - 1) >> shift;
+  p->direct = p->pieces == 1 && p->shapes.input.parts == 1;
+  place_all(d, d.dx != nullptr && !p->direct ? p->shapes.input.parts : 0,
+            d.dweight != nullptr && p->shapes.weight.parts > 1 ? p->shapes.weight.parts : 0, p);
+}
+
 // The fewest pieces whose columns are at most `columns`, in whole units.
 int64_t pieces_of(const la_cross_entropy_desc& d, int64_t columns) {
   columns = round_up(std::max<int64_t>(1, columns), la::kPieceUnit);
   return (d.vocab + columns - 1) / columns;
 }
 
-// Fewest pieces that the workspace holds; false where it holds none.
+// The smallest workspace that serves: dx over several pieces is summed in it, so that
+// one piece may need less than many.
+int64_t least_of_all(const la_cross_entropy_desc& d) {
+  return std::min(least_bytes(d, 1), least_bytes(d, pieces_of(d, la::kPieceUnit)));
+}
+
+// The fewest pieces that the workspace holds, their parts in what is left of it.
+// Where that is less than they would take, more and smaller pieces may be the
+// faster ones (24 tokens' dx in one part leaves most compute units idle): the least
+// modelled time of all up to the first that is not held back, past 16 of every
+// sixteenth. False where the workspace holds none.
 bool plan_for(const la_cross_entropy_desc& d, int64_t given, Plan* p) {
+  if (given < least_of_all(d)) return false;
   const int64_t most = pieces_of(d, la::kPieceUnit);
-  for (int64_t pieces = 1; pieces <= most; ++pieces) {
-    lay_out(d, pieces, p);
-    if (p->bytes <= given || !p->gradients) return p->bytes <= given;
+  int64_t fewest = 1;
+  if (least_bytes(d, 1) > given) {  // from two pieces on each more needs less
+    int64_t held = most;
+    for (fewest = 2; fewest < held;) {
+      const int64_t middle = (fewest + held) / 2;
+      if (least_bytes(d, middle) <= given) held = middle;
+      else fewest = middle + 1;
+    }
   }
-  return false;
+  lay_out(d, fewest, given - least_bytes(d, fewest), p);
+  if (!p->gradients) return true;
+  Plan next = *p;
+  while (next.shapes.held_back && next.pieces < most) {
+    const int64_t pieces = std::max(next.pieces + 1 + next.pieces / 16,
+                                    pieces_of(d, next.columns - la::kPieceUnit));
+    const int64_t least = least_bytes(d, std::min(pieces, most));
+    if (least > given) {  // one piece may need less than two
+      divide(d, std::min(pieces, most), &next);
+      continue;
+    }
+    lay_out(d, std::min(pieces, most), given - least, &next);
+    if (next.shapes.time < p->shapes.time) *p = next;
+  }
+  return true;
 }
 
 la_status launch_failed(hipError_t e) {
@@ -157,10 +212,7 @@ la_status cross_entropy(const la_cross_entropy_desc* d, void* ws, int64_t ws_byt
     buffer(d->dweight, 2, extent(d->vocab, d->dweight_row_stride), "dweight", written);
   if (st != LA_OK) return st;
   Plan p;
-  if (!plan_for(*d, ws_bytes, &p)) {
-    lay_out(*d, pieces_of(*d, la::kPieceUnit), &p);
-    return la::check_workspace(ws, ws_bytes, p.bytes);
-  }
+  if (!plan_for(*d, ws_bytes, &p)) return la::check_workspace(ws, ws_bytes, least_of_all(*d));
   if ((st = la::check_workspace(ws, ws_bytes, p.bytes)) != LA_OK) return st;
   written.push_back(range(ws, p.bytes, "the workspace"));
   if ((st = la::check_disjoint(written, read)) != LA_OK) return st;
@@ -277,7 +329,7 @@ LA_API int64_t la_linear_cross_entropy_workspace_bytes(const la_cross_entropy_de
                               : std::min<int64_t>(kDefaultPieceBytes / (2 * rows) / la::kPieceUnit * la::kPieceUnit,
                                                   LA_MAX_SIDE);
         Plan p;
-        lay_out(*loss, pieces_of(*loss, columns), &p);
+        lay_out(*loss, pieces_of(*loss, columns), kUnlimited, &p);
         ok();
         return p.bytes;
       },

@@ -683,26 +683,46 @@ double time_of(LossTile tile, int64_t tiles, int64_t stages) {
          static_cast<double>(each % 2) * (2.5 + 0.4 * s);
 }
 
-// The tile and parts that take least for an m x n product over `depth`. `least`:
-// elements of a part at least; 0: one part.
-LossShape shape_of(int64_t m, int64_t n, int64_t depth, int64_t least, bool small) {
-  LossShape best = {LossTile::kMedium, 1};
-  double time = 0.0;
-  const int64_t most = least > 0 ? std::max<int64_t>(1, std::min<int64_t>(64, depth / least)) : 1;
+// A product's shape and its modelled time, and whether it would take more parts
+// than it may.
+struct Choice {
+  LossShape shape;
+  double time;
+  bool held_back;
+};
+
+// The tile and parts, at most `most` of them, that take least for an m x n product
+// over `depth`. `least`: elements of a part at least; 0: one part.
+Choice shape_of(int64_t m, int64_t n, int64_t depth, int64_t least, bool small, int64_t most) {
+  Choice best = {{LossTile::kMedium, 1}, 0.0, false}, any = best;
+  const int64_t sensible =
+      least > 0 ? std::max<int64_t>(1, std::min<int64_t>(64, depth / least)) : 1;
   for (LossTile tile : {LossTile::kSmall, LossTile::kMedium, LossTile::kLarge}) {
     if (tile == LossTile::kSmall && !small) continue;
-    for (int64_t k = 1; k <= most; ++k) {
+    for (int64_t k = 1; k <= sensible; ++k) {
       const int64_t stages = (depth + kLossDepth * k - 1) / (kLossDepth * k);
       double t = time_of(tile, tiles_of(tile, m, n) * k, stages);
       // parts' binary32 results are written and read, at 5 TB/s, by a launch more
       if (k > 1) t += 4.0 + static_cast<double>(k * m * n) * 8.0 / 5e6;
-      if (time == 0.0 || t < 0.99 * time) {
-        time = t;
-        best = {tile, static_cast<int32_t>(k)};
-      }
+      const Choice c = {{tile, static_cast<int32_t>(k)}, t, false};
+      if (any.time == 0.0 || t < 0.99 * any.time) any = c;
+      if (k <= most && (best.time == 0.0 || t < 0.99 * best.time)) best = c;
     }
   }
+  if (any.shape.parts <= most) return any;
+  best.held_back = true;
   return best;
+}
+
+// The same for one to 64 tokens, whose tile is given: two workgroups a compute unit.
+Choice few_shape_of(LossTile tile, int64_t hidden, int64_t columns, int64_t most) {
+  const int64_t tiles = (hidden + 127) / 128;
+  // of at least 512 columns each
+  const int64_t wanted = std::max<int64_t>(1, std::min({columns / 512, 512 / tiles, int64_t(64)}));
+  const int64_t parts = std::min(wanted, most);
+  const int64_t stages = (columns + kLossDepth * parts - 1) / (kLossDepth * parts);
+  return {{tile, static_cast<int32_t>(parts)}, time_of(LossTile::kSmall, tiles * parts, stages),
+          parts < wanted};
 }
 
 }  // namespace
@@ -712,22 +732,42 @@ LossShape shape_of(int64_t m, int64_t n, int64_t depth, int64_t least, bool smal
 // 128000, 1.05 GB: logits 198 us, and 262 us through them).
 constexpr int64_t kFewTokens = 64, kFewestTokens = 32;
 
-LossShapes loss_shapes(int64_t tokens, int64_t hidden, int64_t vocab, int64_t columns) {
+// What a piece costs beside its products, us: their launches.
+constexpr double kPieceTime = 10.0;
+
+LossShapes loss_shapes(const LossSizes& z, int64_t room) {
   LossShapes s = {};
-  tokens = std::max<int64_t>(1, tokens);
+  const int64_t tokens = std::max<int64_t>(1, z.tokens);
+  const int64_t columns = std::min(z.columns, z.vocab);
+  const int64_t row_bytes = 4 * ((z.hidden + kLossDepth - 1) / kLossDepth * kLossDepth);
+  // parts of an output of `rows` rows that there is room for, `kept` of them being there
+  // in any case
+  auto most_of = [&](int64_t rows, int64_t kept) {
+    return std::max<int64_t>(1, kept + room / (rows * row_bytes));
+  };
+  const int64_t kept = loss_least_parts(z);
+  const int64_t most_input = most_of(tokens, kept);
+  Choice logits, input;
   if (tokens <= kFewTokens) {
     const LossTile tile = tokens <= kFewestTokens ? LossTile::kSmallest : LossTile::kSmall;
-    const int64_t tiles = (hidden + 127) / 128;
-    // parts for two workgroups a compute unit, of at least 512 columns
-    const int64_t parts = std::max<int64_t>(1, std::min({columns / 512, 512 / tiles, int64_t(64)}));
-    s.logits = {tile, 1};
-    s.input = {tile, static_cast<int32_t>(parts)};
+    const int64_t stages = (z.hidden + kLossDepth - 1) / kLossDepth;
+    logits = {{tile, 1}, time_of(LossTile::kSmall, (z.vocab + 127) / 128, stages), false};
+    input = few_shape_of(tile, z.hidden, columns, most_input);
   } else {
-    s.logits = shape_of(tokens, vocab, hidden, 0, true);
-    s.input = shape_of(tokens, hidden, columns, 512, true);
+    logits = shape_of(tokens, z.vocab, z.hidden, 0, true, 1);
+    input = shape_of(tokens, z.hidden, columns, 512, true, most_input);
   }
-  s.weight = shape_of(columns, hidden, tokens, 512, false);
-  s.chunk_shift = s.logits.tile == LossTile::kLarge ? 7 : 6;
+  if (z.input && input.shape.parts > 1) room -= (input.shape.parts - kept) * tokens * row_bytes;
+  const Choice weight = shape_of(columns, z.hidden, tokens, 512, false,
+                                 most_of(std::max<int64_t>(1, columns), 0));
+  s.logits = logits.shape;
+  s.input = input.shape;
+  s.weight = weight.shape;
+  s.chunk_shift = s.logits.tile == LossTile::kLarge ? 7 : kLeastChunkShift;
+  const double pieces = static_cast<double>(std::max<int64_t>(1, z.pieces));
+  s.time = logits.time * (2.0 - 1.0 / pieces) +
+           pieces * (kPieceTime + (z.input ? input.time : 0.0) + (z.weight ? weight.time : 0.0));
+  s.held_back = (z.input && input.held_back) || (z.weight && weight.held_back);
   return s;
 }
 
