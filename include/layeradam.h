@@ -617,7 +617,9 @@ typedef struct {
 } la_cross_entropy_desc;
 
 /* Workspace of one la_linear_cross_entropy with pieces of at most
- * piece_columns columns, rounded up to a multiple of 256; 0: as many as 4 GiB hold.
+ * piece_columns columns, rounded up to a multiple of 256 (0: as many as 4 GiB
+ * hold), or of larger ones where these need less: it never grows with smaller
+ * piece_columns.
  * That of some number of tokens serves every smaller number too, all else alike.
  * -1 if the descriptor is invalid. Of the pointers only whether dx and dweight
  * are NULL and the alignment of weight is looked at. Host only. */

@@ -1567,8 +1567,9 @@ def linear_cross_entropy_workspace_bytes(tokens: int, hidden: int, vocab: int, *
                                          weight_grad: bool = True, packed: bool = False) -> int:
     """Bytes of workspace of one linear_cross_entropy_gradients() (without
     either gradient: of one linear_cross_entropy()) that holds pieces of up to
-    piece_columns columns of the vocabulary (default: what 4 GiB hold); it
-    serves any smaller number of tokens too.
+    piece_columns columns of the vocabulary (default: what 4 GiB hold), or
+    larger ones where these need less; it serves any smaller number of tokens
+    too.
     packed: the weight's rows are not 16-byte aligned."""
     desc = make_cross_entropy(
         tokens=tokens, hidden=hidden, vocab=vocab, type=TYPE_BF16, target_type=INDEX_INT64,

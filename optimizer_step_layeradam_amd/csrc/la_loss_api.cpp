@@ -147,6 +147,20 @@ int64_t least_of_all(const la_cross_entropy_desc& d) {
   return std::min(least_bytes(d, 1), least_bytes(d, pieces_of(d, la::kPieceUnit)));
 }
 
+// What a call in up to `pieces` pieces asks for, parts of every size included. Fewer
+// pieces may need less: one takes no sum of dx over pieces, and larger ones fewer parts.
+int64_t wanted_bytes(const la_cross_entropy_desc& d, int64_t pieces) {
+  Plan p;
+  lay_out(d, 1, kUnlimited, &p);
+  int64_t bytes = p.bytes;
+  while (pieces > 1 && least_bytes(d, pieces) < bytes) {  // which grows with fewer pieces
+    lay_out(d, pieces, kUnlimited, &p);
+    bytes = std::min(bytes, p.bytes);
+    pieces = p.pieces - 1;  // the next longer columns
+  }
+  return bytes;
+}
+
 // The fewest pieces that the workspace holds, their parts in what is left of it.
 // Where that is less than they would take, more and smaller pieces may be the
 // faster ones (24 tokens' dx in one part leaves most compute units idle): the least
@@ -328,10 +342,9 @@ LA_API int64_t la_linear_cross_entropy_workspace_bytes(const la_cross_entropy_de
             piece_columns > 0 ? std::min(piece_columns, int64_t(LA_MAX_SIDE))
                               : std::min<int64_t>(kDefaultPieceBytes / (2 * rows) / la::kPieceUnit * la::kPieceUnit,
                                                   LA_MAX_SIDE);
-        Plan p;
-        lay_out(*loss, pieces_of(*loss, columns), kUnlimited, &p);
+        const int64_t bytes = wanted_bytes(*loss, pieces_of(*loss, columns));
         ok();
-        return p.bytes;
+        return bytes;
       },
       -1);
 }

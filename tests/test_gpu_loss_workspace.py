@@ -50,3 +50,14 @@ def test_between_least_and_most(tokens, hidden, vocab):
     for k in range(9):
         size = least + (most - least) * k // 8
         truth.check(*run(x, w, y, size))
+
+
+@pytest.mark.parametrize("dtype", [BF, H])
+def test_large_tiles_in_pieces(dtype):
+    """Products of 256 x 256 tiles over several pieces, the last one shorter: the
+    workspace holds less than the whole matrix."""
+    tokens, hidden, vocab = 2310, 4160, 18000
+    size = 2 * tokens * vocab
+    assert size > la.linear_cross_entropy_workspace_bytes(tokens, hidden, vocab, piece_columns=1)
+    x, w, y = (t.cuda() for t in problem(tokens, hidden, vocab, dtype, 43, 0.1))
+    Truth(x, w, y, mean=False).check(*run(x, w, y, size))

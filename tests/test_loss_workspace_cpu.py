@@ -76,3 +76,17 @@ def test_a_refusal_names_the_least_that_serves(tokens, hidden, vocab):
         assert not takes(tokens, hidden, vocab, less)
     for more in (least + 1, 2 * least, need(tokens, hidden, vocab), 1 << 44):
         assert takes(tokens, hidden, vocab, max(more, least))
+
+
+@pytest.mark.parametrize("tokens,hidden,vocab", [
+    (8192, 8192, 4000), (8192, 5120, 150000), (2310, 4160, 8200), (24, 4096, 128000),
+    (1000, 2048, 30000), (3, 64, 900)])
+def test_smaller_pieces_never_need_more(tokens, hidden, vocab):
+    """And what they need is taken."""
+    columns = sorted({1, 256, 257, 512, 1024, 1280, 2048, 2304, 4000, 4096, 8192, 30000, 50000,
+                      75000, 75008, vocab, 1 << 20})
+    sizes = [need(tokens, hidden, vocab, columns=c) for c in columns]
+    assert sizes == sorted(sizes), list(zip(columns, sizes))
+    least = told(tokens, hidden, vocab, 0)
+    for size in sizes:
+        assert size >= least and takes(tokens, hidden, vocab, size)
