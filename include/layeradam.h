@@ -541,8 +541,8 @@ typedef struct {
 LA_API la_status la_norm_forward(const la_norm_desc *norm, const la_norm_forward_io *io,
                                  void *hip_stream);
 
-/* Workspace of one la_norm_backward; -1 if the descriptor is invalid. Pointers
- * are not looked at. Host only. */
+/* Workspace of one la_norm_backward, which serves every smaller number of rows
+ * too; -1 if the descriptor is invalid. Pointers are not looked at. Host only. */
 LA_API int64_t la_norm_backward_workspace_bytes(const la_norm_desc *norm);
 
 /* Enqueue the backward pass on `hip_stream`: without rows, dweight and dbias

@@ -1401,7 +1401,7 @@ def rms_norm_backward(dy, x, weight, stats, *, residual_grad=None, dx=None, dwei
 
 def norm_backward_workspace_bytes(shape, dtype) -> int:
     """Bytes of workspace of one backward pass over a tensor of this shape and
-    type, of either norm."""
+    type, of either norm; it serves any smaller number of rows too."""
     if dtype not in _element_types():
         raise TypeError(f"dtype must be one of {[str(k) for k in _element_types()]}, got {dtype}")
     rows = 1

@@ -39,8 +39,11 @@ constexpr int kNormRegisterBytes = 32768;
 constexpr int kNormWideCols = 32768;
 
 // The backward pass' parts: how many sums over rows are formed side by side,
-// and of how many rows each.
-void norm_parts(int64_t rows, int64_t cols, int type, int32_t* parts, int32_t* rows_per_part);
+// and of how many rows each; and the most that any call of up to these rows has.
+struct NormParts {
+  int32_t parts, rows_per_part, most;
+};
+NormParts norm_parts(int64_t rows, int64_t cols, int type);
 
 hipError_t launch_norm_forward(const NormArgs& a, hipStream_t stream, int64_t max_grid);
 // The backward pass over rows of up to kNormWideCols elements, by their type.

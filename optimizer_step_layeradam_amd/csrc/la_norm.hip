@@ -406,7 +406,7 @@ hipError_t backward(const NormArgs& a, hipStream_t stream, int64_t max_grid,
 
 }  // namespace
 
-void norm_parts(int64_t rows, int64_t cols, int type, int32_t* parts, int32_t* rows_per_part) {
+NormParts norm_parts(int64_t rows, int64_t cols, int type) {
   const int64_t bytes = cols * (type == kFp32 ? 4 : 2);
   // As many workgroups as the backward kernel's registers let a compute unit
   // hold, so that each row's loads are under way beside other rows' work, and all
@@ -428,10 +428,12 @@ void norm_parts(int64_t rows, int64_t cols, int type, int32_t* parts, int32_t* r
     });
   }
   const int64_t most = 256 * each_unit;
-  const int64_t share = std::max(least, (rows + most - 1) / most);
-  const int64_t each = (share + together - 1) / together * together;
-  *rows_per_part = static_cast<int32_t>(each);
-  *parts = static_cast<int32_t>((rows + each - 1) / each);
+  auto parts_of = [&](int64_t each) { return (rows + each - 1) / each; };
+  const int64_t fewest = (least + together - 1) / together * together;
+  const int64_t share = (parts_of(most) + together - 1) / together * together;
+  const int64_t each = std::max(fewest, share);
+  return {static_cast<int32_t>(parts_of(each)), static_cast<int32_t>(each),
+          static_cast<int32_t>(std::min(most, parts_of(fewest)))};
 }
 
 hipError_t launch_norm_forward(const NormArgs& a, hipStream_t stream, int64_t max_grid) {

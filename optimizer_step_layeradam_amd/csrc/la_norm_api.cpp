@@ -160,9 +160,12 @@ int64_t plan_backward(const la_norm_desc& n, int32_t* parts, int32_t* rows_per_p
   *rows_per_part = 1;
   const int64_t rows = n.outer * n.inner;
   if (n.cols == 0 || rows == 0) return 0;
-  la::norm_parts(rows, n.cols, n.type, parts, rows_per_part);
+  const la::NormParts p = la::norm_parts(rows, n.cols, n.type);
+  *parts = p.parts;
+  *rows_per_part = p.rows_per_part;
   la::Taker take;
-  *partial = take(2 * 4 * int64_t(*parts) * n.cols);
+  // places for the parts of every smaller number of rows too, some of which have more
+  *partial = take(2 * 4 * int64_t(p.most) * n.cols);
   *coefficients = take(n.cols > la::kNormWideCols ? 8 * rows : 0);
   return take.at;
 }
