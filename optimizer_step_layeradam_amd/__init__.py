@@ -1165,7 +1165,9 @@ def _element_type(t, what: str) -> int:
 
 def _one_stride(shape, strides):
     """The stride that takes every index of these axes, in order, to its place
-    (0 where there is one place alone), or None."""
+    (0 where there is one place alone, or none), or None."""
+    if 0 in shape:
+        return 0
     axes = [(n, s) for n, s in zip(shape, strides) if n != 1]
     for (_, s), (m, t) in zip(axes, axes[1:]):
         if s != m * t:
