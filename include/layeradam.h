@@ -535,9 +535,10 @@ typedef struct {
   int32_t grad_type; /* a la_element_type                                    */
 } la_norm_backward_io;
 
-/* Enqueue the forward pass on `hip_stream`. Outputs may not overlap inputs or
- * each other. Every argument is checked on the host before anything is
- * enqueued; on failure nothing is enqueued. */
+/* Enqueue the forward pass on `hip_stream`; without rows, or with cols 0,
+ * nothing is written. Outputs may not overlap inputs or each other. Every
+ * argument is checked on the host before anything is enqueued; on failure
+ * nothing is enqueued. */
 LA_API la_status la_norm_forward(const la_norm_desc *norm, const la_norm_forward_io *io,
                                  void *hip_stream);
 

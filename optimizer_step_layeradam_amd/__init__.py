@@ -1308,6 +1308,9 @@ def _norm(kind, x, weight, bias, eps, residual, out, sum_out, stats, stream):
     norm_forward_raw(desc, NormForwardIO(layout(x, "x"), layout(residual, "residual"),
                                          layout(out, "out"), layout(sum_out, "sum_out"), mean,
                                          rstd), _stream_address(stream, layout.device))
+    if layout.cols == 0:  # the call leaves them alone
+        with torch.cuda.stream(stream):
+            stats.fill_(float("nan"))
     return (out, stats) if residual is None else (out, stats, sum_out)
 
 
@@ -1325,7 +1328,7 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, residual=None, o
     out, sum_out: like x (default: new contiguous ones); they may not overlap
        the inputs.
     stats: a float32 tensor of shape (2, rows), mean and 1 / spread, for the
-       backward pass (default: a new one).
+       backward pass (default: a new one); NaN for rows without elements.
     Returns (out, stats), with a residual (out, stats, sum_out). What the call
     allocates belongs to ``stream``, as for orthogonalize().
     """

@@ -29,3 +29,24 @@ def test_no_rows(lead):
     out, stats = la.rms_norm(x, gamma)
     dx, dgamma = la.rms_norm_backward(out, x, gamma, stats)
     assert dx.shape == x.shape and bool((dgamma == 0).all())
+
+
+@pytest.mark.parametrize("given", [False, True])
+@pytest.mark.parametrize("lead", [(1,), (5,), (2, 3, 4)])
+def test_rows_without_elements(lead, given):
+    """Means over nothing are NaN, and so are the statistics of such rows."""
+    x = torch.empty(*lead, 0, dtype=BF, device="cuda")
+    rows = torch.empty(lead).numel()
+    for f, n in ((la.layer_norm, 2), (la.rms_norm, 1)):
+        stats = torch.full((n, rows), 3.0, device="cuda") if given else None
+        out, got = f(x, stats=stats)
+        assert out.shape == x.shape and got.shape == (n, rows)
+        want = torch.full((n, rows), float("nan"), device="cuda")
+        if n == 2:  # as the plain form has them
+            want[0] = x.float().mean(-1).reshape(-1)
+        assert torch.equal(got.isnan(), want.isnan())
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        _, got = f(x, stream=s)
+        torch.cuda.current_stream().wait_stream(s)
+        assert bool(got.isnan().all())
