@@ -481,8 +481,16 @@ LA_API la_status layer_muon_step(const la_muon_layer_desc *layer, const la_muon_
  *
  * Numerics: everything between the inputs and the outputs is FP32, sums
  * included; each output is rounded once, to the nearest even. The same call
- * with the same inputs gives the same bits. A row that holds an Inf or NaN
- * gives NaN in its own results and in the sums over rows, nowhere else.
+ * with the same inputs gives the same bits.
+ *
+ * What is not finite follows the formulas in FP32, and nothing of a row reaches
+ * another but through the sums over rows. A row that holds a NaN is NaN, and so
+ * is a layer norm's that holds an Inf. An RMS norm's row that holds an Inf has
+ * rstd 0: its y is NaN at the Inf and 0 * weight + bias elsewhere, its dx is NaN, and
+ * dweight in the Inf's columns. A row whose squares about the mean pass FP32's
+ * range (elements of some 1e19 and beyond) has rstd 0 too: y is bias, dx only
+ * residual_grad, and the row adds nothing to dweight; NaN, where the layer norm's
+ * sum passes that range as well.
  *
  * Memory: calls are asynchronous on the given stream, allocate nothing,
  * synchronise nothing and can be captured in a HIP graph; the workspace is as
