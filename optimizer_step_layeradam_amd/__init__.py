@@ -1330,7 +1330,9 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, residual=None, o
     stats: a float32 tensor of shape (2, rows), mean and 1 / spread, for the
        backward pass (default: a new one); NaN for rows without elements.
     Returns (out, stats), with a residual (out, stats, sum_out). What the call
-    allocates belongs to ``stream``, as for orthogonalize().
+    allocates belongs to ``stream``, as for orthogonalize(). Autograd records
+    nothing of it, also where an input requires a gradient: that is
+    layer_norm_backward()'s.
     """
     return _norm(NORM_LAYER, x, weight, bias, eps, residual, out, sum_out, stats, stream)
 
@@ -1541,7 +1543,9 @@ def linear_cross_entropy(x, weight, targets, *, ignore_index: int = -100, reduct
        linear_cross_entropy_workspace_bytes() (default: taken from torch's
        allocator for the call).
     Returns the loss, a tensor; nothing is synchronised. What the call
-    allocates belongs to ``stream``, as for orthogonalize().
+    allocates belongs to ``stream``, as for orthogonalize(). Autograd records
+    nothing of it, also where x or the weight requires a gradient: that is
+    linear_cross_entropy_gradients()'s.
     """
     return _cross_entropy(x, weight, targets, ignore_index, reduction, 1.0, loss, losses, None,
                           None, False, False, workspace, stream)[0]
