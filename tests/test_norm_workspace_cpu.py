@@ -51,3 +51,12 @@ def test_a_size_serves_fewer_rows(cols, dtype):
         least = min(least, size)
         assert takes(rows, cols, dtype, least), (rows, least, size)
         assert not takes(rows, cols, dtype, min(least, size) // 1024)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_rows_past_the_registers_keep_two_numbers_each(dtype):
+    """From 32769 elements on; as many parts as there can be at both row counts."""
+    need = la.norm_backward_workspace_bytes
+    for cols, each in ((8192, 0), (16385, 0), (32768, 0), (32769, 8), (70001, 8)):
+        more = need((204800, cols), dtype) - need((102400, cols), dtype)
+        assert more == each * 102400, (cols, more)
