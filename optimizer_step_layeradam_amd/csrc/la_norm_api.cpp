@@ -68,12 +68,14 @@ struct Buffers {
                       static_cast<double>(n.outer) * static_cast<double>(outer) +
                               static_cast<double>(n.inner) * static_cast<double>(inner) <=
                           kMostExtent;
-    // rows that are written may not touch: one of the two strides passes over the other's rows
-    const bool stacked = (n.inner < 2 || inner >= n.cols) &&
-                         (n.outer < 2 || outer >= (n.inner - 1) * inner + n.cols);
-    const bool beside = (n.outer < 2 || outer >= n.cols) &&
-                        (n.inner < 2 || inner >= (n.outer - 1) * outer + n.cols);
-    if (!fits || (writes && !stacked && !beside)) {
+    // rows that are written may not touch: one of the two strides passes over the other's
+    // rows (looked at where `fits`, which keeps these sums far from 64 bits)
+    auto passes = [&](int64_t over, int64_t rows_over, int64_t within, int64_t rows_within) {
+      return (rows_within < 2 || within >= n.cols) &&
+             (rows_over < 2 || over >= (rows_within - 1) * within + n.cols);
+    };
+    if (!fits || (writes && !passes(outer, n.outer, inner, n.inner) &&
+                  !passes(inner, n.inner, outer, n.outer))) {
       st = fail(LA_ERR_INVALID_ARGUMENT,
                 "strides of %s (outer %lld, inner %lld) for %lld x %lld rows of %lld elements", what,
                 static_cast<long long>(t.outer_stride), static_cast<long long>(t.inner_stride),
