@@ -544,9 +544,10 @@ typedef struct {
 } la_norm_backward_io;
 
 /* Enqueue the forward pass on `hip_stream`; without rows, or with cols 0,
- * nothing is written. Outputs may not overlap inputs or each other. Every
- * argument is checked on the host before anything is enqueued; on failure
- * nothing is enqueued. */
+ * nothing is written. The range from an output's first to its last element, what
+ * lies between its rows included, may not overlap that of an input or of another
+ * output. Every argument is checked on the host before anything is enqueued; on
+ * failure nothing is enqueued. */
 LA_API la_status la_norm_forward(const la_norm_desc *norm, const la_norm_forward_io *io,
                                  void *hip_stream);
 
@@ -607,10 +608,12 @@ typedef enum { LA_REDUCE_MEAN = 0, LA_REDUCE_SUM = 1 } la_reduction;
  * rows; both of `type`, LA_TYPE_BF16 or LA_TYPE_FP16, as dx and dweight. Rows
  * are contiguous, row strides in elements: at least hidden, those of x 0 or
  * more, at most 2^40; all buffers are aligned to their element. targets: tokens indices of
- * target_type. A weight whose rows are not 16-byte aligned, or hidden not a
- * multiple of 64, costs a padded copy of it in the workspace and a pass over
- * it. loss: one FP32; losses: tokens of them, or NULL. dx, dweight: NULL where
- * not wanted. Outputs may not overlap inputs or each other. */
+ * target_type. A weight whose rows are not 16-byte aligned or more than
+ * LA_MAX_SIDE elements apart, or hidden not a multiple of 64, costs a padded copy
+ * of it in the workspace and a pass over it. loss: one FP32; losses: tokens of
+ * them, or NULL. dx, dweight: NULL where not wanted. The range from an output's
+ * first to its last element, what lies between its rows included, may not
+ * overlap that of an input or of another output. */
 typedef struct {
   const void *x, *weight, *targets;
   int64_t tokens, hidden, vocab;

@@ -1325,8 +1325,8 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, residual=None, o
     weight, bias: contiguous vectors of one type out of the three, or None.
     residual: a tensor like x that is added first; the sum, rounded to x's
        type, is what is normalised, and goes to sum_out.
-    out, sum_out: like x (default: new contiguous ones); they may not overlap
-       the inputs.
+    out, sum_out: like x (default: new contiguous ones); the memory from their
+       first to their last element may not overlap that of the inputs.
     stats: a float32 tensor of shape (2, rows), mean and 1 / spread, for the
        backward pass (default: a new one); NaN for rows without elements.
     Returns (out, stats), with a residual (out, stats, sum_out). What the call
@@ -1579,7 +1579,8 @@ def linear_cross_entropy_workspace_bytes(tokens: int, hidden: int, vocab: int, *
     piece_columns columns of the vocabulary (default: what 4 GiB hold), or
     larger ones where these need less; it serves any smaller number of tokens
     too.
-    packed: the weight's rows are not 16-byte aligned."""
+    packed: the weight's rows are not 16-byte aligned, or more than MAX_SIDE
+    elements apart."""
     desc = make_cross_entropy(
         tokens=tokens, hidden=hidden, vocab=vocab, type=TYPE_BF16, target_type=INDEX_INT64,
         reduction=REDUCTIONS["mean"], weight=2 if packed else 0, dx=2 if input_grad else 0,

@@ -328,7 +328,7 @@ __global__ __launch_bounds__(256) void softmax_kernel(LossRows r, LossPiece piec
 
 // A product's results from the parts of its sum, in order, times c: 1024 columns
 // of a row a workgroup. INPUT: row i is that of the token it was gathered from.
-// Memory bounds it: 8192 x 5120 from one part 75 us, 3.4 TB/s.
+// Memory bounds it: 8192 x 5120 from two parts 75 us, 5.6 TB/s.
 template <typename T, bool INPUT>
 __global__ __launch_bounds__(256) void parts_kernel(LossRows r, const float* partial, int parts,
                                                     int rows, uint16_t* to, int64_t to_stride) {
@@ -385,7 +385,8 @@ hipError_t launch_loss_gather(const LossRows& r, hipStream_t stream, int64_t max
 hipError_t launch_pack(const uint16_t* from, int64_t stride, int64_t rows, int cols, uint16_t* to,
                        int width, hipStream_t stream, int64_t max_grid) {
   const int64_t span = 256 * kPackPieces;
-  return launch(pack_kernel, (rows * (width / 8) + span - 1) / span, 256, stream, max_grid, from, stride, rows, cols, to, width);
+  return launch(pack_kernel, (rows * (width / 8) + span - 1) / span, 256, stream, max_grid, from,
+                stride, rows, cols, to, width);
 }
 
 hipError_t launch_loss_lse(const LossRows& r, bool sum, hipStream_t stream, int64_t max_grid) {

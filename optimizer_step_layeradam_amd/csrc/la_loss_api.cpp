@@ -106,7 +106,8 @@ void place_all(const la_cross_entropy_desc& d, int64_t input_parts, int64_t weig
   p->target = take(4 * d.tokens);
   p->xc = take(2 * p->rows * p->width);
   p->wc = take(p->pack ? 2 * d.vocab * p->width : 0);
-  p->sums = take(8 * d.tokens * (round_up(d.vocab, 1 << la::kLeastChunkShift) >> la::kLeastChunkShift));
+  constexpr int64_t chunk = int64_t(1) << la::kLeastChunkShift;
+  p->sums = take(8 * d.tokens * ((d.vocab + chunk - 1) / chunk));
   p->target_logit = take(4 * d.tokens);
   p->lse = take(4 * d.tokens);
   p->losses = take(4 * d.tokens);
@@ -338,10 +339,9 @@ LA_API int64_t la_linear_cross_entropy_workspace_bytes(const la_cross_entropy_de
           return -1;
         }
         const int64_t rows = std::max<int64_t>(1, round_up(loss->tokens, la::kLossDepth));
+        const int64_t held = kDefaultPieceBytes / (2 * rows) / la::kPieceUnit * la::kPieceUnit;
         const int64_t columns =
-            piece_columns > 0 ? std::min(piece_columns, int64_t(LA_MAX_SIDE))
-                              : std::min<int64_t>(kDefaultPieceBytes / (2 * rows) / la::kPieceUnit * la::kPieceUnit,
-                                                  LA_MAX_SIDE);
+            std::min<int64_t>(piece_columns > 0 ? piece_columns : held, LA_MAX_SIDE);
         const int64_t bytes = wanted_bytes(*loss, pieces_of(*loss, columns));
         ok();
         return bytes;

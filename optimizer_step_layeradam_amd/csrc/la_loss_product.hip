@@ -169,7 +169,8 @@ __device__ __forceinline__ s16x8 fragment(const uint16_t* from, int first, int s
 }
 
 template <typename T, LossProduct WHAT, int MT, int NT, int WM, int WN, int BUFFERS>
-__global__ __launch_bounds__(64 * WM * WN, BUFFERS == 1 ? 4 : BUFFERS == 2 ? 2 : 1) void loss_product_kernel(LossProductArgs a) {
+__global__ __launch_bounds__(64 * WM * WN, BUFFERS == 1 ? 4 : BUFFERS == 2 ? 2 : 1)
+    void loss_product_kernel(LossProductArgs a) {
   using G = Tile<MT, NT, WM, WN, BUFFERS>;
   constexpr bool INPUT = WHAT == LossProduct::kInput, WEIGHT = WHAT == LossProduct::kWeight;
   constexpr bool PT = WEIGHT, QT = INPUT || WEIGHT;
@@ -401,29 +402,29 @@ __global__ __launch_bounds__(64 * WM * WN, BUFFERS == 1 ? 4 : BUFFERS == 2 ? 2 :
         }
       } else {
 #pragma unroll
-      for (int k = 0; k < BUFFERS - 1; ++k)
-        if (k < stages) copy(k);
-      if (stages >= BUFFERS - 1) wait_and_meet<G::in_flight>();
-      else wait_and_meet<0>();
-      if (stages > 0) part(f[0], 0, 0);
-      int buffer = 0;
-      for (int k = 0; k < stages; ++k) {
-        const int next = buffer + 1 == BUFFERS ? 0 : buffer + 1;
-        const int last = buffer == 0 ? BUFFERS - 1 : buffer - 1;
-        const bool more = k + BUFFERS - 1 < stages;
-        if (more) copy(last);
-#pragma unroll
-        for (int step = 1; step < kLossDepth / 16; ++step) {
-          part(f[step & 1], buffer, step);
-          multiply(f[(step - 1) & 1]);
-          interleave(None());
-        }
-        if (more) wait_and_meet<G::in_flight>();
+        for (int k = 0; k < BUFFERS - 1; ++k)
+          if (k < stages) copy(k);
+        if (stages >= BUFFERS - 1) wait_and_meet<G::in_flight>();
         else wait_and_meet<0>();
-        if (k + 1 < stages) part(f[0], next, 0);
-        multiply(f[1]);
-        buffer = next;
-      }
+        if (stages > 0) part(f[0], 0, 0);
+        int buffer = 0;
+        for (int k = 0; k < stages; ++k) {
+          const int next = buffer + 1 == BUFFERS ? 0 : buffer + 1;
+          const int last = buffer == 0 ? BUFFERS - 1 : buffer - 1;
+          const bool more = k + BUFFERS - 1 < stages;
+          if (more) copy(last);
+#pragma unroll
+          for (int step = 1; step < kLossDepth / 16; ++step) {
+            part(f[step & 1], buffer, step);
+            multiply(f[(step - 1) & 1]);
+            interleave(None());
+          }
+          if (more) wait_and_meet<G::in_flight>();
+          else wait_and_meet<0>();
+          if (k + 1 < stages) part(f[0], next, 0);
+          multiply(f[1]);
+          buffer = next;
+        }
       }
     }
     // Every wave is past its last read of LDS, and no copy is under way.

@@ -116,7 +116,9 @@ __global__ __launch_bounds__(threads_of<G>()) void forward_kernel(NormArgs a) {
 
 // Rows that fill the registers of 1024 lanes: these hold the row alone, as it
 // comes from memory, and the parameters are read where they are needed (from L2).
-// What overlaps a row's sums with other rows' loads is a second workgroup. 4926
+// What overlaps a row's sums with other rows' loads is a second workgroup, where P is
+// 4 at most. The parameters' type is looked at in the loop over vectors, behind which
+// each of their loads is waited for before the next is asked for: P waits a row. 4926
 // BF16 rows of 16448 109 us, 3.0 TB/s, where reading the row once a sum took 309; 4000
 // of 32768 122 us (4.3 TB/s) and 444.
 template <typename T, int P, Ends ENDS>
@@ -139,7 +141,8 @@ __global__ __launch_bounds__(1024, P <= 4 ? 8 : 4) void forward_wide_kernel(Norm
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         const int at = formed_again((p * G + lane) * N);
-        const Vector<T> xv = settled<T, ENDS>(v[p], at, a.cols), rv = settled<T, ENDS>(u[p], at, a.cols);
+        const Vector<T> xv = settled<T, ENDS>(v[p], at, a.cols);
+        const Vector<T> rv = settled<T, ENDS>(u[p], at, a.cols);
         float o[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) o[i] = T::decode(xv.e[i]) + T::decode(rv.e[i]);
@@ -194,7 +197,8 @@ __global__ __launch_bounds__(1024, P <= 4 ? 8 : 4) void forward_wide_kernel(Norm
       asm("" : "+v"(v[p]));
       const Vector<T> s = __builtin_bit_cast(Vector<T>, v[p]);
 #pragma unroll
-      for (int i = 0; i < N; ++i) o[i] = __builtin_fmaf((T::decode(s.e[i]) - mean) * rstd, w[i], b[i]);
+      for (int i = 0; i < N; ++i)
+        o[i] = __builtin_fmaf((T::decode(s.e[i]) - mean) * rstd, w[i], b[i]);
       store_vector<T>(y, at, a.cols, encode_vector<T>(o));
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -318,9 +322,11 @@ __global__ __launch_bounds__(256) void backward_long_kernel(NormArgs a) {
       const Vector<T> xv = load_vector<T>(row_of<T, true>(a.x, row, a.inner), at, a.cols);
       const Vector<T> dv = load_vector<T>(row_of<T, true>(a.dy, row, a.inner), at, a.cols);
       const float rstd = a.rstd[row], mean = a.layer ? a.mean[row] : 0.0f;
-      const float mean_g = a.coefficients[2 * static_cast<int64_t>(row)], mean_gh = a.coefficients[2 * static_cast<int64_t>(row) + 1];
+      const float* coefficients = a.coefficients + 2 * static_cast<int64_t>(row);
+      const float mean_g = coefficients[0], mean_gh = coefficients[1];
       Vector<T> o, sv = {};
-      if (a.dsum.p != nullptr) sv = load_vector<T>(row_of<T, true>(a.dsum, row, a.inner), at, a.cols);
+      if (a.dsum.p != nullptr)
+        sv = load_vector<T>(row_of<T, true>(a.dsum, row, a.inner), at, a.cols);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const float h = (T::decode(xv.e[i]) - mean) * rstd, d = T::decode(dv.e[i]);
@@ -336,7 +342,8 @@ __global__ __launch_bounds__(256) void backward_long_kernel(NormArgs a) {
     for (int i = 0; i < N; ++i) {
       if (at + i >= a.cols) continue;
       if (a.dweight != nullptr) a.partial[static_cast<int64_t>(wg) * a.cols + at + i] = dw[i];
-      if (a.dbias != nullptr) a.partial[static_cast<int64_t>(a.parts + wg) * a.cols + at + i] = db[i];
+      if (a.dbias != nullptr)
+        a.partial[static_cast<int64_t>(a.parts + wg) * a.cols + at + i] = db[i];
     }
   }
 }
@@ -385,8 +392,9 @@ hipError_t forward(const NormArgs& a, hipStream_t stream, int64_t max_grid) {
   return with_shape(bytes, [&](auto g, auto p, auto ends) {
     constexpr int G = decltype(g)::value, P = decltype(p)::value, threads = threads_of<G>();
     return launch(reinterpret_cast<const void*>(&forward_kernel<T, G, P, decltype(ends)::value>),
-                  std::min<int64_t>((static_cast<int64_t>(a.rows) + threads / G - 1) / (threads / G), 2048), threads, a,
-                  stream, max_grid);
+                  std::min<int64_t>(
+                      (static_cast<int64_t>(a.rows) + threads / G - 1) / (threads / G), 2048),
+                  threads, a, stream, max_grid);
   });
 }
 
@@ -394,12 +402,13 @@ template <typename T>
 hipError_t backward(const NormArgs& a, hipStream_t stream, int64_t max_grid,
                     decltype(norm_backward_fp32)* rows) {
   if (a.cols > kNormWideCols) {
-    const hipError_t e = launch(reinterpret_cast<const void*>(&backward_sums_kernel<T>), a.rows, kLongThreads, a,
-               stream, max_grid);
+    const hipError_t e = launch(reinterpret_cast<const void*>(&backward_sums_kernel<T>), a.rows,
+                                kLongThreads, a, stream, max_grid);
     if (e != hipSuccess) return e;
     const int64_t span = 256 * Vector<T>::n;
     return launch(reinterpret_cast<const void*>(&backward_long_kernel<T>),
-                  static_cast<int64_t>(a.parts) * ((a.cols + span - 1) / span), 256, a, stream, max_grid);
+                  static_cast<int64_t>(a.parts) * ((a.cols + span - 1) / span), 256, a, stream,
+                  max_grid);
   }
   return rows(a, stream, max_grid);
 }
@@ -408,13 +417,16 @@ hipError_t backward(const NormArgs& a, hipStream_t stream, int64_t max_grid,
 
 NormParts norm_parts(int64_t rows, int64_t cols, int type) {
   const int64_t bytes = cols * (type == kFp32 ? 4 : 2);
-  // As many workgroups as the backward kernel's registers let a compute unit
-  // hold, so that each row's loads are under way beside other rows' work, and all
-  // of them at once: with a few left over for a second round everything waits for
-  // these. At two vectors a lane three would fit, but 32768 rows of 4096 are 64 to
-  // each of 512 workgroups and 42 or 43 to 768: 171 us and 189. Each takes four
-  // rows at least, for the sake of the sum over the parts, but where a row fills a
-  // compute unit: 50 rows of 32768 took 67 us by four and take 25 one by one.
+  // A few workgroups to each compute unit, so that each row's loads are under way
+  // beside other rows' work: four, two or one by what a lane holds. That is what the
+  // backward kernel's registers allow at once, but in two places. At two vectors a
+  // lane three would fit, and take longer (32768 rows of 4096: 512 parts 171 us, 768
+  // of them 189; not explained). 16-bit rows of 6145 to 8192 elements take more than 256
+  // registers with a bias or a residual's gradient, or where they end inside a vector,
+  // so that one workgroup fits and the two run one after the other (8192 x 8192 with a
+  // residual's gradient 116 us, 4.6 TB/s, as at 5120). Each takes four rows at least, for
+  // the sake of the sum over the parts, but where a row fills a compute unit: 50 rows of
+  // 32768 took 67 us by four and take 25 one by one.
   int64_t together = 1, each_unit = 2, least = 4;  // together: rows taken at once
   if (cols > kNormWideCols) {
   } else if (bytes > kNormRegisterBytes) {

@@ -37,7 +37,8 @@ la_status check_norm(const la_norm_desc* n) {
   if (n->outer < 0 || n->inner < 0 || n->cols < 0 || n->outer > kMostRows ||
       n->inner > kMostRows || n->outer * n->inner > kMostRows || n->cols > LA_MAX_SIDE ||
       static_cast<double>(n->outer * n->inner) * static_cast<double>(n->cols) > 0x1p44)
-    return fail(LA_ERR_INVALID_ARGUMENT, "%lld x %lld rows of %lld elements: at most 2^30 rows of %d, 2^44 elements",
+    return fail(LA_ERR_INVALID_ARGUMENT,
+                "%lld x %lld rows of %lld elements: at most 2^30 rows of %d, 2^44 elements",
                 static_cast<long long>(n->outer), static_cast<long long>(n->inner),
                 static_cast<long long>(n->cols), LA_MAX_SIDE);
   if (!(std::isfinite(static_cast<float>(n->eps)) && n->eps >= 0.0))
@@ -63,7 +64,8 @@ struct Buffers {
       st = fail(LA_ERR_MISALIGNED, "%s is not aligned to its element", what);
       return;
     }
-    const int64_t outer = n.outer > 1 ? t.outer_stride : 0, inner = n.inner > 1 ? t.inner_stride : 0;
+    const int64_t outer = n.outer > 1 ? t.outer_stride : 0;
+    const int64_t inner = n.inner > 1 ? t.inner_stride : 0;
     const bool fits = outer >= 0 && inner >= 0 && outer <= kMostStride && inner <= kMostStride &&
                       static_cast<double>(n.outer) * static_cast<double>(outer) +
                               static_cast<double>(n.inner) * static_cast<double>(inner) <=

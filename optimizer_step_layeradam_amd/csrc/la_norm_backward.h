@@ -9,7 +9,11 @@
 // Memory bounds it, two or three streams read and one written: 32768 BF16 rows of
 // 4096 161 us (5.0 TB/s), 8192 of 5120 with a residual's gradient 73 (4.6), FP32 rows of 2560
 // 46 (5.5), 163840 of 128 24 (5.2). Registers decide how much of it is under way:
-// h and dy w are formed twice, from the row as it came from memory.
+// h and dy w are formed twice, from the row as it came from memory. Rows of 16 to 32 KB
+// fill 1024 lanes' 128 registers with their columns' sums and the weight beside them:
+// nothing of the next row is under way, and 16-bit ones leave 12 to 92 bytes a lane in
+// scratch, up to 228 where they end inside a vector (8192 x 12288 132 us, 4.6 TB/s, with a
+// residual's gradient and a bias 231, 3.5).
 #pragma once
 
 #include "la_norm_kernels.h"
@@ -169,7 +173,9 @@ __global__ __launch_bounds__(threads_of<G>()) void backward_kernel(NormArgs a) {
 // once a row, by the lane whose columns they are), and w is read twice (from L2).
 // 4926 BF16 rows of 16448 182 us (2.7 TB/s), 4000 of 32768 220 (3.6), where two
 // launches that each read x and dy took 380 and 583; rows of 16 to 32 KB are better off
-// above (8192 of 12288: 145 us, here 202, where nothing of the next row is under way).
+// above (8192 of 12288: 145 us, here 202). As in the forward pass each vector's
+// parameters, and its part of dsum, are waited for before the next vector's are asked
+// for: 2 P to 3 P waits a row.
 template <typename T, int P, bool BIAS, bool ADDED, Ends ENDS>
 __global__ __launch_bounds__(1024) void backward_wide_kernel(NormArgs a) {
   constexpr int N = Vector<T>::n, G = 1024;
