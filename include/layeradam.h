@@ -595,10 +595,11 @@ LA_API la_status la_norm_backward(const la_norm_desc *norm, const la_norm_backwa
  * element. A piece of the whole vocabulary costs three products (6 n hidden
  * vocab flops); where the workspace holds less, the logits of every piece
  * behind the first are formed a second time. The call takes the largest pieces
- * that the workspace given to it holds. Rules as for the orthogonalised
- * update: asynchronous, no allocation, calls that may run at once need a
- * workspace each, every call can be captured in a HIP graph (the targets, and
- * with them n, may change between replays).
+ * that the workspace given to it holds, or smaller ones where these leave room
+ * to cut short or narrow products into more parts and are faster for it. Rules
+ * as for the orthogonalised update: asynchronous, no allocation, calls that may
+ * run at once need a workspace each, every call can be captured in a HIP graph
+ * (the targets, and with them n, may change between replays).
  * ------------------------------------------------------------------------- */
 
 typedef enum { LA_INDEX_INT64 = 0, LA_INDEX_INT32 = 1 } la_index_type;
